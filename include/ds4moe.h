@@ -58,7 +58,7 @@ typedef enum {
   DS4MOE_ERR_HOSTMEM = 8      /* host expert weights are not pinned (device-visible) host memory */
 } ds4moe_status;
 
-typedef enum { DS4MOE_F32 = 0, DS4MOE_BF16 = 1 } ds4moe_dtype;
+typedef enum { DS4MOE_F32 = 0, DS4MOE_BF16 = 1, DS4MOE_MX4 = 2 /* 4-bit microscaled: ds4moe_mx4_matmul */ } ds4moe_dtype;
 
 typedef enum { DS4MOE_MODE_ROUTE = 0, DS4MOE_MODE_DECODE = 1, DS4MOE_MODE_PREFILL = 2 } ds4moe_mode;
 
@@ -388,6 +388,149 @@ int ds4moe_cache_stats(const ds4moe_dims *dims, int32_t n_slots, const void *cac
 
 int ds4moe_forward_decode_noalloc(const ds4moe_dims *dims, const ds4moe_weights *w, const void *x, int32_t T,
                                   float *y, ds4moe_routing *route_out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * EXPERT GATE.  Selection of experts from router logits for the gates of
+ * other routed models: sigmoid or softmax scores beside sqrt(softplus), a
+ * bias that moves the selection but not the weights (it balances the load),
+ * groups of experts, weights as they come or renormalised, and a factor.
+ *
+ * Per token, with logits l and s_e = sqrt(softplus(l_e)), sigmoid(l_e) or
+ * softmax(l)_e (over all E experts):
+ *   c_e   = s_e + b_e, experts ranked by c; without a bias by l (the same
+ *           order, with no rounding in it)
+ *   with n_groups > 1, group g holds experts g*E/n_groups ..; its score is the
+ *           sum of its group_rank largest c (with group_rank 1 and no bias its
+ *           largest l), and only the top_groups best groups stay
+ *   top-k of the experts that stay, by c descending; ties go to the lower
+ *           expert, and to the lower group
+ *   w_j   = scale * s_j, or scale * s_j / sum_i s_i with renorm (also where
+ *           the scores themselves leave the fp32 range)
+ * Scores, sums and weights are fp32 whatever the logits' type.  A logit of
+ * -inf or NaN, or a bias of -inf or NaN, masks its expert: it ranks after
+ * every other one, adds nothing to its group (a group with no other expert
+ * ranks last), and where fewer than k experts are left it still fills the
+ * ranks, so that every index is valid and distinct, with weight 0.  A logit of
+ * +inf counts as the largest finite fp32 number. */
+typedef enum { DS4MOE_SCORE_SQRT_SOFTPLUS = 0, DS4MOE_SCORE_SIGMOID = 1, DS4MOE_SCORE_SOFTMAX = 2 } ds4moe_score;
+
+/* Gate (host struct).
+ *   n_experts    E: 1..512
+ *   top_k        k: 1..16, at most top_groups * E / n_groups
+ *   n_groups     1..64, a divisor of E (1 = no groups)
+ *   top_groups   1..n_groups
+ *   group_rank   1 or 2
+ *   score        ds4moe_score
+ *   renorm       0 or 1
+ *   logits_dtype DS4MOE_F32 or DS4MOE_BF16
+ *   scale        finite */
+typedef struct {
+  int32_t n_experts;
+  int32_t top_k;
+  int32_t n_groups;
+  int32_t top_groups;
+  int32_t group_rank;
+  int32_t score;
+  int32_t renorm;
+  int32_t logits_dtype;
+  float scale;
+} ds4moe_gating;
+
+/* Workspace bytes of ds4moe_gate for T tokens (0 <= T <= 2^20); never
+ * decreases with T up to a given number of experts and choices.  0 for NULL or
+ * invalid arguments. */
+size_t ds4moe_gate_workspace_bytes(const ds4moe_gating *g, int32_t T);
+
+/* Gate T >= 0 tokens (0 = no-op, which leaves every output as it is).  logits: rows of E values, ld
+ * elements apart (ld >= E), aligned to their type; bias: [E] fp32 or NULL.  out (host struct):
+ * topk_idx, topk_w, counts, offsets and perm as in ds4moe_route, each may be
+ * NULL; counts, offsets and perm are either all set or all NULL.  out->logits
+ * must be NULL (DS4MOE_ERR_UNSUPPORTED).  ws: ds4moe_gate_workspace_bytes. */
+int ds4moe_gate(const ds4moe_gating *g, const void *logits, int64_t ld, const float *bias, int32_t T,
+                ds4moe_routing *out, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of the gate's weights: d_logits[t,e] = sum_j d_topk_w[t,j] *
+ * d w[t,j] / d l[t,e], with the choice of experts held.  logits, ld and bias
+ * as the gate had them (the bias only says which experts are masked: it has no
+ * gradient), topk_idx [T,k] the gate's choice (an index outside 0..E-1 takes
+ * no part), d_topk_w [T,k] fp32.  d_logits: rows of E values of logits_dtype,
+ * ldd elements apart, every one of which is written; computed in fp32 and
+ * rounded once.  It must not overlap the logits.  No workspace. */
+int ds4moe_gate_backward(const ds4moe_gating *g, const void *logits, int64_t ld, const float *bias,
+                         const int32_t *topk_idx, const float *d_topk_w, int32_t T, void *d_logits, int64_t ldd,
+                         void *stream);
+
+/* ------------------------------------------------------------------------
+ * 4-BIT MICROSCALED VALUES (the pages' native MXFP4 experts: DwarfStar
+ * architecture article, model catalogue).  Blocks of 32 values along a row:
+ * E2M1 codes (sign, then 0, .5, 1, 1.5, 2, 3, 4, 6), two a byte, the even one
+ * in the low nibble, and one E8M0 scale byte X per block, 2^(X-127), 255 =
+ * NaN.  A matrix [rows, cols] is codes [rows, 16*nb] and scales [rows, nb]
+ * bytes with nb = ceil(cols/32), row by row without gaps, as checkpoints hold
+ * them; a last block that is not full is filled with zeros.
+ *
+ * Quantise: X - 127 = floor(log2 max|v|) - 2 clamped to -127.., each v 2^(127-X)
+ * rounded to the nearest value of the grid, ties to the even code, and held
+ * to +-6.  A block of zeros gets X = 0; a block with a NaN or an infinity gets
+ * X = 255 and codes 0.  src: rows of cols values of src_dtype, ld elements
+ * apart (ld >= cols), aligned to their type; codes 16-byte aligned. rows and
+ * cols >= 0 (0 = no-op), cols below 2^31. */
+int ds4moe_mx4_quantize(uint8_t *codes, uint8_t *scales, const void *src, int32_t src_dtype, int64_t rows,
+                        int64_t cols, int64_t ld, void *stream);
+
+/* The values codes and scales stand for, in fp32 or bf16 (exact, but for a
+ * scale of 2^126 and up, where fp32 ends, and bf16 values below 2^-133). */
+int ds4moe_mx4_dequantize(void *dst, int32_t dst_dtype, int64_t ld, const uint8_t *codes, const uint8_t *scales,
+                          int64_t rows, int64_t cols, void *stream);
+
+/* y[M,N] = a[M,K] w[N,K]^T with 4-bit microscaled w, fp32 accumulation, one
+ * rounding to y_dtype.  a_dtype DS4MOE_BF16: rows of K values, lda elements
+ * apart (a multiple of 8, >= K), a_scales NULL.  a_dtype DS4MOE_MX4: codes
+ * [M,K/2] and a_scales [M,K/32], lda = K.  K: a multiple of 32 (a quantised
+ * matrix of other lengths is filled up to one), 32..2^24; M, N: 0..2^24 (0 =
+ * no-op).  y: rows of N values, ldy elements apart, aligned to 16 bytes with
+ * ldy free.  a, w 16-byte aligned.  y must not overlap the operands. */
+int ds4moe_mx4_matmul(void *y, int32_t y_dtype, int64_t ldy, const void *a, const uint8_t *a_scales, int32_t a_dtype,
+                      int64_t lda, const uint8_t *w, const uint8_t *w_scales, int64_t M, int64_t N, int64_t K,
+                      void *stream);
+
+/* Routed experts with 4-bit microscaled weights (host structs).
+ *   hidden, inter  multiples of 32, 32..65536
+ *   n_experts      1..512;  top_k 1..16, at most n_experts
+ *   y_dtype        DS4MOE_F32 or DS4MOE_BF16
+ * gate, up: codes [E, inter, hidden/2] and scales [E, inter, hidden/32];
+ * down: codes [E, hidden, inter/2] and scales [E, hidden, inter/32]. */
+typedef struct {
+  int32_t hidden;
+  int32_t inter;
+  int32_t n_experts;
+  int32_t top_k;
+  int32_t y_dtype;
+} ds4moe_mx4_dims;
+
+typedef struct {
+  const uint8_t *gate;
+  const uint8_t *gate_scales;
+  const uint8_t *up;
+  const uint8_t *up_scales;
+  const uint8_t *down;
+  const uint8_t *down_scales;
+} ds4moe_mx4_weights;
+
+/* Workspace bytes of ds4moe_mx4_experts for T tokens (0 <= T <= 2^20); never
+ * decreases with T.  0 for NULL or invalid arguments. */
+size_t ds4moe_mx4_workspace_bytes(const ds4moe_mx4_dims *dims, int32_t T);
+
+/* y[t] = sum_j topk_w[t,j] Wd_e (silu(Wg_e x_t) * (Wu_e x_t)), e =
+ * topk_idx[t,j], summed in the order of the ranks.  x: bf16 rows of hidden
+ * values, ldx elements apart (a multiple of 8); routing (host struct):
+ * topk_idx, topk_w, counts, offsets and perm, all set, as ds4moe_gate or
+ * ds4moe_route leave them (logits is not read).  y [T,hidden] of y_dtype.
+ * Products have exact bf16 operands and fp32 sums; the SwiGLU intermediate is
+ * rounded to bf16 for a bf16 y, and held to 24 bits for an fp32 y.  An index
+ * outside 0..E-1 adds nothing to its token. */
+int ds4moe_mx4_experts(const ds4moe_mx4_dims *dims, const ds4moe_mx4_weights *w, const void *x, int64_t ldx, int32_t T,
+                       const ds4moe_routing *routing, void *y, void *ws, size_t ws_bytes, void *stream);
 
 /* Static description of a status code (never NULL). */
 const char *ds4moe_status_str(int status);

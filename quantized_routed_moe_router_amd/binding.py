@@ -27,6 +27,8 @@ DS4MOE_ERR_HOSTMEM = 8
 DS4MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 DS4MOE_F32 = 0
 DS4MOE_BF16 = 1
+DS4MOE_MX4 = 2
+SCORE_SQRT_SOFTPLUS, SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1, 2
 MODE_ROUTE, MODE_DECODE, MODE_PREFILL = 0, 1, 2
 
 EXPORTED = ("ds4moe_packed_bytes", "ds4moe_packed_bytes_bits", "ds4moe_pack_q2k", "ds4moe_pack",
@@ -35,7 +37,9 @@ EXPORTED = ("ds4moe_packed_bytes", "ds4moe_packed_bytes_bits", "ds4moe_pack_q2k"
             "ds4moe_version", "ds4moe_forward_timed", "ds4moe_cache_bytes", "ds4moe_cache_reset",
             "ds4moe_forward_decode_cached", "ds4moe_forward_prefill_cached", "ds4moe_cache_stats",
             "ds4moe_forward_decode_noalloc",
-            "ds4moe_read_probe")
+            "ds4moe_read_probe",
+            "ds4moe_gate_workspace_bytes", "ds4moe_gate", "ds4moe_gate_backward", "ds4moe_mx4_quantize",
+            "ds4moe_mx4_dequantize", "ds4moe_mx4_matmul", "ds4moe_mx4_workspace_bytes", "ds4moe_mx4_experts")
 N_TIMED_KERNELS = 11
 KERNEL_SLOTS = ("router", "route", "permute", "gateup", "down", "shared_gateup", "shared_down", "combine",
                 "cache_plan", "cache_fill", "shared_convert")
@@ -54,6 +58,22 @@ class Weights(ctypes.Structure):
 
 class Routing(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("topk_idx", "topk_w", "counts", "offsets", "perm", "logits")]
+
+
+class Gating(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_rank", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("logits_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Mx4Dims(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("y_dtype", ctypes.c_int32)]
+
+
+class Mx4Weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("gate", "gate_scales", "up", "up_scales", "down", "down_scales")]
 
 
 class Ds4MoeError(RuntimeError):
@@ -97,6 +117,16 @@ def lib() -> ctypes.CDLL:
         L.ds4moe_cache_stats.argtypes = [P, I32, P, ctypes.c_size_t, P, P]
         L.ds4moe_forward_decode_noalloc.argtypes = [P, P, P, I32, P, P, P]
         L.ds4moe_read_probe.argtypes = [P, ctypes.c_size_t, I32, P, P, P, P]
+        L.ds4moe_gate_workspace_bytes.argtypes = [P, I32]
+        L.ds4moe_gate_workspace_bytes.restype = ctypes.c_size_t
+        L.ds4moe_gate.argtypes = [P, P, I64, P, I32, P, P, ctypes.c_size_t, P]
+        L.ds4moe_gate_backward.argtypes = [P, P, I64, P, P, P, I32, P, I64, P]
+        L.ds4moe_mx4_quantize.argtypes = [P, P, P, I32, I64, I64, I64, P]
+        L.ds4moe_mx4_dequantize.argtypes = [P, I32, I64, P, P, I64, I64, P]
+        L.ds4moe_mx4_matmul.argtypes = [P, I32, I64, P, P, I32, I64, P, P, I64, I64, I64, P]
+        L.ds4moe_mx4_workspace_bytes.argtypes = [P, I32]
+        L.ds4moe_mx4_workspace_bytes.restype = ctypes.c_size_t
+        L.ds4moe_mx4_experts.argtypes = [P, P, P, I64, I32, P, P, P, ctypes.c_size_t, P]
         L.ds4moe_status_str.argtypes = [ctypes.c_int]
         L.ds4moe_status_str.restype = ctypes.c_char_p
         L.ds4moe_version.restype = ctypes.c_int
@@ -104,7 +134,8 @@ def lib() -> ctypes.CDLL:
                    "ds4moe_cache_reset", "ds4moe_forward_decode_cached", "ds4moe_forward_prefill_cached",
                    "ds4moe_cache_stats",
                    "ds4moe_forward_decode", "ds4moe_forward_decode_noalloc", "ds4moe_read_probe",
-                   "ds4moe_forward_prefill", "ds4moe_forward_timed"):
+                   "ds4moe_forward_prefill", "ds4moe_forward_timed", "ds4moe_gate", "ds4moe_gate_backward",
+                   "ds4moe_mx4_quantize", "ds4moe_mx4_dequantize", "ds4moe_mx4_matmul", "ds4moe_mx4_experts"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -146,6 +177,19 @@ def make_weights(router_w, gate, up, down, router_bias=None, sh_gate=None, sh_up
 
 def make_routing(topk_idx=None, topk_w=None, counts=None, offsets=None, perm=None, logits=None) -> Routing:
     return Routing(*(_ptr(t) for t in (topk_idx, topk_w, counts, offsets, perm, logits)))
+
+
+def make_gating(E, k, n_groups=1, top_groups=1, group_rank=1, score=SCORE_SQRT_SOFTPLUS, renorm=True,
+                logits_dtype=DS4MOE_F32, scale=1.0) -> Gating:
+    return Gating(E, k, n_groups, top_groups, group_rank, score, int(renorm), logits_dtype, scale)
+
+
+def make_mx4_dims(H, I, E, k, y_dtype=DS4MOE_BF16) -> Mx4Dims:
+    return Mx4Dims(H, I, E, k, y_dtype)
+
+
+def make_mx4_weights(gate, gate_scales, up, up_scales, down, down_scales) -> Mx4Weights:
+    return Mx4Weights(*(_ptr(t) for t in (gate, gate_scales, up, up_scales, down, down_scales)))
 
 
 # ---------------------------------------------------------------- entry points
@@ -266,3 +310,44 @@ def ds4moe_read_probe(buf, nbytes: int, n_workgroups: int, sink, events=None, st
     ev = (None, None) if events is None else tuple(ctypes.c_void_p(e.cuda_event) for e in events)
     _check(lib().ds4moe_read_probe(_ptr(buf), nbytes, n_workgroups, _ptr(sink), ev[0], ev[1], _stream(stream)),
            "read_probe")
+
+
+def ds4moe_gate_workspace_bytes(gating: Gating, T: int) -> int:
+    return int(lib().ds4moe_gate_workspace_bytes(ctypes.byref(gating), T))
+
+
+def ds4moe_gate(gating: Gating, logits, ld: int, bias, T: int, routing: Routing, ws, ws_bytes: int, stream=None) -> None:
+    _check(lib().ds4moe_gate(ctypes.byref(gating), _ptr(logits), ld, _ptr(bias), T, ctypes.byref(routing), _ptr(ws),
+                             ws_bytes, _stream(stream)), "gate")
+
+
+def ds4moe_gate_backward(gating: Gating, logits, ld: int, bias, topk_idx, d_topk_w, T: int, d_logits, ldd: int,
+                         stream=None) -> None:
+    _check(lib().ds4moe_gate_backward(ctypes.byref(gating), _ptr(logits), ld, _ptr(bias), _ptr(topk_idx),
+                                      _ptr(d_topk_w), T, _ptr(d_logits), ldd, _stream(stream)), "gate_backward")
+
+
+def ds4moe_mx4_quantize(codes, scales, src, src_dtype: int, rows: int, cols: int, ld: int, stream=None) -> None:
+    _check(lib().ds4moe_mx4_quantize(_ptr(codes), _ptr(scales), _ptr(src), src_dtype, rows, cols, ld,
+                                     _stream(stream)), "mx4_quantize")
+
+
+def ds4moe_mx4_dequantize(dst, dst_dtype: int, ld: int, codes, scales, rows: int, cols: int, stream=None) -> None:
+    _check(lib().ds4moe_mx4_dequantize(_ptr(dst), dst_dtype, ld, _ptr(codes), _ptr(scales), rows, cols,
+                                       _stream(stream)), "mx4_dequantize")
+
+
+def ds4moe_mx4_matmul(y, y_dtype: int, ldy: int, a, a_scales, a_dtype: int, lda: int, w, w_scales, M: int, N: int,
+                      K: int, stream=None) -> None:
+    _check(lib().ds4moe_mx4_matmul(_ptr(y), y_dtype, ldy, _ptr(a), _ptr(a_scales), a_dtype, lda, _ptr(w),
+                                   _ptr(w_scales), M, N, K, _stream(stream)), "mx4_matmul")
+
+
+def ds4moe_mx4_workspace_bytes(dims: Mx4Dims, T: int) -> int:
+    return int(lib().ds4moe_mx4_workspace_bytes(ctypes.byref(dims), T))
+
+
+def ds4moe_mx4_experts(dims: Mx4Dims, weights: Mx4Weights, x, ldx: int, T: int, routing: Routing, y, ws, ws_bytes: int,
+                       stream=None) -> None:
+    _check(lib().ds4moe_mx4_experts(ctypes.byref(dims), ctypes.byref(weights), _ptr(x), ldx, T, ctypes.byref(routing),
+                                    _ptr(y), _ptr(ws), ws_bytes, _stream(stream)), "mx4_experts")

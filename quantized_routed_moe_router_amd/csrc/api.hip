@@ -11,7 +11,7 @@ using namespace ds4;
 
 namespace {
 
-constexpr int kVersion = 300;  // 0.3.0: ds4moe_forward_prefill_cached
+constexpr int kVersion = 400;  // 0.4.0: expert gate, 4-bit microscaled operators
 constexpr int kTileDecode = 16;
 constexpr int kTilePrefill = 64;      // tokens per prefill tile (64-token GEMM kernels)
 constexpr int kTilePrefillWide = 80;  // with the wide-tile GEMM kernels

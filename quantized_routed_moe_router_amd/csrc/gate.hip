@@ -1,0 +1,440 @@
+// Expert gate: scores, groups, top-k, weights and the stable permutation from
+// router logits, and the gradient of the weights.
+//
+// Mathematics, one token: s_e = sigmoid(l_e), softmax(l)_e or
+// sqrt(softplus(l_e)); experts are ranked by s_e + b_e (by l_e where there is
+// no bias: the same order without a rounding), groups of consecutive experts
+// by the sum of their one or two best keys; the weights of the k best experts
+// of the best groups are scale * s_j, divided by their sum where asked.
+#include "mx4.h"
+#include "route_dev.h"
+
+namespace ds4 {
+
+enum { SC_SQRT_SOFTPLUS = 0, SC_SIGMOID = 1, SC_SOFTMAX = 2 };
+
+namespace {
+
+constexpr int GATE_WAVES = 16;       // waves of a gate workgroup, one token each at a time
+constexpr int GATE_MAXE = 512;
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void *p, int64_t i) {
+  if (BF16) return bf16_bits_to_float(((const uint16_t *)p)[i]);
+  return ((const float *)p)[i];
+}
+
+// NaN -> -inf (a masked expert); +inf -> the largest finite value, so that no
+// difference or quotient of scores is a NaN
+__device__ __forceinline__ float clean_logit(float l) {
+  if (!(l >= -3.40282347e38f)) return -INFINITY;
+  return fminf(l, 3.40282347e38f);
+}
+
+// sigmoid or sqrt(softplus) of one finite logit (0 for a masked one)
+__device__ __forceinline__ float own_score(float l, int score) {
+  if (l == -INFINITY) return 0.0f;
+  if (score == SC_SIGMOID) return 1.0f / (1.0f + expf(-l));
+  return l < -17.0f ? expf(0.5f * l) : router_score(l);  // e^l alone is subnormal from -87 on, its root is not
+}
+
+// Scores of chosen logits up to one common factor, for their quotients by
+// their sum: where the largest is far below 0 every score is about e^l (its
+// root for the root form) and would end among the subnormals, so the factor
+// e^-max is taken out of them.
+__device__ __forceinline__ float relative_score(float l, int score, float max) {
+  const float m = max < -60.0f ? max : 0.0f;
+  if (score == SC_SIGMOID) return expf(fminf(l, 0.0f) - m) / (1.0f + expf(-fabsf(l)));
+  return m < 0.0f ? expf(0.5f * (l - m)) : router_score(l);
+}
+
+// order-preserving key of a float: every number >= 2, masked (-inf) 1
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (!(v > -INFINITY)) return 1u;
+  return logit_key(v);
+}
+
+// maximum over the wave, in every lane
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    const uint32_t u = (uint32_t)__shfl_xor((int)v, o);
+    v = v > u ? v : u;
+  }
+  return v;
+}
+__device__ __forceinline__ float wave_max_f(float v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+__device__ __forceinline__ float wave_sum_f(float v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// One token by one wave; lane l holds experts NK*l .. NK*l+NK-1.  Lane j < k
+// returns expert and weight of rank j.  xl, kl: wave-private LDS rows of NK*64
+// floats.
+template <int NK, bool BF16>
+__device__ __forceinline__ void gate_token(const GateArgs &a, int64_t t, float *xl, float *kl, int &my_e, float &my_w) {
+  const int lane = threadIdx.x & 63;
+  float x[NK];
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int e = NK * lane + i;
+    x[i] = e < a.E ? clean_logit(load_logit<BF16>(a.logits, t * a.ld + e)) : -INFINITY;
+    xl[e] = x[i];
+  }
+  // softmax over all experts: maximum and sum
+  float mx = 0.0f, zinv = 1.0f;
+  const bool soft = a.score == SC_SOFTMAX;
+  if (soft) {
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < NK; ++i) m = fmaxf(m, x[i]);
+    mx = wave_max_f(m);
+    float z = 0.0f;
+    if (mx == -INFINITY) mx = 0.0f;  // every expert masked
+#pragma unroll
+    for (int i = 0; i < NK; ++i) z += expf(x[i] - mx);
+    z = wave_sum_f(z);
+    zinv = z > 0.0f ? 1.0f / z : 0.0f;
+  }
+  // value of each expert that the groups are ranked by (-inf where masked);
+  // the experts are, too, where there is a bias, and by the logit otherwise
+  const bool need_scores = a.bias != nullptr || (a.G > 1 && a.group_rank > 1);
+  float v[NK];
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int e = NK * lane + i;
+    v[i] = x[i];
+    if (need_scores && x[i] != -INFINITY) {
+      v[i] = soft ? expf(x[i] - mx) * zinv : own_score(x[i], a.score);
+      if (a.bias && e < a.E) {
+        v[i] += a.bias[e];
+        if (v[i] != v[i]) v[i] = -INFINITY;
+      }
+    }
+  }
+  uint64_t stays = ~0ull;
+  int lanes_per = 64;
+  if (a.G > 1) {
+#pragma unroll
+    for (int i = 0; i < NK; ++i) kl[NK * lane + i] = v[i];
+    wave_lds_order();
+    // lanes_per lanes (a power of two) per group: the two best of the group
+    lanes_per = 64 >> (32 - __clz(a.G - 1));
+    const int g = lane / lanes_per, j = lane % lanes_per;
+    float m1 = -INFINITY, m2 = -INFINITY;
+    if (g < a.G)
+      for (int i = j; i < a.per; i += lanes_per) {
+        const float u = kl[g * a.per + i];
+        m2 = fmaxf(m2, fminf(m1, u));
+        m1 = fmaxf(m1, u);
+      }
+    for (int o = 1; o < lanes_per; o <<= 1) {
+      const float o1 = __shfl_xor(m1, o), o2 = __shfl_xor(m2, o);
+      m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+      m1 = fmaxf(m1, o1);
+    }
+    // a second best that is masked adds nothing; a group with none live is last
+    const float gs = (a.group_rank > 1 && m2 > -INFINITY) ? m1 + m2 : m1;
+    int rank = 0;
+    for (int h = 0; h < a.G; ++h) {
+      const float o = __shfl(gs, h * lanes_per);
+      rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
+    }
+    stays = __ballot(g < a.G && j == 0 && rank < a.top_groups);
+  }
+  uint32_t key[NK];
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int e = NK * lane + i;
+    key[i] = 0u;
+    if (e < a.E) {
+      const int g = a.G > 1 ? (int)(((uint32_t)e * a.per_inv) >> 20) : 0;
+      if (a.G <= 1 || ((stays >> (g * lanes_per)) & 1)) key[i] = order_key(a.bias ? v[i] : x[i]);
+    }
+  }
+  // k rounds of the wave's largest key, ties to the lowest lane and slot, that
+  // is to the lowest expert
+  my_e = 0;
+  uint32_t my_key = 0u;
+  for (int r = 0; r < a.k; ++r) {
+    uint32_t h = key[0];
+#pragma unroll
+    for (int i = 1; i < NK; ++i) h = h > key[i] ? h : key[i];
+    const uint32_t m = wave_max_u32(h);
+    const int win = __ffsll((unsigned long long)__ballot(h == m)) - 1;
+    int at = 0;
+#pragma unroll
+    for (int i = NK - 1; i >= 0; --i) at = key[i] == m ? i : at;
+    at = __shfl(at, win);
+    if (lane == win) {
+#pragma unroll
+      for (int i = 0; i < NK; ++i) key[i] = i == at ? 0u : key[i];
+    }
+    if (lane == r) {
+      my_e = NK * win + at;
+      my_key = m;
+    }
+  }
+  wave_lds_order();
+  float s = 0.0f;
+  const float l = lane < a.k ? xl[my_e] : -INFINITY;
+  const bool live = lane < a.k && my_key > 1u && l != -INFINITY;
+  if (a.renorm) mx = wave_max_f(live ? l : -INFINITY);  // sums of the chosen alone
+  if (live) {
+    if (soft) s = expf(l - mx) * (a.renorm ? 1.0f : zinv);
+    else s = a.renorm ? relative_score(l, a.score, mx) : own_score(l, a.score);
+  }
+  if (a.renorm) {
+    const float S = wave_sum_f(s);
+    s = S > 0.0f ? s / S : 0.0f;
+  }
+  my_w = a.scale * s;
+  wave_lds_order();
+}
+
+// exclusive prefix over `n` <= 512 ints in LDS by the first wave; total returned in every lane of it
+__device__ __forceinline__ int wave_scan_512(const int32_t *c, int32_t *off, int n) {
+  const int lane = threadIdx.x & 63;
+  int v[8], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = 8 * lane + i < n ? c[8 * lane + i] : 0;
+    sum += v[i];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(inc, o);
+    if (lane >= o) inc += u;
+  }
+  int run = inc - sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (8 * lane + i < n) off[8 * lane + i] = run;
+    run += v[i];
+  }
+  return __shfl(inc, 63);
+}
+
+// One workgroup per chunk of tokens, a wave per token; a chunk's tokens go in
+// blocks of 64 whose experts are marked in a 64-bit mask per expert, so the
+// rank of an assignment among its expert's (tokens ascending) is a popcount.
+template <int NK, bool BF16>
+__global__ __launch_bounds__(1024) void k_gate(GateArgs a) {
+  __shared__ float xl[GATE_WAVES][NK * 64], kl[GATE_WAVES][NK * 64];
+  __shared__ unsigned long long mask[GATE_MAXE];
+  __shared__ int32_t run[GATE_MAXE];
+  __shared__ int32_t bi[64 * 16];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int64_t c0 = (int64_t)blockIdx.x * a.chunk;
+  const int n = (int)(a.T - c0 < a.chunk ? a.T - c0 : a.chunk);
+  const bool perm = a.perm != nullptr;
+  for (int e = tid; e < a.E; e += 1024) run[e] = 0;
+  for (int b0 = 0; b0 < n; b0 += 64) {
+    const int nb = n - b0 < 64 ? n - b0 : 64;
+    for (int e = tid; e < a.E; e += 1024) mask[e] = 0ull;
+    __syncthreads();
+    for (int q = wave; q < nb; q += GATE_WAVES) {
+      const int64_t t = c0 + b0 + q;
+      int e;
+      float w;
+      gate_token<NK, BF16>(a, t, xl[wave], kl[wave], e, w);
+      if (lane < a.k) {
+        if (a.idx) a.idx[t * a.k + lane] = e;
+        if (a.w) a.w[t * a.k + lane] = w;
+        if (perm) {
+          bi[q * a.k + lane] = e;
+          atomicOr(&mask[e], 1ull << q);
+        }
+      }
+    }
+    __syncthreads();
+    if (!perm) continue;
+    for (int i = tid; i < nb * a.k; i += 1024) {
+      const int q = i / a.k, e = bi[i];
+      a.lrank[(c0 + b0) * a.k + i] = (uint16_t)(run[e] + __popcll(mask[e] & ((1ull << q) - 1)));
+    }
+    __syncthreads();
+    for (int e = tid; e < a.E; e += 1024) run[e] += __popcll(mask[e]);
+    __syncthreads();
+  }
+  if (!perm) return;
+  for (int e = tid; e < a.E; e += 1024) a.ccnt[(int64_t)blockIdx.x * a.E + e] = (uint16_t)run[e];
+}
+
+// One workgroup per chunk: every expert's count in the chunks before this one
+// and in all, the offsets, and the places of the chunk's assignments.
+__global__ __launch_bounds__(1024) void k_gate_place(GateArgs a) {
+  __shared__ int32_t before[GATE_MAXE], total[GATE_MAXE], off[GATE_MAXE];
+  const int tid = threadIdx.x;
+  for (int e = tid; e < a.E; e += 1024) {
+    before[e] = 0;
+    total[e] = 0;
+  }
+  __syncthreads();
+  const int b = blockIdx.x;
+  for (int i = tid; i < a.nchunk * a.E; i += 1024) {
+    const int c = i / a.E, e = i - c * a.E;
+    const int v = a.ccnt[i];
+    if (v) {
+      atomicAdd(&total[e], v);
+      if (c < b) atomicAdd(&before[e], v);
+    }
+  }
+  __syncthreads();
+  if (tid < 64) {
+    const int all = wave_scan_512(total, off, a.E);
+    if (b == 0 && tid == 0) a.offsets[a.E] = all;
+  }
+  __syncthreads();
+  if (b == 0)
+    for (int e = tid; e < a.E; e += 1024) {
+      a.counts[e] = total[e];
+      a.offsets[e] = off[e];
+    }
+  const int64_t c0 = (int64_t)b * a.chunk;
+  const int n = (int)(a.T - c0 < a.chunk ? a.T - c0 : a.chunk);
+  for (int i = tid; i < n * a.k; i += 1024) {
+    const int64_t as = c0 * a.k + i;
+    const int e = a.idx[as];
+    a.perm[off[e] + before[e] + a.lrank[as]] = (int32_t)as;
+  }
+}
+
+// ---------------------------------------------------------------- gradient
+// One wave per token.  With w_j = scale * s_j (or scale * s_j / S):
+//   d s_j = scale * dw_j                                  (weights as they come)
+//   d s_j = scale / S * (dw_j - sum_i dw_i s_i / S)       (renormalised)
+// and d l = ds * ds/dl; softmax without renormalisation reaches every logit:
+// d l_e = p_e (ds_e - sum_j ds_j p_j).  Softmax with it is a softmax over the
+// chosen logits alone.
+template <int NK, bool BF16>
+__global__ __launch_bounds__(256) void k_gate_backward(GateGradArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= a.T) return;
+  int e = -1;
+  float dw = 0.0f, l = -INFINITY;
+  if (lane < a.k) {
+    e = a.idx[t * a.k + lane];
+    dw = a.dw[t * a.k + lane] * a.scale;
+    if (e >= 0 && e < a.E && !(a.bias && !(a.bias[e] > -INFINITY)))
+      l = clean_logit(load_logit<BF16>(a.logits, t * a.ld + e));
+    else
+      e = -1;
+  }
+  const bool live = l != -INFINITY;
+  float g[NK];
+  const bool soft = a.score == SC_SOFTMAX, dense = soft && !a.renorm;
+  float mine = 0.0f;  // d l of the chosen logit
+  float p[NK];
+  if (dense) {
+    float x[NK], m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int q = lane + 64 * i;
+      x[i] = q < a.E ? clean_logit(load_logit<BF16>(a.logits, t * a.ld + q)) : -INFINITY;
+      m = fmaxf(m, x[i]);
+    }
+    m = wave_max_f(m);
+    if (m == -INFINITY) m = 0.0f;
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      p[i] = expf(x[i] - m);
+      z += p[i];
+    }
+    z = wave_sum_f(z);
+    const float zi = z > 0.0f ? 1.0f / z : 0.0f;
+    const float pj = live ? expf(l - m) * zi : 0.0f;
+    const float dot = wave_sum_f(live ? dw * pj : 0.0f);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) g[i] = -p[i] * zi * dot;
+    mine = live ? dw * pj : 0.0f;
+  } else {
+    // d s/d l * S/s: no quotient by a sum or a score that is small
+    float s = 0.0f, slope = 1.0f;
+    const float m = wave_max_f(l);
+    if (live) {
+      if (soft) s = expf(l - m);
+      else s = a.renorm ? relative_score(l, a.score, m) : own_score(l, a.score);
+      if (a.score == SC_SIGMOID) slope = 1.0f / (1.0f + expf(l));
+      if (a.score == SC_SQRT_SOFTPLUS && l < -17.0f) slope = 0.5f;  // sigmoid / (2 softplus) in the limit
+      else if (a.score == SC_SQRT_SOFTPLUS) slope = 0.5f / (s * s * (1.0f + expf(-l)));
+    }
+    float q = s;
+    const float ds = live ? dw : 0.0f;
+    float dot = 0.0f;
+    if (a.renorm) {
+      const float S = wave_sum_f(s);
+      q = S > 0.0f ? s / S : 0.0f;
+      dot = wave_sum_f(ds * q);
+    }
+    mine = live ? (ds - dot) * q * slope : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) g[i] = 0.0f;
+  }
+  for (int j = 0; j < a.k; ++j) {
+    const int ej = __shfl(e, j);
+    const float v = __shfl(mine, j);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) g[i] += lane + 64 * i == ej ? v : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int q = lane + 64 * i;
+    if (q < a.E) {
+      if (BF16) ((__bf16 *)a.dl)[t * a.ldd + q] = (__bf16)g[i];
+      else ((float *)a.dl)[t * a.ldd + q] = g[i];
+    }
+  }
+}
+
+}  // namespace
+
+int gate_chunk(int64_t T) {
+  if (T <= 64) return 64;
+  int c = 16;
+  while (c < 64 && (T + c - 1) / c > 256) c *= 2;
+  if ((T + c - 1) / c > 256) c = (int)(((T + 255) / 256 + 63) / 64 * 64);
+  return c;
+}
+
+int gate_chunks_max(int64_t T) { return T >= 4096 ? 256 : (int)((T + 15) / 16); }
+
+hipError_t launch_gate(const GateArgs &a, hipStream_t s) {
+  const dim3 g(a.nchunk), b(1024);
+  auto run = [&](auto f32, auto bf16) {
+    if (a.bf16) hipLaunchKernelGGL(bf16, g, b, 0, s, a);
+    else hipLaunchKernelGGL(f32, g, b, 0, s, a);
+  };
+  if (a.E <= 64) run(k_gate<1, false>, k_gate<1, true>);
+  else if (a.E <= 128) run(k_gate<2, false>, k_gate<2, true>);
+  else if (a.E <= 256) run(k_gate<4, false>, k_gate<4, true>);
+  else run(k_gate<8, false>, k_gate<8, true>);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.perm) return e;
+  hipLaunchKernelGGL(k_gate_place, g, b, 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_gate_backward(const GateGradArgs &a, hipStream_t s) {
+  const dim3 g((unsigned)(((int64_t)a.T + 3) / 4)), b(256);
+  auto run = [&](auto f32, auto bf16) {
+    if (a.bf16) hipLaunchKernelGGL(bf16, g, b, 0, s, a);
+    else hipLaunchKernelGGL(f32, g, b, 0, s, a);
+  };
+  if (a.E <= 64) run(k_gate_backward<1, false>, k_gate_backward<1, true>);
+  else if (a.E <= 128) run(k_gate_backward<2, false>, k_gate_backward<2, true>);
+  else if (a.E <= 256) run(k_gate_backward<4, false>, k_gate_backward<4, true>);
+  else run(k_gate_backward<8, false>, k_gate_backward<8, true>);
+  return hipGetLastError();
+}
+
+}  // namespace ds4

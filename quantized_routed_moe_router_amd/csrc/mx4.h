@@ -1,0 +1,82 @@
+// Launch wrappers of the expert gate and of the 4-bit microscaled operators
+// (internal to the library).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ds4 {
+
+// ---------------------------------------------------------------- gate
+struct GateArgs {
+  const void *logits;   // [T, ld] fp32 or bf16
+  int64_t ld;
+  const float *bias;    // [E] or null
+  int32_t T, E, k, G, top_groups, group_rank, per;  // per = E / G
+  uint32_t per_inv;     // ceil(2^20 / per): e / per = e * per_inv >> 20 for e < 512
+  int32_t score;        // ds4moe_score
+  bool renorm, bf16;
+  float scale;
+  int32_t *idx;         // [T,k]
+  float *w;             // [T,k]
+  int32_t *counts, *offsets, *perm;  // all set, or all null
+  uint16_t *ccnt;       // [nchunk][E] counts of a chunk (more than one chunk)
+  uint16_t *lrank;      // [T*k] an assignment's rank among its expert's in the chunk
+  int32_t chunk, nchunk;
+};
+
+struct GateGradArgs {
+  const void *logits;
+  int64_t ld;
+  const float *bias;    // [E] or null
+  const int32_t *idx;
+  const float *dw;
+  void *dl;
+  int64_t ldd;
+  int32_t T, E, k, score;
+  bool renorm, bf16;
+  float scale;
+};
+
+int gate_chunk(int64_t T);       // tokens per workgroup of the gate
+int gate_chunks_max(int64_t T);  // the most workgroups for T tokens or fewer
+hipError_t launch_gate(const GateArgs &a, hipStream_t s);
+hipError_t launch_gate_backward(const GateGradArgs &a, hipStream_t s);
+
+// ---------------------------------------------------------------- 4-bit microscaled values
+hipError_t launch_mx4_quantize(uint8_t *codes, uint8_t *scales, const void *src, bool bf16, int64_t rows, int64_t cols,
+                               int64_t ld, hipStream_t s);
+hipError_t launch_mx4_dequantize(void *dst, bool bf16, int64_t ld, const uint8_t *codes, const uint8_t *scales,
+                                 int64_t rows, int64_t cols, hipStream_t s);
+
+// y[M,N] = a[M,K] w[N,K]^T
+struct Mx4Product {
+  void *y;
+  int64_t ldy;
+  bool y_bf16;
+  const void *a;              // bf16 [M, lda], or codes [M, K/2]
+  const uint8_t *a_scales;    // codes' scales [M, K/32], null for bf16
+  int64_t lda;
+  const uint8_t *w, *ws;      // codes [N, K/2], scales [N, K/32]
+  int64_t M, N, K;
+};
+hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t s);
+
+// The routed SwiGLU experts.
+struct Mx4Experts {
+  const uint8_t *gate, *gate_s, *up, *up_s, *down, *down_s;  // [E,I,H/2], [E,I,H/32], down [E,H,I/2], [E,H,I/32]
+  const uint16_t *x;          // bf16 [T, ldx]
+  int64_t ldx;
+  int32_t T, H, I, E, k;
+  const int32_t *idx, *counts, *offsets, *perm;
+  const float *w;
+  void *y;                    // [T,H]
+  bool y_bf16;
+  uint16_t *h;                // [planes][T*k][I] bf16 by position of the permutation
+  float *ya;                  // [T*k][H] by assignment
+};
+// bf16 terms that the SwiGLU intermediate is held in
+inline int mx4_h_planes(bool y_bf16) { return y_bf16 ? 1 : 3; }
+hipError_t launch_mx4_experts(const Mx4Experts &p, hipStream_t s);
+
+}  // namespace ds4
