@@ -69,7 +69,7 @@ int validate_mx4(const ds4moe_mx4_dims *d) {
 }
 
 struct Mx4Layout {
-  size_t h, ya, total;
+  size_t h, ya, tiles, total;
 };
 
 Mx4Layout mx4_layout(const ds4moe_mx4_dims &d, int64_t T) {
@@ -83,6 +83,7 @@ Mx4Layout mx4_layout(const ds4moe_mx4_dims &d, int64_t T) {
   const size_t A = (size_t)T * d.top_k;
   L.h = take(2 * (size_t)mx4_h_planes(d.y_dtype == DS4MOE_BF16) * A * d.inter);
   L.ya = take(4 * A * d.hidden);
+  L.tiles = take(sizeof(Mx4Tiles) + sizeof(Mx4Tile) * (size_t)mx4_max_tiles((int64_t)A, d.n_experts));
   L.total = off;
   return L;
 }
@@ -273,6 +274,8 @@ int ds4moe_mx4_experts(const ds4moe_mx4_dims *dims, const ds4moe_mx4_weights *w,
   p.y_bf16 = d.y_dtype == DS4MOE_BF16;
   p.h = at<uint16_t>(ws, L.h);
   p.ya = at<float>(ws, L.ya);
+  p.tiles = at<Mx4Tiles>(ws, L.tiles);
+  p.max_tiles = (int32_t)mx4_max_tiles((int64_t)T * d.top_k, d.n_experts);
   return hip_status(launch_mx4_experts(p, (hipStream_t)stream));
 }
 

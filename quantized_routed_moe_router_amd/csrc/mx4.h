@@ -62,6 +62,15 @@ struct Mx4Product {
 };
 hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t s);
 
+// up to 96 tokens of one expert: positions p0 .. p0 + n - 1 of the permutation
+struct Mx4Tile {
+  int32_t e, p0, n, pad;
+};
+struct Mx4Tiles {
+  int32_t count, pad[3];
+  Mx4Tile tile[1];            // [count]
+};
+
 // The routed SwiGLU experts.
 struct Mx4Experts {
   const uint8_t *gate, *gate_s, *up, *up_s, *down, *down_s;  // [E,I,H/2], [E,I,H/32], down [E,H,I/2], [E,H,I/32]
@@ -74,7 +83,12 @@ struct Mx4Experts {
   bool y_bf16;
   uint16_t *h;                // [planes][T*k][I] bf16 by position of the permutation
   float *ya;                  // [T*k][H] by assignment
+  Mx4Tiles *tiles;
+  int32_t max_tiles;
 };
+int64_t mx4_max_tiles(int64_t assignments, int64_t experts);
+hipError_t launch_mx4_gemm_experts(const Mx4Experts &p, hipStream_t s);  // h and ya; more than a few tokens
+hipError_t launch_mx4_gemm(const Mx4Product &p, hipStream_t s);          // bf16 activations, many rows
 // bf16 terms that the SwiGLU intermediate is held in
 inline int mx4_h_planes(bool y_bf16) { return y_bf16 ? 1 : 3; }
 hipError_t launch_mx4_experts(const Mx4Experts &p, hipStream_t s);

@@ -5,48 +5,11 @@
 // in nibble k % 2 of byte k / 2, one scale byte per 32 codes; byte X stands
 // for 2^(X-127), 255 for NaN.  A lane that holds 16 bytes of codes holds one
 // block, so every lane of a matrix instruction has one scale.
-#include "mx4.h"
-#include "common.h"
+#include "mx4_dev.h"
 
 namespace ds4 {
 
-typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-typedef int i8v __attribute__((ext_vector_type(8)));
-
 namespace {
-
-__device__ __forceinline__ f4 mfma_bf16(bf8 a, bf8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-
-// 16x16x128 product of two 4-bit operands; each lane gives the scale byte of
-// its own block in bits 0-7 of sa and sb
-__device__ __forceinline__ f4 mfma_mx4(u4 a, u4 b, f4 c, uint32_t sa, uint32_t sb) {
-  const i8v A = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-  const i8v B = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
-// The scale as the conversion takes it: a float of which only the exponent
-// counts (exponent field 0 is 2^-127, 255 gives NaN).
-__device__ __forceinline__ float scale_float(uint32_t byte) { return __uint_as_float(byte << 23); }
-
-// 8 codes -> 8 bf16 times the scale: exact (two significant bits) as long as
-// the value is a normal bf16 or a multiple of 2^-133
-__device__ __forceinline__ bf8 codes_bf16(uint32_t c, float scale) {
-  const bf2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0);
-  const bf2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1);
-  const bf2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2);
-  const bf2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3);
-  return bf8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-}
-
-__device__ __forceinline__ bf8 zero_bf8() {
-  const u4 z = {0, 0, 0, 0};
-  return __builtin_bit_cast(bf8, z);
-}
-
-__device__ __forceinline__ u4 load16(const void *p) { return *reinterpret_cast<const u4 *>(p); }
 
 // ---------------------------------------------------------------- quantise, dequantise
 // n / d for n < 2^31 by a multiplication: m = ceil(2^(32+s) / d), 2^s >= d
@@ -277,8 +240,6 @@ __device__ __forceinline__ ExpertRange expert_of(const Mx4Experts &p, int a) {
   return r;
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
-
 template <int PL>
 __global__ __launch_bounds__(64 * SM_WAVES) void k_mx4_gateup_small(Mx4Experts p) {
   __shared__ f4 part[SM_WAVES * 64];
@@ -304,19 +265,8 @@ __global__ __launch_bounds__(64 * SM_WAVES) void k_mx4_gateup_small(Mx4Experts p
     join_waves(part, ag, wave, SM_WAVES);
     join_waves(part, au, wave, SM_WAVES);
     if (wave == 0 && t0 + r < er.n && n0 + 4 * g < p.I) {
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = silu_mul(ag[i], au[i]);
-#pragma unroll
-      for (int q = 0; q < PL; ++q) {
-        bf4 b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          b[i] = (__bf16)v[i];
-          v[i] = fabsf((float)b[i]) < INFINITY ? v[i] - (float)b[i] : 0.0f;
-        }
-        *reinterpret_cast<bf4 *>(p.h + ((int64_t)q * A + pos) * p.I + n0 + 4 * g) = b;
-      }
+      store_terms<PL>(p.h + (int64_t)pos * p.I + n0 + 4 * g, (int64_t)A * p.I, silu_mul(ag[0], au[0]),
+                      silu_mul(ag[1], au[1]), silu_mul(ag[2], au[2]), silu_mul(ag[3], au[3]));
     }
   }
 }
@@ -418,6 +368,7 @@ hipError_t launch_mx4_dequantize(void *dst, bool bf16, int64_t ld, const uint8_t
 }
 
 hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t s) {
+  if (!p.a_scales && p.M > 16) return launch_mx4_gemm(p, s);
   const int64_t mt = (p.M + 15) / 16;
   const dim3 g((unsigned)((p.N + 15) / 16), (unsigned)(mt < 65535 ? mt : 65535)), b(64 * SM_WAVES);
   if (p.a_scales && p.y_bf16) hipLaunchKernelGGL((k_mx4_small<true, true>), g, b, 0, s, p);
@@ -430,15 +381,18 @@ hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t s) {
 hipError_t launch_mx4_experts(const Mx4Experts &p, hipStream_t s) {
   const int A = p.T * p.k;
   const dim3 b(64 * SM_WAVES), gg(A, (p.I + 15) / 16), gd(A, (p.H + 15) / 16), gc(p.T, (p.H / 4 + 255) / 256);
-  if (p.y_bf16) {
+  if (p.T > 16) {
+    const hipError_t e = launch_mx4_gemm_experts(p, s);
+    if (e != hipSuccess) return e;
+  } else if (p.y_bf16) {
     hipLaunchKernelGGL((k_mx4_gateup_small<1>), gg, b, 0, s, p);
     hipLaunchKernelGGL((k_mx4_down_small<1>), gd, b, 0, s, p);
-    hipLaunchKernelGGL((k_mx4_combine<true>), gc, dim3(256), 0, s, p);
   } else {
     hipLaunchKernelGGL((k_mx4_gateup_small<3>), gg, b, 0, s, p);
     hipLaunchKernelGGL((k_mx4_down_small<3>), gd, b, 0, s, p);
-    hipLaunchKernelGGL((k_mx4_combine<false>), gc, dim3(256), 0, s, p);
   }
+  if (p.y_bf16) hipLaunchKernelGGL((k_mx4_combine<true>), gc, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((k_mx4_combine<false>), gc, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

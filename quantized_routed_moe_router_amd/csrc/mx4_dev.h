@@ -1,0 +1,79 @@
+// Device-side pieces shared by the 4-bit microscaled kernels.
+#pragma once
+#include "common.h"
+#include "mx4.h"
+
+namespace ds4 {
+
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef int i8v __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f4 mfma_bf16(bf8 a, bf8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+
+// 16x16x128 product of two 4-bit operands; each lane gives the scale byte of
+// its own block in bits 0-7 of sa and sb
+__device__ __forceinline__ f4 mfma_mx4(u4 a, u4 b, f4 c, uint32_t sa, uint32_t sb) {
+  const i8v A = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i8v B = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+// The scale as the conversion takes it: a float of which only the exponent
+// counts (exponent field 0 is 2^-127, 255 gives NaN).
+__device__ __forceinline__ float scale_float(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// 8 codes -> 8 bf16 times the scale: exact (two significant bits) as long as
+// the value is a normal bf16 or a multiple of 2^-133
+__device__ __forceinline__ bf8 codes_bf16(uint32_t c, float scale) {
+  const bf2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0);
+  const bf2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1);
+  const bf2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2);
+  const bf2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3);
+  return bf8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+__device__ __forceinline__ bf8 zero_bf8() {
+  const u4 z = {0, 0, 0, 0};
+  return __builtin_bit_cast(bf8, z);
+}
+
+__device__ __forceinline__ u4 load16(const void *p) { return *reinterpret_cast<const u4 *>(p); }
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// 4 adjacent values of the SwiGLU intermediate as PL bf16 terms, each the
+// rounding of what the ones before it leave (planes `plane` elements apart)
+template <int PL>
+__device__ __forceinline__ void store_terms(uint16_t *p, int64_t plane, float v0, float v1, float v2, float v3) {
+  float v[4] = {v0, v1, v2, v3};
+#pragma unroll
+  for (int q = 0; q < PL; ++q) {
+    bf4 b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      b[i] = (__bf16)v[i];
+      v[i] = fabsf((float)b[i]) < INFINITY ? v[i] - (float)b[i] : 0.0f;
+    }
+    *reinterpret_cast<bf4 *>(p + q * plane) = b;
+  }
+}
+
+// 16 bytes per lane from global memory into LDS without a register: lane l's
+// bytes land at lds + 16 l (lds wave-uniform; inactive lanes write nothing)
+__device__ __forceinline__ void load_lds16(const void *src, void *lds) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                   (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+}
+
+// a workgroup barrier that leaves loads in flight (__syncthreads waits for
+// all of them); LDS accesses before it are done
+__device__ __forceinline__ void barrier_keep_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+}  // namespace ds4

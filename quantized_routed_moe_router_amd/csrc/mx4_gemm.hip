@@ -1,0 +1,348 @@
+// Products of many rows of bf16 activations with 4-bit microscaled weights:
+// the routed experts' gate/up and down products and the dense product.
+//
+// A workgroup of four waves takes up to 96 activation rows (one expert's
+// tokens, or rows of a matrix) and 256 weight rows.  Each wave owns 64 weight
+// rows: their codes go from memory to its registers, 16 bytes (one block of
+// 32, one scale) per lane, and become exact bf16 operands there by one
+// conversion instruction per pair, so a weight is read and converted once per
+// workgroup.  The activations, which all four waves need, are staged in LDS
+// 128 columns at a time by loads that bypass the registers, double-buffered.
+// Lane (r, g) = (l % 16, l / 16) holds block g of a row's 128 columns; step j
+// of 4 multiplies columns 32 g + 8 j .. + 7 of both operands, so the four
+// steps cover the 128 in another order, the same for both.
+#include "mx4_dev.h"
+
+namespace ds4 {
+
+namespace {
+
+constexpr int GM_ROWS = 96;              // activation rows of a tile
+constexpr int GM_STAGE = GM_ROWS * 256;  // bytes of one stage: 128 bf16 columns
+constexpr int GM_WROWS = 256;            // weight rows of a workgroup
+
+// what a workgroup multiplies
+struct GemmTile {
+  const uint8_t *w[4], *s[4];  // codes and scales of the wave's four groups of 16 weight rows (wave-uniform)
+  uint32_t wo[4], so[4];       // this lane's row in them
+  int64_t K;
+  int nblk, nst;               // blocks of 32 and stages of 128 columns
+};
+
+struct Codes {
+  u4 c[4];
+  uint32_t s[4];
+};
+
+__device__ __forceinline__ void load_codes(const GemmTile &t, int st, Codes &c) {
+  const int g = (threadIdx.x >> 4) & 3;
+  const int blk = 4 * st + g;
+  if (4 * st + 4 <= t.nblk) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c.c[i] = load16(t.w[i] + (t.wo[i] + (uint32_t)blk * 16u));
+      c.s[i] = t.s[i][t.so[i] + (uint32_t)blk];
+    }
+  } else {  // the last stage of a length that is no multiple of 128: zeros past the end
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c.c[i] = u4{0, 0, 0, 0};
+      c.s[i] = 127;
+      if (blk < t.nblk) {
+        c.c[i] = load16(t.w[i] + (t.wo[i] + (uint32_t)blk * 16u));
+        c.s[i] = t.s[i][t.so[i] + (uint32_t)blk];
+      }
+    }
+  }
+}
+
+// Activation rows 16 q + 4 wave + lane/16 of the tile go to LDS row by row,
+// 256 bytes each, the 16-byte chunk c of row r at place c ^ (r % 16): the 16
+// rows that one operand read takes a chunk of then lie in 16 different places.
+template <int MT>
+__device__ __forceinline__ void load_rows(const uint8_t *const *rows, int64_t K, int st, char *lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int q = 0; q < MT; ++q) {
+    const int r = 16 * q + 4 * wave + (lane >> 4);
+    const int c = (lane & 15) ^ (r & 15);
+    const int64_t k = (int64_t)st * 128 + c * 8;
+    char *to = lds + (16 * q + 4 * wave) * 256;
+    if ((int64_t)st * 128 + 128 <= K || k < K) load_lds16(rows[q] + k * 2, to);
+    else *reinterpret_cast<u4 *>(to + lane * 16) = u4{0, 0, 0, 0};
+  }
+}
+
+// acc[i][m] += weight rows of group i times activation rows 16 m .. over the
+// K columns, `planes` times (the terms of the activations, plane bytes apart)
+template <int MT>
+__device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t *const *rows, int planes, int64_t plane,
+                                          char *lds, f4 (&acc)[4][MT]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[i][m] = f4{0, 0, 0, 0};
+  const int total = t.nst * planes;
+  const uint8_t *at[MT];
+#pragma unroll
+  for (int q = 0; q < MT; ++q) at[q] = rows[q];
+  Codes now, next;
+  load_rows<MT>(at, t.K, 0, lds);
+  load_codes(t, 0, now);
+  wait_vm<0>();
+  barrier_keep_loads();
+  int st = 0;
+  for (int s = 0; s < total; ++s) {
+    const char *x = lds + (s & 1) * GM_STAGE;
+    if (s + 1 < total) {
+      if (++st == t.nst) {
+        st = 0;
+#pragma unroll
+        for (int q = 0; q < MT; ++q) at[q] += plane;
+      }
+      load_rows<MT>(at, t.K, st, lds + ((s + 1) & 1) * GM_STAGE);
+      asm volatile("" ::: "memory");  // the wait below counts the loads issued after these
+      load_codes(t, st, next);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bf8 b[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        b[m] = *reinterpret_cast<const bf8 *>(x + (16 * m + r) * 256 + (((4 * g + j) ^ r) << 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf8 a = codes_bf16(now.c[i][j], scale_float(now.s[i]));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[i][m] = mfma_bf16(a, b[m], acc[i][m]);
+      }
+    }
+    // the next stage's rows have landed (its codes, issued after them, may be on their way)
+    if (s + 1 < total) wait_vm<8>();
+    barrier_keep_loads();
+    now = next;
+  }
+}
+
+// The workgroup's tile: each XCD takes a contiguous part of the tile list (its
+// neighbours are the same expert's, whose weights are then in that XCD's L2),
+// and all weight rows of a tile one after the other (its activations stay there).
+__device__ __forceinline__ bool tile_of(int id, int ntiles, int nrows, int &tile, int &nb) {
+  const int per = (ntiles + 7) / 8, x = id & 7, j = id >> 3;
+  tile = x * per + j / nrows;
+  nb = j % nrows;
+  return tile < ntiles && j / nrows < per;
+}
+
+__device__ __forceinline__ void weight_rows(GemmTile &t, int i, const uint8_t *w, const uint8_t *s, int64_t row0, int64_t N) {
+  const int r = threadIdx.x & 15;
+  if (row0 >= N) row0 = 0;  // a group past the end: read, never stored
+  t.w[i] = w + row0 * (t.K / 2);
+  t.s[i] = s + row0 * (t.K / 32);
+  const uint32_t l = (uint32_t)(row0 + r < N ? r : N - 1 - row0);
+  t.wo[i] = l * (uint32_t)(t.K / 2);
+  t.so[i] = l * (uint32_t)(t.K / 32);
+}
+
+template <int MT, int PL>
+__device__ __forceinline__ void gateup_tile(const Mx4Experts &p, const Mx4Tile &tl, int nb, char *lds) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int A = p.T * p.k;
+  GemmTile t;
+  t.K = p.H;
+  t.nblk = p.H / 32;
+  t.nst = (t.nblk + 3) / 4;
+  const int n0 = nb * (GM_WROWS / 2) + wave * 32;
+  const int64_t eo = (int64_t)tl.e * p.I;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint8_t *w = (i < 2 ? p.gate : p.up) + eo * (p.H / 2), *s = (i < 2 ? p.gate_s : p.up_s) + eo * (p.H / 32);
+    weight_rows(t, i, w, s, n0 + 16 * (i & 1), p.I);
+  }
+  const uint8_t *rows[MT];
+#pragma unroll
+  for (int q = 0; q < MT; ++q) {
+    const int row = 16 * q + 4 * wave + (lane >> 4);
+    int a = p.perm[tl.p0 + (row < tl.n ? row : 0)];
+    a = a < 0 ? 0 : a >= A ? A - 1 : a;
+    rows[q] = (const uint8_t *)(p.x + (int64_t)(a / p.k) * p.ldx);
+  }
+  f4 acc[4][MT];
+  gemm_tile<MT>(t, rows, 1, 0, lds, acc);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = 16 * m + r;
+    if (row >= tl.n) continue;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = n0 + 16 * i + 4 * g;
+      if (n >= p.I) continue;
+      const f4 u = acc[i][m], v = acc[2 + i][m];
+      store_terms<PL>(p.h + (int64_t)(tl.p0 + row) * p.I + n, (int64_t)A * p.I, silu_mul(u[0], v[0]), silu_mul(u[1], v[1]),
+                      silu_mul(u[2], v[2]), silu_mul(u[3], v[3]));
+    }
+  }
+}
+
+template <int MT, int PL>
+__device__ __forceinline__ void down_tile(const Mx4Experts &p, const Mx4Tile &tl, int nb, char *lds) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int A = p.T * p.k;
+  GemmTile t;
+  t.K = p.I;
+  t.nblk = p.I / 32;
+  t.nst = (t.nblk + 3) / 4;
+  const int n0 = nb * GM_WROWS + wave * 64;
+  const int64_t eo = (int64_t)tl.e * p.H;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    weight_rows(t, i, p.down + eo * (p.I / 2), p.down_s + eo * (p.I / 32), n0 + 16 * i, p.H);
+  const uint8_t *rows[MT];
+#pragma unroll
+  for (int q = 0; q < MT; ++q) {
+    const int row = 16 * q + 4 * wave + (lane >> 4);
+    rows[q] = (const uint8_t *)(p.h + (int64_t)(tl.p0 + (row < tl.n ? row : 0)) * p.I);
+  }
+  f4 acc[4][MT];
+  gemm_tile<MT>(t, rows, PL, (int64_t)A * p.I * 2, lds, acc);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = 16 * m + r;
+    if (row >= tl.n) continue;
+    const int a = p.perm[tl.p0 + row];
+    if (a < 0 || a >= A) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = n0 + 16 * i + 4 * g;
+      if (n < p.H) *reinterpret_cast<f4 *>(p.ya + (int64_t)a * p.H + n) = acc[i][m];
+    }
+  }
+}
+
+// one instance per number of groups of 16 activation rows, so that a tile of
+// 70 tokens multiplies 80 rows and not 96
+#define BY_GROUPS(n, CALL)      \
+  switch (((n) + 15) / 16) {    \
+    case 1: CALL(1); break;     \
+    case 2: CALL(2); break;     \
+    case 3: CALL(3); break;     \
+    case 4: CALL(4); break;     \
+    case 5: CALL(5); break;     \
+    default: CALL(6); break;    \
+  }
+
+template <int PL, bool DOWN>
+__global__ __launch_bounds__(256, 2) void k_mx4_gemm_experts(Mx4Experts p, int nrows) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * GM_STAGE];
+  int ti, nb;
+  if (!tile_of(blockIdx.x, p.tiles->count, nrows, ti, nb)) return;
+  const Mx4Tile tl = p.tiles->tile[ti];
+#define CALL(MT) (DOWN ? down_tile<MT, PL>(p, tl, nb, lds) : gateup_tile<MT, PL>(p, tl, nb, lds))
+  BY_GROUPS(tl.n, CALL)
+#undef CALL
+}
+
+// The list of tiles, experts ascending: one workgroup, a thread per expert.
+__global__ __launch_bounds__(512) void k_mx4_plan(Mx4Experts p) {
+  __shared__ int32_t sum[512];
+  const int e = threadIdx.x, A = p.T * p.k;
+  int n = 0, p0 = 0;
+  if (e < p.E) {
+    p0 = p.offsets[e];
+    n = p.counts[e];
+    if (p0 < 0 || p0 > A) n = 0;
+    else if (n > A - p0) n = A - p0;
+    if (n < 0) n = 0;
+  }
+  const int nt = (n + GM_ROWS - 1) / GM_ROWS;
+  sum[e] = nt;
+  __syncthreads();
+  for (int o = 1; o < 512; o <<= 1) {
+    const int v = e >= o ? sum[e - o] : 0;
+    __syncthreads();
+    sum[e] += v;
+    __syncthreads();
+  }
+  if (e == 511) p.tiles->count = sum[511] < p.max_tiles ? sum[511] : p.max_tiles;
+  for (int i = 0; i < nt; ++i) {
+    const int at = sum[e] - nt + i;
+    if (at < p.max_tiles) p.tiles->tile[at] = Mx4Tile{e, p0 + i * GM_ROWS, n - i * GM_ROWS < GM_ROWS ? n - i * GM_ROWS : GM_ROWS, 0};
+  }
+}
+
+template <int MT, bool YBF>
+__device__ __forceinline__ void product_tile(const Mx4Product &p, int64_t m0, int64_t n, int nb, char *lds) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  GemmTile t;
+  t.K = p.K;
+  t.nblk = (int)(p.K / 32);
+  t.nst = (t.nblk + 3) / 4;
+  const int64_t n0 = (int64_t)nb * GM_WROWS + wave * 64;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) weight_rows(t, i, p.w, p.ws, n0 + 16 * i, p.N);
+  const uint8_t *rows[MT];
+#pragma unroll
+  for (int q = 0; q < MT; ++q) {
+    const int64_t row = 16 * q + 4 * wave + (lane >> 4);
+    rows[q] = (const uint8_t *)p.a + (m0 + (row < n ? row : 0)) * p.lda * 2;
+  }
+  f4 acc[4][MT];
+  gemm_tile<MT>(t, rows, 1, 0, lds, acc);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = 16 * m + r;
+    if (row >= n) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int64_t c = n0 + 16 * i + 4 * g + v;
+        if (c < p.N) {
+          if (YBF) ((__bf16 *)p.y)[(m0 + row) * p.ldy + c] = (__bf16)acc[i][m][v];
+          else ((float *)p.y)[(m0 + row) * p.ldy + c] = acc[i][m][v];
+        }
+      }
+  }
+}
+
+template <bool YBF>
+__global__ __launch_bounds__(256, 2) void k_mx4_gemm(Mx4Product p, int mtiles, int nrows) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * GM_STAGE];
+  int ti, nb;
+  if (!tile_of(blockIdx.x, mtiles, nrows, ti, nb)) return;
+  const int64_t m0 = (int64_t)ti * GM_ROWS, n = p.M - m0 < GM_ROWS ? p.M - m0 : GM_ROWS;
+#define CALL(MT) product_tile<MT, YBF>(p, m0, n, nb, lds)
+  BY_GROUPS((int)n, CALL)
+#undef CALL
+}
+
+inline unsigned tile_grid(int64_t ntiles, int64_t nrows) { return (unsigned)((ntiles + 7) / 8 * nrows * 8); }
+
+}  // namespace
+
+int64_t mx4_max_tiles(int64_t A, int64_t E) { return A / GM_ROWS + (A < E ? A : E); }
+
+hipError_t launch_mx4_gemm_experts(const Mx4Experts &p, hipStream_t s) {
+  const int nu = (p.I + GM_WROWS / 2 - 1) / (GM_WROWS / 2), nd = (p.H + GM_WROWS - 1) / GM_WROWS;
+  const dim3 b(256);
+  hipLaunchKernelGGL(k_mx4_plan, dim3(1), dim3(512), 0, s, p);
+  if (p.y_bf16) {
+    hipLaunchKernelGGL((k_mx4_gemm_experts<1, false>), dim3(tile_grid(p.max_tiles, nu)), b, 0, s, p, nu);
+    hipLaunchKernelGGL((k_mx4_gemm_experts<1, true>), dim3(tile_grid(p.max_tiles, nd)), b, 0, s, p, nd);
+  } else {
+    hipLaunchKernelGGL((k_mx4_gemm_experts<3, false>), dim3(tile_grid(p.max_tiles, nu)), b, 0, s, p, nu);
+    hipLaunchKernelGGL((k_mx4_gemm_experts<3, true>), dim3(tile_grid(p.max_tiles, nd)), b, 0, s, p, nd);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_gemm(const Mx4Product &p, hipStream_t s) {
+  const int64_t mt = (p.M + GM_ROWS - 1) / GM_ROWS, nr = (p.N + GM_WROWS - 1) / GM_WROWS;
+  const dim3 g(tile_grid(mt, nr)), b(256);
+  if (p.y_bf16) hipLaunchKernelGGL((k_mx4_gemm<true>), g, b, 0, s, p, (int)mt, (int)nr);
+  else hipLaunchKernelGGL((k_mx4_gemm<false>), g, b, 0, s, p, (int)mt, (int)nr);
+  return hipGetLastError();
+}
+
+}  // namespace ds4
