@@ -89,8 +89,14 @@ struct Mx4Experts {
 int64_t mx4_max_tiles(int64_t assignments, int64_t experts);
 hipError_t launch_mx4_gemm_experts(const Mx4Experts &p, hipStream_t s);  // h and ya; more than a few tokens
 hipError_t launch_mx4_gemm(const Mx4Product &p, hipStream_t s);          // bf16 activations, many rows
-// bf16 terms that the SwiGLU intermediate is held in
-inline int mx4_h_planes(bool y_bf16) { return y_bf16 ? 1 : 3; }
+hipError_t launch_mx4_gemm4(const Mx4Product &p, hipStream_t s);         // 4-bit activations, many rows
+constexpr int MX4_FEW = 16;  // tokens (and rows of a product) that the kernels for few rows take
+constexpr int MX4_ONE = 4;   // tokens whose down projection adds the experts up itself
+// bf16 terms that the SwiGLU intermediate is held in: 24 bits for an fp32
+// result; for a bf16 one 16 bits where the second term costs nothing
+inline int mx4_h_planes(bool y_bf16, int64_t T) { return !y_bf16 ? 3 : T <= MX4_FEW ? 2 : 1; }
+hipError_t launch_mx4_product_few(const Mx4Product &p, hipStream_t s);
+hipError_t launch_mx4_experts_few(const Mx4Experts &p, hipStream_t s);  // h, then ya, or y for up to MX4_ONE tokens
 hipError_t launch_mx4_experts(const Mx4Experts &p, hipStream_t s);
 
 }  // namespace ds4

@@ -135,168 +135,7 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize(void *dst, int64_t ld, c
     }
 }
 
-// ---------------------------------------------------------------- products with few rows of activations
-// A wave multiplies 16 weight rows with 16 activation rows over its share of
-// k; the waves of a workgroup take turns along k (128 at a time) and add up
-// through LDS.  Lane (r, g) = (l % 16, l / 16) holds block g of the 128
-// codes of weight row r, and for the bf16 steps j = 0..3 the activations
-// 32 g + 8 j .. + 7 of row r: the steps cover the 128 in another order, the
-// same for both operands.
-constexpr int SM_WAVES = 8;
-
-struct WRow {
-  const uint8_t *c, *s;  // codes and scales of this lane's weight row, null outside
-};
-
-// adds w[16 rows] x a[16 rows]^T over k-tiles kt = wave, wave + nw, ... of nk128; K a multiple of 32
-template <bool MX4A>
-__device__ __forceinline__ void small_dot(f4 &acc, const uint8_t *wc, const uint8_t *wsc, const uint8_t *ap,
-                                          const uint8_t *asc, int64_t K, int wave, int nw) {
-  const int g = (threadIdx.x >> 4) & 3;
-  const int nt = (int)((K + 127) / 128);
-  for (int kt = wave; kt < nt; kt += nw) {
-    const int64_t blk = (int64_t)kt * 4 + g;
-    const bool in = blk * 32 < K;
-    u4 w = {0, 0, 0, 0};
-    uint32_t sw = 127, sa = 127;
-    if (in && wc) {
-      w = load16(wc + blk * 16);
-      sw = wsc[blk];
-    }
-    if (MX4A) {
-      u4 a = {0, 0, 0, 0};
-      if (in && ap) {
-        a = load16(ap + blk * 16);
-        sa = asc[blk];
-      }
-      acc = mfma_mx4(w, a, acc, sw, sa);
-    } else {
-      const float sf = scale_float(sw);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf8 x = zero_bf8();
-        if (in && ap) x = __builtin_bit_cast(bf8, load16(ap + (blk * 32 + 8 * j) * 2));
-        acc = mfma_bf16(codes_bf16(w[j], sf), x, acc);
-      }
-    }
-  }
-}
-
-// adds the waves' partial tiles; the sum is left in wave 0's lanes
-__device__ __forceinline__ void join_waves(f4 *part, f4 &acc, int wave, int nw) {
-  const int lane = threadIdx.x & 63;
-  __syncthreads();
-  part[wave * 64 + lane] = acc;
-  __syncthreads();
-  if (wave == 0)
-    for (int i = 1; i < nw; ++i) acc += part[i * 64 + lane];
-}
-
-template <bool MX4A, bool YBF>
-__global__ __launch_bounds__(64 * SM_WAVES) void k_mx4_small(Mx4Product p) {
-  __shared__ f4 part[SM_WAVES * 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, n = n0 + r;
-  const uint8_t *wc = n < p.N ? p.w + n * (p.K / 2) : nullptr;
-  const uint8_t *wsc = p.ws + n * (p.K / 32);
-  for (int64_t m0 = (int64_t)blockIdx.y * 16; m0 < p.M; m0 += (int64_t)gridDim.y * 16) {
-    const int64_t m = m0 + r;
-    const uint8_t *ap = nullptr, *asc = nullptr;
-    if (m < p.M) {
-      ap = (const uint8_t *)p.a + (MX4A ? m * (p.K / 2) : m * p.lda * 2);
-      if (MX4A) asc = p.a_scales + m * (p.K / 32);
-    }
-    f4 acc = {0, 0, 0, 0};
-    small_dot<MX4A>(acc, wc, wsc, ap, asc, p.K, wave, SM_WAVES);
-    join_waves(part, acc, wave, SM_WAVES);
-    if (wave == 0 && m < p.M) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t nn = n0 + 4 * g + i;
-        if (nn < p.N) {
-          if (YBF) ((__bf16 *)p.y)[m * p.ldy + nn] = (__bf16)acc[i];
-          else ((float *)p.y)[m * p.ldy + nn] = acc[i];
-        }
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------------- routed experts, few tokens each
-// The assignment that opens an expert's range of the permutation stands for
-// the expert; the others have nothing to do.  All of the routing is held to
-// its ranges before it addresses anything.
-struct ExpertRange {
-  int e, p0, n;
-};
-__device__ __forceinline__ ExpertRange expert_of(const Mx4Experts &p, int a) {
-  const int A = p.T * p.k;
-  ExpertRange r{p.idx[a], 0, 0};
-  if (r.e < 0 || r.e >= p.E) return r;
-  r.p0 = p.offsets[r.e];
-  if (r.p0 < 0 || r.p0 >= A || p.perm[r.p0] != a) return r;
-  const int n = p.counts[r.e];
-  r.n = n < 0 ? 0 : n > A - r.p0 ? A - r.p0 : n;
-  return r;
-}
-
-template <int PL>
-__global__ __launch_bounds__(64 * SM_WAVES) void k_mx4_gateup_small(Mx4Experts p) {
-  __shared__ f4 part[SM_WAVES * 64];
-  const ExpertRange er = expert_of(p, blockIdx.x);
-  if (er.n == 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int A = p.T * p.k;
-  const int n0 = blockIdx.y * 16;
-  const int64_t row = (int64_t)er.e * p.I + n0 + r;
-  const bool in = n0 + r < p.I;
-  const uint8_t *gc = in ? p.gate + row * (p.H / 2) : nullptr, *uc = in ? p.up + row * (p.H / 2) : nullptr;
-  const uint8_t *gs = p.gate_s + row * (p.H / 32), *us = p.up_s + row * (p.H / 32);
-  for (int t0 = 0; t0 < er.n; t0 += 16) {
-    const int pos = er.p0 + t0 + r;
-    const uint8_t *xp = nullptr;
-    if (t0 + r < er.n) {
-      const int a = p.perm[pos];
-      if (a >= 0 && a < A) xp = (const uint8_t *)(p.x + (int64_t)(a / p.k) * p.ldx);
-    }
-    f4 ag = {0, 0, 0, 0}, au = {0, 0, 0, 0};
-    small_dot<false>(ag, gc, gs, xp, nullptr, p.H, wave, SM_WAVES);
-    small_dot<false>(au, uc, us, xp, nullptr, p.H, wave, SM_WAVES);
-    join_waves(part, ag, wave, SM_WAVES);
-    join_waves(part, au, wave, SM_WAVES);
-    if (wave == 0 && t0 + r < er.n && n0 + 4 * g < p.I) {
-      store_terms<PL>(p.h + (int64_t)pos * p.I + n0 + 4 * g, (int64_t)A * p.I, silu_mul(ag[0], au[0]),
-                      silu_mul(ag[1], au[1]), silu_mul(ag[2], au[2]), silu_mul(ag[3], au[3]));
-    }
-  }
-}
-
-template <int PL>
-__global__ __launch_bounds__(64 * SM_WAVES) void k_mx4_down_small(Mx4Experts p) {
-  __shared__ f4 part[SM_WAVES * 64];
-  const ExpertRange er = expert_of(p, blockIdx.x);
-  if (er.n == 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int A = p.T * p.k;
-  const int n0 = blockIdx.y * 16;
-  const int64_t row = (int64_t)er.e * p.H + n0 + r;
-  const uint8_t *wc = n0 + r < p.H ? p.down + row * (p.I / 2) : nullptr;
-  const uint8_t *wsc = p.down_s + row * (p.I / 32);
-  for (int t0 = 0; t0 < er.n; t0 += 16) {
-    const int pos = er.p0 + t0 + r;
-    f4 acc = {0, 0, 0, 0};
-    for (int q = 0; q < PL; ++q) {
-      const uint8_t *hp = t0 + r < er.n ? (const uint8_t *)(p.h + ((int64_t)q * A + pos) * p.I) : nullptr;
-      small_dot<false>(acc, wc, wsc, hp, nullptr, p.I, wave, SM_WAVES);
-    }
-    join_waves(part, acc, wave, SM_WAVES);
-    if (wave == 0 && t0 + r < er.n && n0 + 4 * g < p.H) {
-      const int a = p.perm[pos];
-      if (a >= 0 && a < A) *reinterpret_cast<f4 *>(p.ya + (int64_t)a * p.H + n0 + 4 * g) = acc;
-    }
-  }
-}
-
+// ---------------------------------------------------------------- routed experts: the sum
 // y[t] = sum_j w[t,j] ya[t*k+j], in the order of the ranks
 template <bool YBF>
 __global__ __launch_bounds__(256) void k_mx4_combine(Mx4Experts p) {
@@ -368,31 +207,16 @@ hipError_t launch_mx4_dequantize(void *dst, bool bf16, int64_t ld, const uint8_t
 }
 
 hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t s) {
-  if (!p.a_scales && p.M > 16) return launch_mx4_gemm(p, s);
-  const int64_t mt = (p.M + 15) / 16;
-  const dim3 g((unsigned)((p.N + 15) / 16), (unsigned)(mt < 65535 ? mt : 65535)), b(64 * SM_WAVES);
-  if (p.a_scales && p.y_bf16) hipLaunchKernelGGL((k_mx4_small<true, true>), g, b, 0, s, p);
-  else if (p.a_scales) hipLaunchKernelGGL((k_mx4_small<true, false>), g, b, 0, s, p);
-  else if (p.y_bf16) hipLaunchKernelGGL((k_mx4_small<false, true>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((k_mx4_small<false, false>), g, b, 0, s, p);
-  return hipGetLastError();
+  if (p.M <= MX4_FEW) return launch_mx4_product_few(p, s);
+  return p.a_scales ? launch_mx4_gemm4(p, s) : launch_mx4_gemm(p, s);
 }
 
 hipError_t launch_mx4_experts(const Mx4Experts &p, hipStream_t s) {
-  const int A = p.T * p.k;
-  const dim3 b(64 * SM_WAVES), gg(A, (p.I + 15) / 16), gd(A, (p.H + 15) / 16), gc(p.T, (p.H / 4 + 255) / 256);
-  if (p.T > 16) {
-    const hipError_t e = launch_mx4_gemm_experts(p, s);
-    if (e != hipSuccess) return e;
-  } else if (p.y_bf16) {
-    hipLaunchKernelGGL((k_mx4_gateup_small<1>), gg, b, 0, s, p);
-    hipLaunchKernelGGL((k_mx4_down_small<1>), gd, b, 0, s, p);
-  } else {
-    hipLaunchKernelGGL((k_mx4_gateup_small<3>), gg, b, 0, s, p);
-    hipLaunchKernelGGL((k_mx4_down_small<3>), gd, b, 0, s, p);
-  }
-  if (p.y_bf16) hipLaunchKernelGGL((k_mx4_combine<true>), gc, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((k_mx4_combine<false>), gc, dim3(256), 0, s, p);
+  const hipError_t e = p.T <= MX4_FEW ? launch_mx4_experts_few(p, s) : launch_mx4_gemm_experts(p, s);
+  if (e != hipSuccess || p.T <= MX4_ONE) return e;
+  const dim3 g(p.T, (p.H / 4 + 255) / 256), b(256);
+  if (p.y_bf16) hipLaunchKernelGGL((k_mx4_combine<true>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((k_mx4_combine<false>), g, b, 0, s, p);
   return hipGetLastError();
 }
 

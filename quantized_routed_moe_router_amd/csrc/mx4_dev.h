@@ -3,6 +3,8 @@
 #include "common.h"
 #include "mx4.h"
 
+#include <type_traits>
+
 namespace ds4 {
 
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
@@ -66,6 +68,29 @@ __device__ __forceinline__ void load_lds16(const void *src, void *lds) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
                                    (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
 }
+
+// four adjacent results of row m from column n on
+template <bool YBF>
+__device__ __forceinline__ void store_row4(const Mx4Product &p, int64_t m, int64_t n, f4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < p.N) {
+      if (YBF) ((__bf16 *)p.y)[m * p.ldy + n + i] = (__bf16)v[i];
+      else ((float *)p.y)[m * p.ldy + n + i] = v[i];
+    }
+}
+
+// The workgroup's tile and weight rows.  Consecutive workgroups go to
+// different XCDs, each of which takes a contiguous part of the work, all
+// weight rows of a tile one after the other: a tile's activations stay in that
+// XCD's L2, and neighbouring tiles (of one expert) share its weights there.
+__device__ __forceinline__ bool tile_of(int id, int ntiles, int nrows, int &tile, int &nb) {
+  const int all = ntiles * nrows, per = (all + 7) / 8, j = id >> 3, at = (id & 7) * per + j;
+  tile = at / nrows;
+  nb = at - tile * nrows;
+  return j < per && at < all;
+}
+inline unsigned tile_grid(int64_t ntiles, int64_t nrows) { return (unsigned)((ntiles * nrows + 7) / 8 * 8); }
 
 // a workgroup barrier that leaves loads in flight (__syncthreads waits for
 // all of them); LDS accesses before it are done

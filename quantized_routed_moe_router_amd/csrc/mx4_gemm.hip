@@ -125,16 +125,6 @@ __device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t *cons
   }
 }
 
-// The workgroup's tile: each XCD takes a contiguous part of the tile list (its
-// neighbours are the same expert's, whose weights are then in that XCD's L2),
-// and all weight rows of a tile one after the other (its activations stay there).
-__device__ __forceinline__ bool tile_of(int id, int ntiles, int nrows, int &tile, int &nb) {
-  const int per = (ntiles + 7) / 8, x = id & 7, j = id >> 3;
-  tile = x * per + j / nrows;
-  nb = j % nrows;
-  return tile < ntiles && j / nrows < per;
-}
-
 __device__ __forceinline__ void weight_rows(GemmTile &t, int i, const uint8_t *w, const uint8_t *s, int64_t row0, int64_t N) {
   const int r = threadIdx.x & 15;
   if (row0 >= N) row0 = 0;  // a group past the end: read, never stored
@@ -294,15 +284,7 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, int64_t m0, in
     const int row = 16 * m + r;
     if (row >= n) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int64_t c = n0 + 16 * i + 4 * g + v;
-        if (c < p.N) {
-          if (YBF) ((__bf16 *)p.y)[(m0 + row) * p.ldy + c] = (__bf16)acc[i][m][v];
-          else ((float *)p.y)[(m0 + row) * p.ldy + c] = acc[i][m][v];
-        }
-      }
+    for (int i = 0; i < 4; ++i) store_row4<YBF>(p, m0 + row, n0 + 16 * i + 4 * g, acc[i][m]);
   }
 }
 
@@ -316,8 +298,6 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm(Mx4Product p, int mtiles, i
   BY_GROUPS((int)n, CALL)
 #undef CALL
 }
-
-inline unsigned tile_grid(int64_t ntiles, int64_t nrows) { return (unsigned)((ntiles + 7) / 8 * nrows * 8); }
 
 }  // namespace
 

@@ -1,0 +1,376 @@
+// Products of a few rows of activations with 4-bit microscaled weights, and
+// the routed experts of up to 16 tokens: the weights' bytes are what counts.
+//
+// A wave holds up to KT k-tiles (128 columns of 16 weight rows, 16 bytes or
+// one block per lane) of NM groups of rows in registers, all of them asked
+// for before the first is used, so that a CU has 64 KB and more on the way.
+// The waves of a workgroup share k (or the experts of a token) and add up
+// through LDS in a fixed order.  The matrix instructions have 16 columns for
+// the tokens; four tokens at a time are staged in LDS and fill four of them.
+#include "mx4_dev.h"
+
+namespace ds4 {
+
+namespace {
+
+constexpr int SW = 8;          // waves of a workgroup
+constexpr int MAXA = 256;      // assignments of a small batch
+
+// This wave's LDS: the assignments of its expert.  The ballot of a match
+// gives every lane its place.
+struct Members {
+  uint8_t a[MAXA];
+};
+
+// The expert of assignment a0 and the assignments that have it, ascending;
+// n = 0 if a0 is not the first of them or its index is out of range.
+__device__ __forceinline__ int find_members(const int32_t *__restrict__ idx, int A, int a0, int E, Members &mb, int &e) {
+  const int lane = threadIdx.x & 63;
+  int v[MAXA / 64];
+#pragma unroll
+  for (int i = 0; i < MAXA / 64; ++i) v[i] = 64 * i + lane < A ? idx[64 * i + lane] : -1;
+  e = -1;
+#pragma unroll
+  for (int i = 0; i < MAXA / 64; ++i)
+    if (a0 >> 6 == i) e = __builtin_amdgcn_readlane(v[i], a0 & 63);
+  if (e < 0 || e >= E) return 0;
+  int n = 0;
+  bool first = true;
+#pragma unroll
+  for (int i = 0; i < MAXA / 64; ++i) {
+    const uint64_t m = __ballot(v[i] == e);
+    if (v[i] == e)
+      mb.a[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = (uint8_t)(64 * i + lane);
+    if (n == 0 && m && 64 * i + __ffsll((unsigned long long)m) - 1 != a0) first = false;
+    n += __popcll(m);
+  }
+  return first ? n : 0;
+}
+
+// NM groups of 16 weight rows with one lane offset; row r of the wave's lanes
+// past the matrix's end reads the last row
+template <int NM>
+struct Rows {
+  const uint8_t *w[NM], *s[NM];
+  uint32_t wo[NM], so[NM];
+};
+
+template <int NM>
+__device__ __forceinline__ void set_rows(Rows<NM> &R, int i, const uint8_t *w, const uint8_t *s, int64_t row0, int64_t N,
+                                         int64_t K) {
+  const int r = threadIdx.x & 15;
+  if (row0 >= N) row0 = 0;
+  R.w[i] = w + row0 * (K / 2);
+  R.s[i] = s + row0 * (K / 32);
+  const uint32_t l = (uint32_t)(row0 + r < N ? r : N - 1 - row0);
+  R.wo[i] = l * (uint32_t)(K / 2);
+  R.so[i] = l * (uint32_t)(K / 32);
+}
+
+// acc[i] += weight rows of group i times the n <= 16 activation rows over the
+// k-tiles kt0, kt0 + step, ...  row(m): row m of the activations, whose PL
+// terms lie `plane` bytes apart.  lds: PL * KT * 1024 bytes of this wave.
+template <int NM, int KT, int PL, typename F>
+__device__ __forceinline__ void small_dot(f4 (&acc)[NM], const Rows<NM> &R, int64_t K, int kt0, int step, int n, F row,
+                                          int64_t plane, char *lds) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int nblk = (int)(K / 32), nt = (nblk + 3) / 4;
+  for (int c = kt0; c < nt; c += step * KT) {
+    u4 w[NM][KT];
+    uint32_t sc[NM][KT];
+    for (int m0 = 0; m0 < n; m0 += 4) {
+      // piece l + 64 u of the stage: term, row, tile, 16-byte chunk
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // reads of the last stage are done
+#pragma unroll
+      for (int u = 0; u < PL * KT; ++u) {
+        const int id = lane + 64 * u, ch = id & 15, i = (id >> 4) % KT, m = (id >> 4) / KT % 4, q = (id >> 6) / KT;
+        const int64_t k = ((int64_t)c + (int64_t)step * i) * 128 + ch * 8;
+        if (m0 + m < n) {
+          char *to = lds + 1024 * u;
+          if (k < K) load_lds16(row(m0 + m) + q * plane + k * 2, to);
+          else *reinterpret_cast<u4 *>(to + 16 * lane) = u4{0, 0, 0, 0};
+        }
+      }
+      asm volatile("" ::: "memory");  // the wait below counts the loads issued after these
+      if (m0 == 0) {
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          const int blk = (c + step * t) * 4 + g, b = blk < nblk ? blk : nblk - 1;
+#pragma unroll
+          for (int i = 0; i < NM; ++i) {
+            w[i][t] = load16(R.w[i] + (R.wo[i] + (uint32_t)b * 16u));
+            sc[i][t] = R.s[i][R.so[i] + (uint32_t)b];
+          }
+        }
+        wait_vm<2 * NM * KT>();
+      } else {
+        wait_vm<0>();
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      asm volatile("" ::: "memory");
+      const bool mine = r >= m0 && r < m0 + 4 && r < n;
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        const bool out = (c + step * t) * 4 + g >= nblk;
+        if (c + step * t >= nt) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          bf8 x[PL];
+#pragma unroll
+          for (int q = 0; q < PL; ++q) {
+            x[q] = zero_bf8();
+            if (mine) x[q] = *reinterpret_cast<const bf8 *>(lds + (((q * 4 + (r & 3)) * KT + t) * 16 + 4 * g + j) * 16);
+          }
+#pragma unroll
+          for (int i = 0; i < NM; ++i) {
+            const bf8 a = codes_bf16(out ? 0 : w[i][t][j], scale_float(out ? 127 : sc[i][t]));
+#pragma unroll
+            for (int q = 0; q < PL; ++q) acc[i] = mfma_bf16(a, x[q], acc[i]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// acc += 16 weight rows times one activation row over all of k.  lds: PL * KT * 256 bytes of this wave.
+template <int KT, int PL>
+__device__ __forceinline__ void one_dot(f4 &acc, const Rows<1> &R, int64_t K, const uint8_t *x, int64_t plane, char *lds) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int nblk = (int)(K / 32), nt = (nblk + 3) / 4;
+  for (int c = 0; c < nt; c += KT) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+#pragma unroll
+    for (int u = 0; u < PL * KT / 4; ++u) {
+      const int id = lane + 64 * u, ch = id & 15, i = (id >> 4) % KT, q = (id >> 4) / KT;
+      const int64_t k = (int64_t)(c + i) * 128 + ch * 8;
+      char *to = lds + 1024 * u;
+      if (k < K) load_lds16(x + q * plane + k * 2, to);
+      else *reinterpret_cast<u4 *>(to + 16 * lane) = u4{0, 0, 0, 0};
+    }
+    asm volatile("" ::: "memory");  // the wait below counts the loads issued after these
+    u4 w[KT];
+    uint32_t sc[KT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int blk = (c + t) * 4 + g, b = blk < nblk ? blk : nblk - 1;
+      w[t] = load16(R.w[0] + (R.wo[0] + (uint32_t)b * 16u));
+      sc[t] = R.s[0][R.so[0] + (uint32_t)b];
+    }
+    wait_vm<2 * KT>();
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const bool out = (c + t) * 4 + g >= nblk;
+      if (c + t >= nt) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bf8 a = codes_bf16(out ? 0 : w[t][j], scale_float(out ? 127 : sc[t]));
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+          bf8 x8 = zero_bf8();
+          if (r == 0) x8 = *reinterpret_cast<const bf8 *>(lds + ((q * KT + t) * 16 + 4 * g + j) * 16);
+          acc = mfma_bf16(a, x8, acc);
+        }
+      }
+    }
+  }
+}
+
+// the workgroup's sum of acc, wave by wave, in wave 0
+template <int NM>
+__device__ __forceinline__ void join_waves(f4 *part, f4 (&acc)[NM]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __syncthreads();
+  if (wave)
+#pragma unroll
+    for (int i = 0; i < NM; ++i) part[((wave - 1) * NM + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  if (wave == 0)
+#pragma unroll
+    for (int q = 0; q < SW - 1; ++q)
+#pragma unroll
+      for (int i = 0; i < NM; ++i) acc[i] += part[(q * NM + i) * 64 + lane];
+}
+
+// ---------------------------------------------------------------- experts of up to 16 tokens
+// h rows are the assignments here, so no permutation is needed: every wave
+// finds its expert's tokens in the list of choices.
+template <int PL>
+__global__ __launch_bounds__(64 * SW) void k_mx4_gateup_few(Mx4Experts p) {
+  constexpr int KT = 4;
+  __shared__ __attribute__((aligned(16))) char lds[SW * KT * 1024];
+  __shared__ Members mb[SW];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int A = p.T * p.k;
+  int e;
+  const int n = find_members(p.idx, A, blockIdx.y, p.E, mb[wave], e);
+  if (n == 0) return;
+  const int n0 = blockIdx.x * 16;
+  Rows<2> R;
+  set_rows(R, 0, p.gate + (int64_t)e * p.I * (p.H / 2), p.gate_s + (int64_t)e * p.I * (p.H / 32), n0, p.I, p.H);
+  set_rows(R, 1, p.up + (int64_t)e * p.I * (p.H / 2), p.up_s + (int64_t)e * p.I * (p.H / 32), n0, p.I, p.H);
+  for (int m0 = 0; m0 < n; m0 += 16) {
+    f4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    small_dot<2, KT, 1>(acc, R, p.H, wave, SW, n - m0 < 16 ? n - m0 : 16,
+                        [&](int m) { return (const uint8_t *)(p.x + (int64_t)(mb[wave].a[m0 + m] / p.k) * p.ldx); }, 0,
+                        lds + wave * KT * 1024);
+    join_waves<2>(reinterpret_cast<f4 *>(lds), acc);
+    if (wave == 0 && m0 + r < n)
+      store_terms<PL>(p.h + (int64_t)mb[0].a[m0 + r] * p.I + n0 + 4 * g, (int64_t)A * p.I, silu_mul(acc[0][0], acc[1][0]),
+                      silu_mul(acc[0][1], acc[1][1]), silu_mul(acc[0][2], acc[1][2]), silu_mul(acc[0][3], acc[1][3]));
+    __syncthreads();
+  }
+}
+
+template <int PL>
+__global__ __launch_bounds__(64 * SW) void k_mx4_down_few(Mx4Experts p) {
+  constexpr int KT = 2, NM = 4;
+  __shared__ __attribute__((aligned(16))) char lds[SW * (NM * 1024 > PL * KT * 1024 ? NM * 1024 : PL * KT * 1024)];
+  __shared__ Members mb[SW];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int A = p.T * p.k;
+  int e;
+  const int n = find_members(p.idx, A, blockIdx.y, p.E, mb[wave], e);
+  if (n == 0) return;
+  const int n0 = blockIdx.x * 16 * NM;
+  Rows<NM> R;
+#pragma unroll
+  for (int i = 0; i < NM; ++i)
+    set_rows(R, i, p.down + (int64_t)e * p.H * (p.I / 2), p.down_s + (int64_t)e * p.H * (p.I / 32), n0 + 16 * i, p.H, p.I);
+  for (int m0 = 0; m0 < n; m0 += 16) {
+    f4 acc[NM];
+#pragma unroll
+    for (int i = 0; i < NM; ++i) acc[i] = f4{0, 0, 0, 0};
+    small_dot<NM, KT, PL>(acc, R, p.I, wave, SW, n - m0 < 16 ? n - m0 : 16,
+                          [&](int m) { return (const uint8_t *)(p.h + (int64_t)mb[wave].a[m0 + m] * p.I); },
+                          (int64_t)A * p.I * 2, lds + wave * PL * KT * 1024);
+    join_waves<NM>(reinterpret_cast<f4 *>(lds), acc);
+    if (wave == 0 && m0 + r < n)
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        const int c = n0 + 16 * i + 4 * g;
+        if (c < p.H) *reinterpret_cast<f4 *>(p.ya + (int64_t)mb[0].a[m0 + r] * p.H + c) = acc[i];
+      }
+    __syncthreads();
+  }
+}
+
+// Down projection and weighted sum of one token: each wave takes experts of
+// the token, whole rows of k, and the first wave adds them up in the order of
+// the ranks.
+template <int PL, bool YBF>
+__global__ __launch_bounds__(64 * SW) void k_mx4_down_one(Mx4Experts p) {
+  constexpr int KT = 8;
+  __shared__ __attribute__((aligned(16))) char lds[SW * PL * KT * 256];
+  __shared__ f4 part[16][4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int t = blockIdx.y, n0 = blockIdx.x * 16, A = p.T * p.k;
+  for (int j = wave; j < p.k; j += SW) {
+    const int a = t * p.k + j, e = p.idx[a];
+    f4 acc[1] = {{0, 0, 0, 0}};
+    if (e >= 0 && e < p.E) {
+      Rows<1> R;
+      set_rows(R, 0, p.down + (int64_t)e * p.H * (p.I / 2), p.down_s + (int64_t)e * p.H * (p.I / 32), n0, p.H, p.I);
+      one_dot<KT, PL>(acc[0], R, p.I, (const uint8_t *)(p.h + (int64_t)a * p.I), (int64_t)A * p.I * 2,
+                      lds + wave * PL * KT * 256);
+      const float w = p.w[a];
+      acc[0] *= w;
+    }
+    if (r == 0) part[j][g] = acc[0];
+  }
+  __syncthreads();
+  if (threadIdx.x < 4) {
+    f4 y = {0, 0, 0, 0};
+    for (int j = 0; j < p.k; ++j) y += part[j][threadIdx.x];
+    const int64_t at = (int64_t)t * p.H + n0 + 4 * threadIdx.x;
+    if (YBF) *reinterpret_cast<bf4 *>((__bf16 *)p.y + at) = bf4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+    else *reinterpret_cast<f4 *>((float *)p.y + at) = y;
+  }
+}
+
+// ---------------------------------------------------------------- product of up to 16 rows
+template <bool YBF>
+__global__ __launch_bounds__(64 * SW) void k_mx4_product_few(Mx4Product p) {
+  constexpr int KT = 4;
+  __shared__ __attribute__((aligned(16))) char lds[SW * KT * 1024];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  Rows<1> R;
+  set_rows(R, 0, p.w, p.ws, n0, p.N, p.K);
+  f4 acc[1] = {{0, 0, 0, 0}};
+  small_dot<1, KT, 1>(acc, R, p.K, wave, SW, (int)p.M, [&](int m) { return (const uint8_t *)p.a + m * p.lda * 2; }, 0,
+                      lds + wave * KT * 1024);
+  join_waves<1>(reinterpret_cast<f4 *>(lds), acc);
+  if (wave == 0 && r < p.M) store_row4<YBF>(p, r, n0 + 4 * g, acc[0]);
+}
+
+// both operands in 4 bits: one scaled matrix instruction per k-tile
+template <bool YBF>
+__global__ __launch_bounds__(64 * SW) void k_mx4_product_few4(Mx4Product p) {
+  constexpr int KT = 4;
+  __shared__ f4 part[(SW - 1) * 64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int nblk = (int)(p.K / 32), nt = (nblk + 3) / 4;
+  Rows<2> R;
+  set_rows(R, 0, p.w, p.ws, n0, p.N, p.K);
+  set_rows(R, 1, (const uint8_t *)p.a, p.a_scales, 0, p.M, p.K);
+  f4 acc[1] = {{0, 0, 0, 0}};
+  for (int c = wave; c < nt; c += SW * KT) {
+    u4 w[2][KT];
+    uint32_t sc[2][KT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int blk = (c + SW * t) * 4 + g, b = blk < nblk ? blk : nblk - 1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i][t] = load16(R.w[i] + (R.wo[i] + (uint32_t)b * 16u));
+        sc[i][t] = R.s[i][R.so[i] + (uint32_t)b];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const bool out = (c + SW * t) * 4 + g >= nblk;
+      if (c + SW * t >= nt) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (out) {
+          w[i][t] = u4{0, 0, 0, 0};
+          sc[i][t] = 127;
+        }
+      acc[0] = mfma_mx4(w[0][t], w[1][t], acc[0], sc[0][t], sc[1][t]);
+    }
+  }
+  join_waves<1>(part, acc);
+  if (wave == 0 && r < p.M) store_row4<YBF>(p, r, n0 + 4 * g, acc[0]);
+}
+
+}  // namespace
+
+hipError_t launch_mx4_product_few(const Mx4Product &p, hipStream_t s) {
+  const dim3 g((unsigned)((p.N + 15) / 16)), b(64 * SW);
+  if (p.a_scales && p.y_bf16) hipLaunchKernelGGL(k_mx4_product_few4<true>, g, b, 0, s, p);
+  else if (p.a_scales) hipLaunchKernelGGL(k_mx4_product_few4<false>, g, b, 0, s, p);
+  else if (p.y_bf16) hipLaunchKernelGGL(k_mx4_product_few<true>, g, b, 0, s, p);
+  else hipLaunchKernelGGL(k_mx4_product_few<false>, g, b, 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_experts_few(const Mx4Experts &p, hipStream_t s) {
+  const int A = p.T * p.k;
+  const dim3 b(64 * SW), gg((p.I + 15) / 16, A), gd((p.H + 63) / 64, A), go((p.H + 15) / 16, p.T);
+  if (p.y_bf16) hipLaunchKernelGGL(k_mx4_gateup_few<2>, gg, b, 0, s, p);
+  else hipLaunchKernelGGL(k_mx4_gateup_few<3>, gg, b, 0, s, p);
+  if (p.T <= MX4_ONE) {
+    if (p.y_bf16) hipLaunchKernelGGL((k_mx4_down_one<2, true>), go, b, 0, s, p);
+    else hipLaunchKernelGGL((k_mx4_down_one<3, false>), go, b, 0, s, p);
+  } else {
+    if (p.y_bf16) hipLaunchKernelGGL(k_mx4_down_few<2>, gd, b, 0, s, p);
+    else hipLaunchKernelGGL(k_mx4_down_few<3>, gd, b, 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace ds4
