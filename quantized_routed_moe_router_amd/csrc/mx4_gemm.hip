@@ -87,24 +87,25 @@ __device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t *cons
   const uint8_t *at[MT];
 #pragma unroll
   for (int q = 0; q < MT; ++q) at[q] = rows[q];
-  Codes now, next;
+  Codes c0, c1;
   load_rows<MT>(at, t.K, 0, lds);
-  load_codes(t, 0, now);
+  load_codes(t, 0, c0);
   wait_vm<0>();
   barrier_keep_loads();
-  int st = 0;
-  for (int s = 0; s < total; ++s) {
+  int st = 0, s = 0;
+  // one stage: the next one's loads, this one's products.  Past the end the
+  // last stage is loaded again: with no condition on the loads the products
+  // wait for their own codes alone.
+  auto stage = [&](const Codes &now, Codes &next) {
     const char *x = lds + (s & 1) * GM_STAGE;
-    if (s + 1 < total) {
-      if (++st == t.nst) {
-        st = 0;
+    if (++s < total && ++st == t.nst) {
+      st = 0;
 #pragma unroll
-        for (int q = 0; q < MT; ++q) at[q] += plane;
-      }
-      load_rows<MT>(at, t.K, st, lds + ((s + 1) & 1) * GM_STAGE);
-      asm volatile("" ::: "memory");  // the wait below counts the loads issued after these
-      load_codes(t, st, next);
+      for (int q = 0; q < MT; ++q) at[q] += plane;
     }
+    load_rows<MT>(at, t.K, st, lds + (s & 1) * GM_STAGE);
+    asm volatile("" ::: "memory");  // the wait below counts the loads issued after these
+    load_codes(t, st, next);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       bf8 b[MT];
@@ -119,10 +120,15 @@ __device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t *cons
       }
     }
     // the next stage's rows have landed (its codes, issued after them, may be on their way)
-    if (s + 1 < total) wait_vm<8>();
+    wait_vm<8>();
     barrier_keep_loads();
-    now = next;
+  };
+  while (s + 1 < total) {
+    stage(c0, c1);
+    stage(c1, c0);
   }
+  if (s < total) stage(c0, c1);
+  wait_vm<0>();  // the last loads into LDS, before it is released
 }
 
 __device__ __forceinline__ void weight_rows(GemmTile &t, int i, const uint8_t *w, const uint8_t *s, int64_t row0, int64_t N) {

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int SW = 8;          // waves of a workgroup
 constexpr int MAXA = 256;      // assignments of a small batch
+constexpr int FEW_TILES = 8;   // 128-column tiles and terms of a wave that its LDS holds (8 KB)
 
 // This wave's LDS: the assignments of its expert.  The ballot of a match
 // gives every lane its place.
@@ -134,7 +135,8 @@ __device__ __forceinline__ void small_dot(f4 (&acc)[NM], const Rows<NM> &R, int6
 }
 
 // acc += 16 weight rows times one activation row over all of k.  lds: PL * KT * 256 bytes of this wave.
-template <int KT, int PL>
+// WIDE: K a multiple of 512, the scales of 4 tiles are loaded at once.
+template <int KT, int PL, bool WIDE>
 __device__ __forceinline__ void one_dot(f4 &acc, const Rows<1> &R, int64_t K, const uint8_t *x, int64_t plane, char *lds) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int nblk = (int)(K / 32), nt = (nblk + 3) / 4;
@@ -150,23 +152,31 @@ __device__ __forceinline__ void one_dot(f4 &acc, const Rows<1> &R, int64_t K, co
     }
     asm volatile("" ::: "memory");  // the wait below counts the loads issued after these
     u4 w[KT];
-    uint32_t sc[KT];
+    uint32_t sc[KT / 4][4];
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       const int blk = (c + t) * 4 + g, b = blk < nblk ? blk : nblk - 1;
       w[t] = load16(R.w[0] + (R.wo[0] + (uint32_t)b * 16u));
-      sc[t] = R.s[0][R.so[0] + (uint32_t)b];
+      if (!WIDE) sc[t / 4][t % 4] = R.s[0][R.so[0] + (uint32_t)b];
     }
-    wait_vm<2 * KT>();
+    if (WIDE)
+#pragma unroll
+      for (int t = 0; t < KT; t += 4) {
+        const int b = (c + t) * 4;
+        __builtin_memcpy(sc[t / 4], R.s[0] + (R.so[0] + (uint32_t)(b < nblk ? b : 0)), 16);
+      }
+    wait_vm<KT + (WIDE ? KT / 4 : KT)>();
     __builtin_amdgcn_s_waitcnt(0xC07F);
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-      const bool out = (c + t) * 4 + g >= nblk;
       if (c + t >= nt) continue;
+      const bool out = !WIDE && (c + t) * 4 + g >= nblk;
+      const uint32_t sb = sc[t / 4][t % 4];
+      const float sf = WIDE ? scale_float((sb >> (8 * g)) & 255u) : scale_float(out ? 127 : sb);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bf8 a = codes_bf16(out ? 0 : w[t][j], scale_float(out ? 127 : sc[t]));
+        const bf8 a = codes_bf16(out ? 0 : w[t][j], sf);
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
           bf8 x8 = zero_bf8();
@@ -194,66 +204,245 @@ __device__ __forceinline__ void join_waves(f4 *part, f4 (&acc)[NM]) {
       for (int i = 0; i < NM; ++i) acc[i] += part[(q * NM + i) * 64 + lane];
 }
 
+// Streaming form for up to 4 activation rows: they are staged once, and the
+// weights of nrt row tiles of NM groups go by, each step's loads on their way
+// while the step before is multiplied.  A step is KT adjacent tiles of k,
+// whole lines of memory.  With SPL = SW the waves share k, their steps
+// alternate, and each stages its own part; with SPL = 1 every wave has row
+// tiles of its own over all of k, and nothing to wait for.  Where a row's
+// scales allow it (WIDE: their number a multiple of 4 KT) a lane loads those
+// of a step at once and picks its block's.  xs: PL * 4 rows of nti * 256
+// bytes of LDS, this wave's or (SPL = 1) the workgroup's.
+template <int KT, int SPL>
+inline __host__ __device__ int few_tiles(int64_t K) {  // staged tiles, whole steps
+  return (int)((K / 32 + 4 * SPL * KT - 1) / (4 * SPL * KT)) * KT;
+}
+
+template <int KT, int PL, int SPL, typename F>
+__device__ __forceinline__ void stage_rows(int64_t K, int wave, int n, F row, int64_t plane, char *xs) {
+  const int lane = threadIdx.x & 63, nti = few_tiles<KT, SPL>(K);
+  for (int u = SPL == 1 ? wave : 0; u < PL * nti; u += SPL == 1 ? SW : 1) {
+    const int id = lane + 64 * u, ch = id & 15, i = (id >> 4) % nti, m = (id >> 4) / nti % 4, q = (id >> 6) / nti;
+    const int64_t k = (int64_t)(SPL == 1 ? i : KT * (wave + SW * (i / KT)) + i % KT) * 128 + ch * 8;
+    char *to = xs + 1024 * u;
+    if (m < n) {
+      if (k < K) load_lds16(row(m) + q * plane + k * 2, to);
+      else *reinterpret_cast<u4 *>(to + 16 * lane) = u4{0, 0, 0, 0};
+    }
+  }
+  asm volatile("" ::: "memory");  // the waits count the loads issued after these
+}
+
+template <int NM, int KT, bool WIDE>
+struct Ahead {
+  u4 w[NM][KT];
+  uint32_t s[NM][KT];  // WIDE: the scales of tile t, one byte per block; else this lane's
+};
+
+// scale bytes [b, b + 4 KT) of a row
+template <int KT>
+__device__ __forceinline__ void load_scales(const uint8_t *p, uint32_t (&s)[KT]) {
+  static_assert(KT == 2 || KT % 4 == 0, "whole loads");
+#pragma unroll
+  for (int t = 0; t < KT; t += 4) __builtin_memcpy(s + t, p + 4 * t, KT == 2 ? 8 : 16);
+}
+
+template <int NM, int KT, int PL, int SPL, bool WIDE, typename B, typename D>
+__device__ __forceinline__ void stream_rows(int64_t K, int wave, int nrt, int n, const char *xs, B base, D done) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int nblk = (int)(K / 32), nt = (nblk + 3) / 4, nti = few_tiles<KT, SPL>(K), nch = nti / KT, steps = nrt * nch;
+  const uint32_t wo = (uint32_t)r * (uint32_t)(K / 2), so = (uint32_t)r * (uint32_t)(K / 32);
+  int rl = 0, cl = 0;  // row tile and step of the next loads
+  auto load = [&](Ahead<NM, KT, WIDE> &a) {
+    const int t0 = SPL == 1 ? KT * cl : KT * (wave + SW * cl);
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      const uint8_t *w, *s;
+      base(i, rl, w, s);
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        const int blk = (t0 + t) * 4 + g, b = blk < nblk ? blk : nblk - 1;
+        a.w[i][t] = load16(w + (wo + (uint32_t)b * 16u));
+        if (!WIDE) a.s[i][t] = s[so + (uint32_t)b];
+      }
+      if (WIDE) load_scales<KT>(s + (so + (uint32_t)(t0 * 4 < nblk ? t0 * 4 : 0)), a.s[i]);
+    }
+    if (++cl == nch) {
+      cl = 0;
+      ++rl;
+    }
+  };
+  f4 acc[NM];
+  int rt = 0, c = 0;
+  auto step = [&](const Ahead<NM, KT, WIDE> &a) {
+    if (c == 0)
+#pragma unroll
+      for (int i = 0; i < NM; ++i) acc[i] = f4{0, 0, 0, 0};
+    const int t0 = SPL == 1 ? KT * c : KT * (wave + SW * c);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      if (t0 + t >= nt) continue;
+      const bool out = !WIDE && (t0 + t) * 4 + g >= nblk;
+      float sf[NM];
+#pragma unroll
+      for (int i = 0; i < NM; ++i) sf[i] = WIDE ? scale_float((a.s[i][t] >> (8 * g)) & 255u) : scale_float(out ? 127 : a.s[i][t]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bf8 x[PL];
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+          x[q] = zero_bf8();
+          if (r < n) x[q] = *reinterpret_cast<const bf8 *>(xs + ((q * 4 + r) * nti + c * KT + t) * 256 + (4 * g + j) * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+          const bf8 w = codes_bf16(out ? 0 : a.w[i][t][j], sf[i]);
+#pragma unroll
+          for (int q = 0; q < PL; ++q) acc[i] = mfma_bf16(w, x[q], acc[i]);
+        }
+      }
+    }
+    if (++c == nch) {
+      c = 0;
+      done(rt++, acc);
+    }
+  };
+  Ahead<NM, KT, WIDE> a0, a1;
+  load(a0);
+  wait_vm<NM * KT + (WIDE ? NM * ((KT + 3) / 4) : NM * KT)>();  // the activations are there
+  if (SPL == 1) barrier_keep_loads();
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  asm volatile("" ::: "memory");
+  // no load in the loop hangs on a condition: a step then waits for its own
+  // loads alone, and not for the next step's
+  int q = 0;
+  for (; q + 2 < steps; q += 2) {
+    load(a1);
+    step(a0);
+    load(a0);
+    step(a1);
+  }
+  if (q + 2 == steps) {
+    load(a1);
+    step(a0);
+    step(a1);
+  } else {
+    step(a0);
+  }
+}
+
+// the waves' sums of a row tile to one of them (each in its turn), which then
+// has it in acc; part: two buffers of SW * NM * 64 values
+template <int NM>
+__device__ __forceinline__ bool join_tile(f4 *part, int rt, int wave, f4 (&acc)[NM]) {
+  const int lane = threadIdx.x & 63;
+  f4 *const b = part + (rt & 1) * SW * NM * 64;
+#pragma unroll
+  for (int i = 0; i < NM; ++i) b[(wave * NM + i) * 64 + lane] = acc[i];
+  barrier_keep_loads();
+  if (wave != (rt & (SW - 1))) return false;
+#pragma unroll
+  for (int i = 0; i < NM; ++i) acc[i] = b[i * 64 + lane];
+#pragma unroll
+  for (int q = 1; q < SW; ++q)
+#pragma unroll
+    for (int i = 0; i < NM; ++i) acc[i] += b[(q * NM + i) * 64 + lane];
+  return true;
+}
+
 // ---------------------------------------------------------------- experts of up to 16 tokens
 // h rows are the assignments here, so no permutation is needed: every wave
 // finds its expert's tokens in the list of choices.
 template <int PL>
-__global__ __launch_bounds__(64 * SW) void k_mx4_gateup_few(Mx4Experts p) {
+__global__ __launch_bounds__(64 * SW) void k_mx4_gateup_few(Mx4Experts p, int nrt) {
   constexpr int KT = 4;
-  __shared__ __attribute__((aligned(16))) char lds[SW * KT * 1024];
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  __shared__ f4 part[2 * SW * 2 * 64];
   __shared__ Members mb[SW];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
   const int A = p.T * p.k;
   int e;
   const int n = find_members(p.idx, A, blockIdx.y, p.E, mb[wave], e);
   if (n == 0) return;
-  const int n0 = blockIdx.x * 16;
-  Rows<2> R;
-  set_rows(R, 0, p.gate + (int64_t)e * p.I * (p.H / 2), p.gate_s + (int64_t)e * p.I * (p.H / 32), n0, p.I, p.H);
-  set_rows(R, 1, p.up + (int64_t)e * p.I * (p.H / 2), p.up_s + (int64_t)e * p.I * (p.H / 32), n0, p.I, p.H);
-  for (int m0 = 0; m0 < n; m0 += 16) {
-    f4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    small_dot<2, KT, 1>(acc, R, p.H, wave, SW, n - m0 < 16 ? n - m0 : 16,
-                        [&](int m) { return (const uint8_t *)(p.x + (int64_t)(mb[wave].a[m0 + m] / p.k) * p.ldx); }, 0,
-                        lds + wave * KT * 1024);
-    join_waves<2>(reinterpret_cast<f4 *>(lds), acc);
-    if (wave == 0 && m0 + r < n)
-      store_terms<PL>(p.h + (int64_t)mb[0].a[m0 + r] * p.I + n0 + 4 * g, (int64_t)A * p.I, silu_mul(acc[0][0], acc[1][0]),
-                      silu_mul(acc[0][1], acc[1][1]), silu_mul(acc[0][2], acc[1][2]), silu_mul(acc[0][3], acc[1][3]));
-    __syncthreads();
+  const int n0 = blockIdx.x * 16 * nrt, rts = min(nrt, (p.I - n0 + 15) / 16);
+  const uint8_t *const ew[2] = {p.gate + (int64_t)e * p.I * (p.H / 2), p.up + (int64_t)e * p.I * (p.H / 2)};
+  const uint8_t *const es[2] = {p.gate_s + (int64_t)e * p.I * (p.H / 32), p.up_s + (int64_t)e * p.I * (p.H / 32)};
+  auto row = [&](int m) { return (const uint8_t *)(p.x + (int64_t)(mb[wave].a[m] / p.k) * p.ldx); };
+  auto store = [&](int m, int rt, const f4 &u, const f4 &v) {
+    store_terms<PL>(p.h + (int64_t)mb[wave].a[m] * p.I + n0 + 16 * rt + 4 * g, (int64_t)A * p.I, silu_mul(u[0], v[0]),
+                    silu_mul(u[1], v[1]), silu_mul(u[2], v[2]), silu_mul(u[3], v[3]));
+  };
+  if (n <= 4 && few_tiles<KT, SW>(p.H) <= FEW_TILES) {
+    char *const xs = lds + wave * few_tiles<KT, SW>(p.H) * 1024;
+    stage_rows<KT, 1, SW>(p.H, wave, n, row, 0, xs);
+    auto base = [&](int i, int rt, const uint8_t *&w, const uint8_t *&s) {
+      w = ew[i] + (int64_t)(n0 + 16 * rt) * (p.H / 2);
+      s = es[i] + (int64_t)(n0 + 16 * rt) * (p.H / 32);
+    };
+    auto done = [&](int rt, f4 (&acc)[2]) {
+      if (join_tile<2>(part, rt, wave, acc) && r < n) store(r, rt, acc[0], acc[1]);
+    };
+    if (p.H % (128 * KT) == 0) stream_rows<2, KT, 1, SW, true>(p.H, wave, rts, n, xs, base, done);
+    else stream_rows<2, KT, 1, SW, false>(p.H, wave, rts, n, xs, base, done);
+    return;
+  }
+  for (int rt = 0; rt < rts; ++rt) {
+    Rows<2> R;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) set_rows(R, i, ew[i], es[i], n0 + 16 * rt, p.I, p.H);
+    for (int m0 = 0; m0 < n; m0 += 16) {
+      f4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+      small_dot<2, KT, 1>(acc, R, p.H, wave, SW, min(n - m0, 16), [&](int m) { return row(m0 + m); }, 0, lds + wave * KT * 1024);
+      join_waves<2>(part, acc);
+      if (wave == 0 && m0 + r < n) store(m0 + r, rt, acc[0], acc[1]);
+    }
   }
 }
 
 template <int PL>
-__global__ __launch_bounds__(64 * SW) void k_mx4_down_few(Mx4Experts p) {
-  constexpr int KT = 2, NM = 4;
-  __shared__ __attribute__((aligned(16))) char lds[SW * (NM * 1024 > PL * KT * 1024 ? NM * 1024 : PL * KT * 1024)];
+__global__ __launch_bounds__(64 * SW) void k_mx4_down_few(Mx4Experts p, int nrt) {
+  constexpr int KT = 8;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ Members mb[SW];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
   const int A = p.T * p.k;
   int e;
   const int n = find_members(p.idx, A, blockIdx.y, p.E, mb[wave], e);
   if (n == 0) return;
-  const int n0 = blockIdx.x * 16 * NM;
-  Rows<NM> R;
-#pragma unroll
-  for (int i = 0; i < NM; ++i)
-    set_rows(R, i, p.down + (int64_t)e * p.H * (p.I / 2), p.down_s + (int64_t)e * p.H * (p.I / 32), n0 + 16 * i, p.H, p.I);
-  for (int m0 = 0; m0 < n; m0 += 16) {
-    f4 acc[NM];
-#pragma unroll
-    for (int i = 0; i < NM; ++i) acc[i] = f4{0, 0, 0, 0};
-    small_dot<NM, KT, PL>(acc, R, p.I, wave, SW, n - m0 < 16 ? n - m0 : 16,
-                          [&](int m) { return (const uint8_t *)(p.h + (int64_t)mb[wave].a[m0 + m] * p.I); },
-                          (int64_t)A * p.I * 2, lds + wave * PL * KT * 1024);
-    join_waves<NM>(reinterpret_cast<f4 *>(lds), acc);
-    if (wave == 0 && m0 + r < n)
-#pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        const int c = n0 + 16 * i + 4 * g;
-        if (c < p.H) *reinterpret_cast<f4 *>(p.ya + (int64_t)mb[0].a[m0 + r] * p.H + c) = acc[i];
-      }
-    __syncthreads();
+  const uint8_t *const ew = p.down + (int64_t)e * p.H * (p.I / 2), *const es = p.down_s + (int64_t)e * p.H * (p.I / 32);
+  auto row = [&](int m) { return (const uint8_t *)(p.h + (int64_t)mb[wave].a[m] * p.I); };
+  auto store = [&](int m, int c, const f4 &acc) {
+    if (c < p.H) *reinterpret_cast<f4 *>(p.ya + (int64_t)mb[wave].a[m] * p.H + c + 4 * g) = acc;
+  };
+  if (n <= 4 && PL * few_tiles<KT, 1>(p.I) <= SW * FEW_TILES) {
+    const int n0 = (blockIdx.x * SW + wave) * 16 * nrt;  // the wave's rows
+    stage_rows<KT, PL, 1>(p.I, wave, n, row, (int64_t)A * p.I * 2, lds);
+    auto base = [&](int, int rt, const uint8_t *&w, const uint8_t *&s) {
+      int c = n0 + 16 * rt;
+      if (c >= p.H) c = 0;  // past the end: read, never stored
+      w = ew + (int64_t)c * (p.I / 2);
+      s = es + (int64_t)c * (p.I / 32);
+    };
+    auto done = [&](int rt, f4 (&acc)[1]) {
+      if (r < n) store(r, n0 + 16 * rt, acc[0]);
+    };
+    if (p.I % (128 * KT) == 0) stream_rows<1, KT, PL, 1, true>(p.I, wave, nrt, n, lds, base, done);
+    else stream_rows<1, KT, PL, 1, false>(p.I, wave, nrt, n, lds, base, done);
+    return;
+  }
+  f4 *const part = reinterpret_cast<f4 *>(lds + SW * PL * 2 * 1024);
+  for (int rt = 0; rt < SW * nrt; ++rt) {
+    const int c = (blockIdx.x * SW * nrt + rt) * 16;
+    if (c >= p.H) break;
+    Rows<1> R;
+    set_rows(R, 0, ew, es, c, p.H, p.I);
+    for (int m0 = 0; m0 < n; m0 += 16) {
+      f4 acc[1] = {{0, 0, 0, 0}};
+      small_dot<1, 2, PL>(acc, R, p.I, wave, SW, min(n - m0, 16), [&](int m) { return row(m0 + m); }, (int64_t)A * p.I * 2,
+                          lds + wave * PL * 2 * 1024);
+      join_waves<1>(part, acc);
+      if (wave == 0 && m0 + r < n) store(m0 + r, c, acc[0]);
+    }
   }
 }
 
@@ -262,7 +451,7 @@ __global__ __launch_bounds__(64 * SW) void k_mx4_down_few(Mx4Experts p) {
 // the ranks.
 template <int PL, bool YBF>
 __global__ __launch_bounds__(64 * SW) void k_mx4_down_one(Mx4Experts p) {
-  constexpr int KT = 8;
+  constexpr int KT = 16;
   __shared__ __attribute__((aligned(16))) char lds[SW * PL * KT * 256];
   __shared__ f4 part[16][4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -273,8 +462,10 @@ __global__ __launch_bounds__(64 * SW) void k_mx4_down_one(Mx4Experts p) {
     if (e >= 0 && e < p.E) {
       Rows<1> R;
       set_rows(R, 0, p.down + (int64_t)e * p.H * (p.I / 2), p.down_s + (int64_t)e * p.H * (p.I / 32), n0, p.H, p.I);
-      one_dot<KT, PL>(acc[0], R, p.I, (const uint8_t *)(p.h + (int64_t)a * p.I), (int64_t)A * p.I * 2,
-                      lds + wave * PL * KT * 256);
+      const uint8_t *h = (const uint8_t *)(p.h + (int64_t)a * p.I);
+      char *const xs = lds + wave * PL * KT * 256;
+      if (p.I % 512 == 0) one_dot<KT, PL, true>(acc[0], R, p.I, h, (int64_t)A * p.I * 2, xs);
+      else one_dot<KT, PL, false>(acc[0], R, p.I, h, (int64_t)A * p.I * 2, xs);
       const float w = p.w[a];
       acc[0] *= w;
     }
@@ -358,17 +549,34 @@ hipError_t launch_mx4_product_few(const Mx4Product &p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// LDS: the staged rows of the streaming form, and no less than the other form's
+static unsigned gateup_lds(int64_t K) {
+  const int t = few_tiles<4, SW>(K);
+  return (unsigned)(SW * 1024 * (t <= FEW_TILES && t > 4 ? t : 4));
+}
+static unsigned down_lds(int64_t K, int PL) {
+  const int t = PL * few_tiles<8, 1>(K), least = SW * PL * 2 + SW;
+  return (unsigned)(1024 * (t <= SW * FEW_TILES && t > least ? t : least));
+}
+
 hipError_t launch_mx4_experts_few(const Mx4Experts &p, hipStream_t s) {
   const int A = p.T * p.k;
-  const dim3 b(64 * SW), gg((p.I + 15) / 16, A), gd((p.H + 63) / 64, A), go((p.H + 15) / 16, p.T);
-  if (p.y_bf16) hipLaunchKernelGGL(k_mx4_gateup_few<2>, gg, b, 0, s, p);
-  else hipLaunchKernelGGL(k_mx4_gateup_few<3>, gg, b, 0, s, p);
+  // row tiles one after the other: the more, the longer the stream, as long as every CU has two workgroups
+  auto tiles = [&](int per) {
+    int n = 4;
+    while (n > 1 && (per + n - 1) / n * A < 512) n /= 2;
+    return n;
+  };
+  const int tu = (p.I + 15) / 16, td = (p.H + 16 * SW - 1) / (16 * SW), nu = tiles(tu), nd = tiles(td);
+  const dim3 b(64 * SW), gg((tu + nu - 1) / nu, A), gd((td + nd - 1) / nd, A), go((p.H + 15) / 16, p.T);
+  if (p.y_bf16) hipLaunchKernelGGL(k_mx4_gateup_few<2>, gg, b, gateup_lds(p.H), s, p, nu);
+  else hipLaunchKernelGGL(k_mx4_gateup_few<3>, gg, b, gateup_lds(p.H), s, p, nu);
   if (p.T <= MX4_ONE) {
     if (p.y_bf16) hipLaunchKernelGGL((k_mx4_down_one<2, true>), go, b, 0, s, p);
     else hipLaunchKernelGGL((k_mx4_down_one<3, false>), go, b, 0, s, p);
   } else {
-    if (p.y_bf16) hipLaunchKernelGGL(k_mx4_down_few<2>, gd, b, 0, s, p);
-    else hipLaunchKernelGGL(k_mx4_down_few<3>, gd, b, 0, s, p);
+    if (p.y_bf16) hipLaunchKernelGGL(k_mx4_down_few<2>, gd, b, down_lds(p.I, 2), s, p, nd);
+    else hipLaunchKernelGGL(k_mx4_down_few<3>, gd, b, down_lds(p.I, 3), s, p, nd);
   }
   return hipGetLastError();
 }
