@@ -69,6 +69,33 @@ __device__ __forceinline__ void load_lds16(const void *src, void *lds) {
                                    (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
 }
 
+// dword g of the result: bytes g of the four dwords (block 4 s + g of a row of
+// 16 scales goes to byte s of dword g)
+__device__ __forceinline__ u4 transpose_bytes(u4 v) {
+  const uint32_t a = __builtin_amdgcn_perm(v[1], v[0], 0x05010400);  // a0 b0 a1 b1
+  const uint32_t b = __builtin_amdgcn_perm(v[1], v[0], 0x07030602);
+  const uint32_t c = __builtin_amdgcn_perm(v[3], v[2], 0x05010400);
+  const uint32_t d = __builtin_amdgcn_perm(v[3], v[2], 0x07030602);
+  return u4{__builtin_amdgcn_perm(c, a, 0x05040100), __builtin_amdgcn_perm(c, a, 0x07060302),
+            __builtin_amdgcn_perm(d, b, 0x05040100), __builtin_amdgcn_perm(d, b, 0x07060302)};
+}
+
+// 16 scale bytes from block b on of a row of nblk; 127 past its end
+__device__ __forceinline__ u4 scales16(const uint8_t *row, int b, int nblk) {
+  u4 v;
+  if (b + 16 <= nblk) {
+    __builtin_memcpy(&v, row + b, 16);  // rows of scales lie at any byte
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i] |= (b + 4 * i + j < nblk ? (uint32_t)row[b + 4 * i + j] : 127u) << (8 * j);
+    }
+  }
+  return v;
+}
+
 // four adjacent results of row m from column n on
 template <bool YBF>
 __device__ __forceinline__ void store_row4(const Mx4Product &p, int64_t m, int64_t n, f4 v) {
@@ -91,6 +118,9 @@ __device__ __forceinline__ bool tile_of(int id, int ntiles, int nrows, int &tile
   return j < per && at < all;
 }
 inline unsigned tile_grid(int64_t ntiles, int64_t nrows) { return (unsigned)((ntiles * nrows + 7) / 8 * 8); }
+
+// between LDS accesses of one wave, which execute in order: holds the compiler to it
+__device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
 
 // a workgroup barrier that leaves loads in flight (__syncthreads waits for
 // all of them); LDS accesses before it are done

@@ -7,10 +7,14 @@
 // 32, one scale) per lane, and become exact bf16 operands there by one
 // conversion instruction per pair, so a weight is read and converted once per
 // workgroup.  The activations, which all four waves need, are staged in LDS
-// 128 columns at a time by loads that bypass the registers, double-buffered.
+// 128 columns at a time by loads that bypass the registers.
 // Lane (r, g) = (l % 16, l / 16) holds block g of a row's 128 columns; step j
 // of 4 multiplies columns 32 g + 8 j .. + 7 of both operands, so the four
 // steps cover the 128 in another order, the same for both.
+//
+// Memory answers later than a stage lasts, so codes are asked for three stages
+// ahead (four sets of registers) and activations two (three buffers); loads
+// are counted in order, so a wait for activations lets the later codes fly.
 #include "mx4_dev.h"
 
 namespace ds4 {
@@ -23,15 +27,15 @@ constexpr int GM_WROWS = 256;            // weight rows of a workgroup
 
 // what a workgroup multiplies
 struct GemmTile {
-  const uint8_t *w[4], *s[4];  // codes and scales of the wave's four groups of 16 weight rows (wave-uniform)
-  uint32_t wo[4], so[4];       // this lane's row in them
+  const uint8_t *w[4];         // codes of the wave's four groups of 16 weight rows (wave-uniform)
+  uint32_t wo[4];              // this lane's row in them
+  const uint8_t *srow;         // scales of row l of the 64
   int64_t K;
   int nblk, nst;               // blocks of 32 and stages of 128 columns
 };
 
 struct Codes {
   u4 c[4];
-  uint32_t s[4];
 };
 
 __device__ __forceinline__ void load_codes(const GemmTile &t, int st, Codes &c) {
@@ -39,19 +43,12 @@ __device__ __forceinline__ void load_codes(const GemmTile &t, int st, Codes &c) 
   const int blk = 4 * st + g;
   if (4 * st + 4 <= t.nblk) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c.c[i] = load16(t.w[i] + (t.wo[i] + (uint32_t)blk * 16u));
-      c.s[i] = t.s[i][t.so[i] + (uint32_t)blk];
-    }
+    for (int i = 0; i < 4; ++i) c.c[i] = load16(t.w[i] + (t.wo[i] + (uint32_t)blk * 16u));
   } else {  // the last stage of a length that is no multiple of 128: zeros past the end
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       c.c[i] = u4{0, 0, 0, 0};
-      c.s[i] = 127;
-      if (blk < t.nblk) {
-        c.c[i] = load16(t.w[i] + (t.wo[i] + (uint32_t)blk * 16u));
-        c.s[i] = t.s[i][t.so[i] + (uint32_t)blk];
-      }
+      if (blk < t.nblk) c.c[i] = load16(t.w[i] + (t.wo[i] + (uint32_t)blk * 16u));
     }
   }
 }
@@ -74,38 +71,47 @@ __device__ __forceinline__ void load_rows(const uint8_t *const *rows, int64_t K,
 }
 
 // acc[i][m] += weight rows of group i times activation rows 16 m .. over the
-// K columns, `planes` times (the terms of the activations, plane bytes apart)
+// K columns.  lds: three stages, then 1 KB of scales per wave.
 template <int MT>
-__device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t *const *rows, int planes, int64_t plane,
-                                          char *lds, f4 (&acc)[4][MT]) {
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *const *rows, char *lds, f4 (&acc)[4][MT]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6;
+  char *const lsc = lds + 3 * GM_STAGE + wave * 1024;
+  const int last = t.nst - 1;
+  // scales of 512 columns of the wave's 64 rows, one row per lane, turned in
+  // LDS into one dword per lane and group: byte s is the lane's block of stage s
+  u4 sc;
+  uint32_t sd[4];
+  auto turn_scales = [&]() {
+    *reinterpret_cast<u4 *>(lsc + lane * 16) = transpose_bytes(sc);
+    lds_order();
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[i][m] = f4{0, 0, 0, 0};
-  const int total = t.nst * planes;
-  const uint8_t *at[MT];
-#pragma unroll
-  for (int q = 0; q < MT; ++q) at[q] = rows[q];
-  Codes c0, c1;
-  load_rows<MT>(at, t.K, 0, lds);
+    for (int i = 0; i < 4; ++i) sd[i] = *reinterpret_cast<const uint32_t *>(lsc + (16 * i + r) * 16 + 4 * g);
+    lds_order();
+  };
+  Codes c0, c1, c2, c3;
+  sc = scales16(t.srow, 0, t.nblk);
+  load_rows<MT>(rows, t.K, 0, lds);
+  asm volatile("" ::: "memory");  // the waits count the loads issued after these
   load_codes(t, 0, c0);
-  wait_vm<0>();
+  load_rows<MT>(rows, t.K, min(1, last), lds + GM_STAGE);
+  asm volatile("" ::: "memory");
+  load_codes(t, min(1, last), c1);
+  load_codes(t, min(2, last), c2);
+  turn_scales();
+  wait_vm<12 + MT>();
   barrier_keep_loads();
-  int st = 0, s = 0;
-  // one stage: the next one's loads, this one's products.  Past the end the
-  // last stage is loaded again: with no condition on the loads the products
-  // wait for their own codes alone.
-  auto stage = [&](const Codes &now, Codes &next) {
-    const char *x = lds + (s & 1) * GM_STAGE;
-    if (++s < total && ++st == t.nst) {
-      st = 0;
-#pragma unroll
-      for (int q = 0; q < MT; ++q) at[q] += plane;
-    }
-    load_rows<MT>(at, t.K, st, lds + (s & 1) * GM_STAGE);
-    asm volatile("" ::: "memory");  // the wait below counts the loads issued after these
-    load_codes(t, st, next);
+  int s = 0;
+  const char *x = lds;             // this stage's buffer
+  char *in = lds + 2 * GM_STAGE;   // the buffer that is filled
+  char *const end = lds + 3 * GM_STAGE;
+  // One stage: loads for later ones, then the products.  Past the end the last
+  // stage is loaded again: with no condition on the loads every wait is for a
+  // fixed number of them.
+  auto stage = [&](auto S, const Codes &now, Codes &later) {
+    if (S == 0) sc = scales16(t.srow, min(s + 4, last / 4 * 4) * 4, t.nblk);
+    load_rows<MT>(rows, t.K, min(s + 2, last), in);
+    asm volatile("" ::: "memory");
+    load_codes(t, min(s + 3, last), later);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       bf8 b[MT];
@@ -114,31 +120,53 @@ __device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t *cons
         b[m] = *reinterpret_cast<const bf8 *>(x + (16 * m + r) * 256 + (((4 * g + j) ^ r) << 4));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bf8 a = codes_bf16(now.c[i][j], scale_float(now.s[i]));
+        const bf8 a = codes_bf16(now.c[i][j], scale_float((sd[i] >> (8 * S)) & 255u));
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = mfma_bf16(a, b[m], acc[i][m]);
       }
     }
-    // the next stage's rows have landed (its codes, issued after them, may be on their way)
-    wait_vm<8>();
+    if (S == 3) turn_scales();
+    // the next stage's rows have landed; on their way may be the rows after
+    // them and the codes of the last two stages' loads
+    wait_vm<8 + MT>();
     barrier_keep_loads();
+    x = x + GM_STAGE == end ? lds : x + GM_STAGE;
+    in = in + GM_STAGE == end ? lds : in + GM_STAGE;
+    return ++s > last;
   };
-  while (s + 1 < total) {
-    stage(c0, c1);
-    stage(c1, c0);
+  for (;;) {
+    if (stage(std::integral_constant<int, 0>{}, c0, c3)) break;
+    if (stage(std::integral_constant<int, 1>{}, c1, c0)) break;
+    if (stage(std::integral_constant<int, 2>{}, c2, c1)) break;
+    if (stage(std::integral_constant<int, 3>{}, c3, c2)) break;
   }
-  if (s < total) stage(c0, c1);
-  wait_vm<0>();  // the last loads into LDS, before it is released
+  wait_vm<0>();  // the last loads into LDS, before it is used again or released
+  barrier_keep_loads();
 }
 
+// ... over `planes` terms of the activations, plane bytes apart
+template <int MT>
+__device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t **rows, int planes, int64_t plane, char *lds,
+                                          f4 (&acc)[4][MT]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[i][m] = f4{0, 0, 0, 0};
+  for (int q = 0; q < planes; ++q) {
+    gemm_columns<MT>(t, rows, lds, acc);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) rows[m] += plane;
+  }
+}
+
+// group i of the wave: 16 rows of the matrix (w, s) from row0 on
 __device__ __forceinline__ void weight_rows(GemmTile &t, int i, const uint8_t *w, const uint8_t *s, int64_t row0, int64_t N) {
   const int r = threadIdx.x & 15;
   if (row0 >= N) row0 = 0;  // a group past the end: read, never stored
   t.w[i] = w + row0 * (t.K / 2);
-  t.s[i] = s + row0 * (t.K / 32);
   const uint32_t l = (uint32_t)(row0 + r < N ? r : N - 1 - row0);
   t.wo[i] = l * (uint32_t)(t.K / 2);
-  t.so[i] = l * (uint32_t)(t.K / 32);
+  if ((int)((threadIdx.x >> 4) & 3) == i) t.srow = s + (row0 + l) * (t.K / 32);
 }
 
 template <int MT, int PL>
@@ -230,7 +258,7 @@ __device__ __forceinline__ void down_tile(const Mx4Experts &p, const Mx4Tile &tl
 
 template <int PL, bool DOWN>
 __global__ __launch_bounds__(256, 2) void k_mx4_gemm_experts(Mx4Experts p, int nrows) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * GM_STAGE];
+  __shared__ __attribute__((aligned(16))) char lds[3 * GM_STAGE + 4096];
   int ti, nb;
   if (!tile_of(blockIdx.x, p.tiles->count, nrows, ti, nb)) return;
   const Mx4Tile tl = p.tiles->tile[ti];
@@ -296,7 +324,7 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, int64_t m0, in
 
 template <bool YBF>
 __global__ __launch_bounds__(256, 2) void k_mx4_gemm(Mx4Product p, int mtiles, int nrows) {
-  __shared__ __attribute__((aligned(16))) char lds[2 * GM_STAGE];
+  __shared__ __attribute__((aligned(16))) char lds[3 * GM_STAGE + 4096];
   int ti, nb;
   if (!tile_of(blockIdx.x, mtiles, nrows, ti, nb)) return;
   const int64_t m0 = (int64_t)ti * GM_ROWS, n = p.M - m0 < GM_ROWS ? p.M - m0 : GM_ROWS;

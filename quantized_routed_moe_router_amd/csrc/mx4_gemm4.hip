@@ -15,38 +15,11 @@ namespace ds4 {
 
 namespace {
 
-// dword g of the result: bytes g of the four dwords (block 4 s + g of a row of
-// 16 scales goes to byte s of dword g)
-__device__ __forceinline__ u4 transpose_bytes(u4 v) {
-  const uint32_t a = __builtin_amdgcn_perm(v[1], v[0], 0x05010400);  // a0 b0 a1 b1
-  const uint32_t b = __builtin_amdgcn_perm(v[1], v[0], 0x07030602);
-  const uint32_t c = __builtin_amdgcn_perm(v[3], v[2], 0x05010400);
-  const uint32_t d = __builtin_amdgcn_perm(v[3], v[2], 0x07030602);
-  return u4{__builtin_amdgcn_perm(c, a, 0x05040100), __builtin_amdgcn_perm(c, a, 0x07060302),
-            __builtin_amdgcn_perm(d, b, 0x05040100), __builtin_amdgcn_perm(d, b, 0x07060302)};
-}
-
 template <int S>
 __device__ __forceinline__ f4 mfma_sel(u4 a, u4 b, f4 c, uint32_t sa, uint32_t sb) {
   const i8v A = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
   const i8v B = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, S, (int)sa, S, (int)sb);
-}
-
-// 16 scale bytes from block b on of a row of nblk; 127 past its end
-__device__ __forceinline__ u4 scales16(const uint8_t *row, int b, int nblk) {
-  u4 v;
-  if (b + 16 <= nblk) {
-    __builtin_memcpy(&v, row + b, 16);  // rows of scales lie at any byte
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[i] |= (b + 4 * i + j < nblk ? (uint32_t)row[b + 4 * i + j] : 127u) << (8 * j);
-    }
-  }
-  return v;
 }
 
 template <int MT, int NT, bool YBF>
