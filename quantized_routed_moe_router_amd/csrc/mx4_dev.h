@@ -119,6 +119,20 @@ __device__ __forceinline__ bool tile_of(int id, int ntiles, int nrows, int &tile
 }
 inline unsigned tile_grid(int64_t ntiles, int64_t nrows) { return (unsigned)((ntiles * nrows + 7) / 8 * 8); }
 
+// Codes are loaded four lanes to a row (lane l: row l / 4, block l % 4), 64
+// adjacent bytes that memory serves in one piece; a matrix instruction wants
+// lane (r, g) = (l % 16, l / 16) to hold block g of row r.  The cross-lane
+// read takes them there: with the lanes' own order every lane is a piece of
+// its own, and the L1's lookups were what bound the large products (64% of
+// its cycles, for 43% of the matrix units').
+__device__ __forceinline__ u4 to_lanes(u4 v) {
+  const int l = threadIdx.x & 63, from = ((l & 15) * 4 + (l >> 4)) * 4;
+  u4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[i]);
+  return o;
+}
+
 // between LDS accesses of one wave, which execute in order: holds the compiler to it
 __device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
 

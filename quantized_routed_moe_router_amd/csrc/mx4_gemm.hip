@@ -12,9 +12,9 @@
 // of 4 multiplies columns 32 g + 8 j .. + 7 of both operands, so the four
 // steps cover the 128 in another order, the same for both.
 //
-// Memory answers later than a stage lasts, so codes are asked for three stages
-// ahead (four sets of registers) and activations two (three buffers); loads
-// are counted in order, so a wait for activations lets the later codes fly.
+// Memory answers later than a stage lasts, so codes are asked for two and three
+// stages ahead and activations two (three buffers); loads are counted in
+// order, so a wait for activations lets the later codes fly.
 #include "mx4_dev.h"
 
 namespace ds4 {
@@ -28,7 +28,7 @@ constexpr int GM_WROWS = 256;            // weight rows of a workgroup
 // what a workgroup multiplies
 struct GemmTile {
   const uint8_t *w[4];         // codes of the wave's four groups of 16 weight rows (wave-uniform)
-  uint32_t wo[4];              // this lane's row in them
+  uint32_t wo[4];              // the row in them that this lane loads
   const uint8_t *srow;         // scales of row l of the 64
   int64_t K;
   int nblk, nst;               // blocks of 32 and stages of 128 columns
@@ -38,10 +38,11 @@ struct Codes {
   u4 c[4];
 };
 
+// EVEN: K is a multiple of 128, and no stage ends early
+template <bool EVEN>
 __device__ __forceinline__ void load_codes(const GemmTile &t, int st, Codes &c) {
-  const int g = (threadIdx.x >> 4) & 3;
-  const int blk = 4 * st + g;
-  if (4 * st + 4 <= t.nblk) {
+  const int blk = 4 * st + (threadIdx.x & 3);
+  if (EVEN || 4 * st + 4 <= t.nblk) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c.c[i] = load16(t.w[i] + (t.wo[i] + (uint32_t)blk * 16u));
   } else {  // the last stage of a length that is no multiple of 128: zeros past the end
@@ -56,25 +57,24 @@ __device__ __forceinline__ void load_codes(const GemmTile &t, int st, Codes &c) 
 // Activation rows 16 q + 4 wave + lane/16 of the tile go to LDS row by row,
 // 256 bytes each, the 16-byte chunk c of row r at place c ^ (r % 16): the 16
 // rows that one operand read takes a chunk of then lie in 16 different places.
-template <int MT>
+template <int MT, bool EVEN>
 __device__ __forceinline__ void load_rows(const uint8_t *const *rows, int64_t K, int st, char *lds) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
   for (int q = 0; q < MT; ++q) {
-    const int r = 16 * q + 4 * wave + (lane >> 4);
-    const int c = (lane & 15) ^ (r & 15);
+    const int c = (lane & 15) ^ ((4 * wave + (lane >> 4)) & 15);
     const int64_t k = (int64_t)st * 128 + c * 8;
     char *to = lds + (16 * q + 4 * wave) * 256;
-    if ((int64_t)st * 128 + 128 <= K || k < K) load_lds16(rows[q] + k * 2, to);
+    if (EVEN || (int64_t)st * 128 + 128 <= K || k < K) load_lds16(rows[q] + k * 2, to);
     else *reinterpret_cast<u4 *>(to + lane * 16) = u4{0, 0, 0, 0};
   }
 }
 
 // acc[i][m] += weight rows of group i times activation rows 16 m .. over the
 // K columns.  lds: three stages, then 1 KB of scales per wave.
-template <int MT>
+template <int MT, bool EVEN>
 __device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *const *rows, char *lds, f4 (&acc)[4][MT]) {
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   char *const lsc = lds + 3 * GM_STAGE + wave * 1024;
   const int last = t.nst - 1;
   // scales of 512 columns of the wave's 64 rows, one row per lane, turned in
@@ -88,30 +88,38 @@ __device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *c
     for (int i = 0; i < 4; ++i) sd[i] = *reinterpret_cast<const uint32_t *>(lsc + (16 * i + r) * 16 + 4 * g);
     lds_order();
   };
-  Codes c0, c1, c2, c3;
+  Codes c0, c1, c2, c3;  // stages s % 4, turned to the lanes' order one stage before they are used
+  auto turn_codes = [&](Codes &c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.c[i] = to_lanes(c.c[i]);
+  };
   sc = scales16(t.srow, 0, t.nblk);
-  load_rows<MT>(rows, t.K, 0, lds);
+  load_rows<MT, EVEN>(rows, t.K, 0, lds);
   asm volatile("" ::: "memory");  // the waits count the loads issued after these
-  load_codes(t, 0, c0);
-  load_rows<MT>(rows, t.K, min(1, last), lds + GM_STAGE);
-  asm volatile("" ::: "memory");
-  load_codes(t, min(1, last), c1);
-  load_codes(t, min(2, last), c2);
+  load_codes<EVEN>(t, 0, c0);
+  load_codes<EVEN>(t, min(1, last), c1);
+  load_rows<MT, EVEN>(rows, t.K, min(1, last), lds + GM_STAGE);
+  turn_codes(c0);
   turn_scales();
-  wait_vm<12 + MT>();
+  wait_vm<4 + MT>();
   barrier_keep_loads();
   int s = 0;
   const char *x = lds;             // this stage's buffer
   char *in = lds + 2 * GM_STAGE;   // the buffer that is filled
   char *const end = lds + 3 * GM_STAGE;
-  // One stage: loads for later ones, then the products.  Past the end the last
-  // stage is loaded again: with no condition on the loads every wait is for a
-  // fixed number of them.
-  auto stage = [&](auto S, const Codes &now, Codes &later) {
+  // One stage: the rows two stages on and, at every other one, the codes of
+  // two stages (adjacent halves of 128-byte lines), then the products.  Past
+  // the end the last stage is loaded again: with no condition on the loads
+  // every wait is for a fixed number of them.
+  auto stage = [&](auto S, const Codes &now, Codes &next, Codes &l0, Codes &l1) {
     if (S == 0) sc = scales16(t.srow, min(s + 4, last / 4 * 4) * 4, t.nblk);
-    load_rows<MT>(rows, t.K, min(s + 2, last), in);
+    load_rows<MT, EVEN>(rows, t.K, min(s + 2, last), in);
     asm volatile("" ::: "memory");
-    load_codes(t, min(s + 3, last), later);
+    if (S % 2 == 0) {
+      load_codes<EVEN>(t, min(s + 2, last), l0);
+      load_codes<EVEN>(t, min(s + 3, last), l1);
+      asm volatile("" ::: "memory");
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       bf8 b[MT];
@@ -126,8 +134,9 @@ __device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *c
       }
     }
     if (S == 3) turn_scales();
+    turn_codes(next);
     // the next stage's rows have landed; on their way may be the rows after
-    // them and the codes of the last two stages' loads
+    // them and one pair of stages' codes
     wait_vm<8 + MT>();
     barrier_keep_loads();
     x = x + GM_STAGE == end ? lds : x + GM_STAGE;
@@ -135,17 +144,17 @@ __device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *c
     return ++s > last;
   };
   for (;;) {
-    if (stage(std::integral_constant<int, 0>{}, c0, c3)) break;
-    if (stage(std::integral_constant<int, 1>{}, c1, c0)) break;
-    if (stage(std::integral_constant<int, 2>{}, c2, c1)) break;
-    if (stage(std::integral_constant<int, 3>{}, c3, c2)) break;
+    if (stage(std::integral_constant<int, 0>{}, c0, c1, c2, c3)) break;
+    if (stage(std::integral_constant<int, 1>{}, c1, c2, c2, c3)) break;
+    if (stage(std::integral_constant<int, 2>{}, c2, c3, c0, c1)) break;
+    if (stage(std::integral_constant<int, 3>{}, c3, c0, c0, c1)) break;
   }
   wait_vm<0>();  // the last loads into LDS, before it is used again or released
   barrier_keep_loads();
 }
 
 // ... over `planes` terms of the activations, plane bytes apart
-template <int MT>
+template <int MT, bool EVEN>
 __device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t **rows, int planes, int64_t plane, char *lds,
                                           f4 (&acc)[4][MT]) {
 #pragma unroll
@@ -153,7 +162,7 @@ __device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t **row
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[i][m] = f4{0, 0, 0, 0};
   for (int q = 0; q < planes; ++q) {
-    gemm_columns<MT>(t, rows, lds, acc);
+    gemm_columns<MT, EVEN>(t, rows, lds, acc);
 #pragma unroll
     for (int m = 0; m < MT; ++m) rows[m] += plane;
   }
@@ -161,15 +170,14 @@ __device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t **row
 
 // group i of the wave: 16 rows of the matrix (w, s) from row0 on
 __device__ __forceinline__ void weight_rows(GemmTile &t, int i, const uint8_t *w, const uint8_t *s, int64_t row0, int64_t N) {
-  const int r = threadIdx.x & 15;
   if (row0 >= N) row0 = 0;  // a group past the end: read, never stored
   t.w[i] = w + row0 * (t.K / 2);
-  const uint32_t l = (uint32_t)(row0 + r < N ? r : N - 1 - row0);
-  t.wo[i] = l * (uint32_t)(t.K / 2);
-  if ((int)((threadIdx.x >> 4) & 3) == i) t.srow = s + (row0 + l) * (t.K / 32);
+  const int lane = threadIdx.x & 63, c = lane >> 2, r = lane & 15;  // rows of this lane's codes and scales
+  t.wo[i] = (uint32_t)(row0 + c < N ? c : N - 1 - row0) * (uint32_t)(t.K / 2);
+  if (lane >> 4 == i) t.srow = s + (row0 + r < N ? row0 + r : N - 1) * (t.K / 32);
 }
 
-template <int MT, int PL>
+template <int MT, int PL, bool EVEN>
 __device__ __forceinline__ void gateup_tile(const Mx4Experts &p, const Mx4Tile &tl, int nb, char *lds) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
   const int A = p.T * p.k;
@@ -193,7 +201,7 @@ __device__ __forceinline__ void gateup_tile(const Mx4Experts &p, const Mx4Tile &
     rows[q] = (const uint8_t *)(p.x + (int64_t)(a / p.k) * p.ldx);
   }
   f4 acc[4][MT];
-  gemm_tile<MT>(t, rows, 1, 0, lds, acc);
+  gemm_tile<MT, EVEN>(t, rows, 1, 0, lds, acc);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = 16 * m + r;
@@ -209,7 +217,7 @@ __device__ __forceinline__ void gateup_tile(const Mx4Experts &p, const Mx4Tile &
   }
 }
 
-template <int MT, int PL>
+template <int MT, int PL, bool EVEN>
 __device__ __forceinline__ void down_tile(const Mx4Experts &p, const Mx4Tile &tl, int nb, char *lds) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
   const int A = p.T * p.k;
@@ -229,7 +237,7 @@ __device__ __forceinline__ void down_tile(const Mx4Experts &p, const Mx4Tile &tl
     rows[q] = (const uint8_t *)(p.h + (int64_t)(tl.p0 + (row < tl.n ? row : 0)) * p.I);
   }
   f4 acc[4][MT];
-  gemm_tile<MT>(t, rows, PL, (int64_t)A * p.I * 2, lds, acc);
+  gemm_tile<MT, EVEN>(t, rows, PL, (int64_t)A * p.I * 2, lds, acc);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = 16 * m + r;
@@ -256,13 +264,13 @@ __device__ __forceinline__ void down_tile(const Mx4Experts &p, const Mx4Tile &tl
     default: CALL(6); break;    \
   }
 
-template <int PL, bool DOWN>
+template <int PL, bool DOWN, bool EVEN>
 __global__ __launch_bounds__(256, 2) void k_mx4_gemm_experts(Mx4Experts p, int nrows) {
   __shared__ __attribute__((aligned(16))) char lds[3 * GM_STAGE + 4096];
   int ti, nb;
   if (!tile_of(blockIdx.x, p.tiles->count, nrows, ti, nb)) return;
   const Mx4Tile tl = p.tiles->tile[ti];
-#define CALL(MT) (DOWN ? down_tile<MT, PL>(p, tl, nb, lds) : gateup_tile<MT, PL>(p, tl, nb, lds))
+#define CALL(MT) (DOWN ? down_tile<MT, PL, EVEN>(p, tl, nb, lds) : gateup_tile<MT, PL, EVEN>(p, tl, nb, lds))
   BY_GROUPS(tl.n, CALL)
 #undef CALL
 }
@@ -295,7 +303,7 @@ __global__ __launch_bounds__(512) void k_mx4_plan(Mx4Experts p) {
   }
 }
 
-template <int MT, bool YBF>
+template <int MT, bool YBF, bool EVEN>
 __device__ __forceinline__ void product_tile(const Mx4Product &p, int64_t m0, int64_t n, int nb, char *lds) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
   GemmTile t;
@@ -312,7 +320,7 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, int64_t m0, in
     rows[q] = (const uint8_t *)p.a + (m0 + (row < n ? row : 0)) * p.lda * 2;
   }
   f4 acc[4][MT];
-  gemm_tile<MT>(t, rows, 1, 0, lds, acc);
+  gemm_tile<MT, EVEN>(t, rows, 1, 0, lds, acc);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = 16 * m + r;
@@ -322,13 +330,13 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, int64_t m0, in
   }
 }
 
-template <bool YBF>
+template <bool YBF, bool EVEN>
 __global__ __launch_bounds__(256, 2) void k_mx4_gemm(Mx4Product p, int mtiles, int nrows) {
   __shared__ __attribute__((aligned(16))) char lds[3 * GM_STAGE + 4096];
   int ti, nb;
   if (!tile_of(blockIdx.x, mtiles, nrows, ti, nb)) return;
   const int64_t m0 = (int64_t)ti * GM_ROWS, n = p.M - m0 < GM_ROWS ? p.M - m0 : GM_ROWS;
-#define CALL(MT) product_tile<MT, YBF>(p, m0, n, nb, lds)
+#define CALL(MT) product_tile<MT, YBF, EVEN>(p, m0, n, nb, lds)
   BY_GROUPS((int)n, CALL)
 #undef CALL
 }
@@ -339,23 +347,22 @@ int64_t mx4_max_tiles(int64_t A, int64_t E) { return A / GM_ROWS + (A < E ? A : 
 
 hipError_t launch_mx4_gemm_experts(const Mx4Experts &p, hipStream_t s) {
   const int nu = (p.I + GM_WROWS / 2 - 1) / (GM_WROWS / 2), nd = (p.H + GM_WROWS - 1) / GM_WROWS;
-  const dim3 b(256);
+  const dim3 b(256), gu(tile_grid(p.max_tiles, nu)), gd(tile_grid(p.max_tiles, nd));
   hipLaunchKernelGGL(k_mx4_plan, dim3(1), dim3(512), 0, s, p);
-  if (p.y_bf16) {
-    hipLaunchKernelGGL((k_mx4_gemm_experts<1, false>), dim3(tile_grid(p.max_tiles, nu)), b, 0, s, p, nu);
-    hipLaunchKernelGGL((k_mx4_gemm_experts<1, true>), dim3(tile_grid(p.max_tiles, nd)), b, 0, s, p, nd);
-  } else {
-    hipLaunchKernelGGL((k_mx4_gemm_experts<3, false>), dim3(tile_grid(p.max_tiles, nu)), b, 0, s, p, nu);
-    hipLaunchKernelGGL((k_mx4_gemm_experts<3, true>), dim3(tile_grid(p.max_tiles, nd)), b, 0, s, p, nd);
-  }
+  auto up = p.y_bf16 ? (p.H % 128 ? k_mx4_gemm_experts<1, false, false> : k_mx4_gemm_experts<1, false, true>)
+                     : (p.H % 128 ? k_mx4_gemm_experts<3, false, false> : k_mx4_gemm_experts<3, false, true>);
+  auto down = p.y_bf16 ? (p.I % 128 ? k_mx4_gemm_experts<1, true, false> : k_mx4_gemm_experts<1, true, true>)
+                       : (p.I % 128 ? k_mx4_gemm_experts<3, true, false> : k_mx4_gemm_experts<3, true, true>);
+  hipLaunchKernelGGL(up, gu, b, 0, s, p, nu);
+  hipLaunchKernelGGL(down, gd, b, 0, s, p, nd);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_gemm(const Mx4Product &p, hipStream_t s) {
   const int64_t mt = (p.M + GM_ROWS - 1) / GM_ROWS, nr = (p.N + GM_WROWS - 1) / GM_WROWS;
-  const dim3 g(tile_grid(mt, nr)), b(256);
-  if (p.y_bf16) hipLaunchKernelGGL((k_mx4_gemm<true>), g, b, 0, s, p, (int)mt, (int)nr);
-  else hipLaunchKernelGGL((k_mx4_gemm<false>), g, b, 0, s, p, (int)mt, (int)nr);
+  auto f = p.y_bf16 ? (p.K % 128 ? k_mx4_gemm<true, false> : k_mx4_gemm<true, true>)
+                    : (p.K % 128 ? k_mx4_gemm<false, false> : k_mx4_gemm<false, true>);
+  hipLaunchKernelGGL(f, dim3(tile_grid(mt, nr)), dim3(256), 0, s, p, (int)mt, (int)nr);
   return hipGetLastError();
 }
 
