@@ -107,6 +107,36 @@ __device__ __forceinline__ void store_row4(const Mx4Product &p, int64_t m, int64
     }
 }
 
+// NV (4, 8 or 16) adjacent results of row m from column n on, n a multiple of
+// NV; wide: rows are a multiple of 16 bytes apart
+template <bool YBF, int NV>
+__device__ __forceinline__ void store_cols(const Mx4Product &p, bool wide, int64_t m, int64_t n, const float (&v)[NV]) {
+  if (wide && n + NV <= p.N) {
+    if (YBF) {
+      __bf16 *y = (__bf16 *)p.y + m * p.ldy + n;
+#pragma unroll
+      for (int i = 0; i < NV; i += 8) {
+        if (NV == 4) *reinterpret_cast<bf4 *>(y) = bf4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        else
+          *reinterpret_cast<bf8 *>(y + i) = bf8{(__bf16)v[i], (__bf16)v[i + 1], (__bf16)v[i + 2], (__bf16)v[i + 3],
+                                                (__bf16)v[i + 4], (__bf16)v[i + 5], (__bf16)v[i + 6], (__bf16)v[i + 7]};
+      }
+    } else {
+      float *y = (float *)p.y + m * p.ldy + n;
+#pragma unroll
+      for (int i = 0; i < NV; i += 4) *reinterpret_cast<f4 *>(y + i) = f4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (n + i < p.N) {
+      if (YBF) ((__bf16 *)p.y)[m * p.ldy + n + i] = (__bf16)v[i];
+      else ((float *)p.y)[m * p.ldy + n + i] = v[i];
+    }
+}
+__device__ __forceinline__ bool wide_rows(const Mx4Product &p) { return p.ldy % (p.y_bf16 ? 8 : 4) == 0; }
+
 // The workgroup's tile and weight rows.  Consecutive workgroups go to
 // different XCDs, each of which takes a contiguous part of the work, all
 // weight rows of a tile one after the other: a tile's activations stay in that
@@ -132,6 +162,15 @@ __device__ __forceinline__ u4 to_lanes(u4 v) {
   for (int i = 0; i < 4; ++i) o[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[i]);
   return o;
 }
+
+// Places of the 16-byte chunks of staged rows.  A 16-byte LDS read serves the
+// lanes 0-3, 12-15, 20-23 and 24-27 together, then 4-7, 8-11, 16-19 and 28-31,
+// and the same of the upper half; with these exchanges the rows that read
+// chunk g and those that read g + 1 there lie in different banks (4.4 cycles a
+// read; 8.1 with the row's own bits in their order, where they meet in pairs).
+// r: row 0..15 of its group; chunk c goes to place c ^ f.
+__device__ __forceinline__ int place8(int r) { return (r & 2) | (r >> 3) << 2; }                 // rows of 8 chunks
+__device__ __forceinline__ int place16(int r) { return (r & 3) | ((4 - (r >> 2)) & 3) << 2; }  // rows of 16 chunks
 
 // between LDS accesses of one wave, which execute in order: holds the compiler to it
 __device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }

@@ -55,14 +55,13 @@ __device__ __forceinline__ void load_codes(const GemmTile &t, int st, Codes &c) 
 }
 
 // Activation rows 16 q + 4 wave + lane/16 of the tile go to LDS row by row,
-// 256 bytes each, the 16-byte chunk c of row r at place c ^ (r % 16): the 16
-// rows that one operand read takes a chunk of then lie in 16 different places.
+// 256 bytes each.
 template <int MT, bool EVEN>
 __device__ __forceinline__ void load_rows(const uint8_t *const *rows, int64_t K, int st, char *lds) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
   for (int q = 0; q < MT; ++q) {
-    const int c = (lane & 15) ^ ((4 * wave + (lane >> 4)) & 15);
+    const int c = (lane & 15) ^ place16(4 * wave + (lane >> 4));
     const int64_t k = (int64_t)st * 128 + c * 8;
     char *to = lds + (16 * q + 4 * wave) * 256;
     if (EVEN || (int64_t)st * 128 + 128 <= K || k < K) load_lds16(rows[q] + k * 2, to);
@@ -125,7 +124,7 @@ __device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *c
       bf8 b[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
-        b[m] = *reinterpret_cast<const bf8 *>(x + (16 * m + r) * 256 + (((4 * g + j) ^ r) << 4));
+        b[m] = *reinterpret_cast<const bf8 *>(x + (16 * m + r) * 256 + (((4 * g + j) ^ place16(r)) << 4));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bf8 a = codes_bf16(now.c[i][j], scale_float((sd[i] >> (8 * S)) & 255u));

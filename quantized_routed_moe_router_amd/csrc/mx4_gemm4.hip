@@ -3,11 +3,14 @@
 // one scale byte per lane's block.
 //
 // A workgroup of four waves has 16 MT activation rows and 64 NT weight rows.
-// Both operands' codes are staged in LDS, 128 columns at a time and three
-// buffers deep, by loads that bypass the registers; a wave multiplies all the
+// Both operands' codes are staged in LDS, 256 columns (whole lines of memory)
+// at a time and three buffers deep, by loads that bypass the registers; a wave multiplies all the
 // activation rows with its own 16 NT weight rows.  (Weights straight to
 // registers come in the wrong order: a lane's row is not its neighbour's, and
 // 64 lookups a load or as many cross-lane reads cost more than the LDS does.)
+// Row 4 g' + v of its i-th group of 16 is row 4 NT g' + 4 i + v of them: a
+// lane's results are then 4 NT adjacent columns, whole pieces of memory (two
+// bytes at a time, the stores took a third of the kernel).
 // The scales of 512 columns (16 bytes a row) are turned into the order of the
 // lanes on their way through LDS: lane (r, g) then reads one dword with the
 // scales of its block of four successive instructions, each of which picks
@@ -28,16 +31,15 @@ __device__ __forceinline__ f4 mfma_sel(u4 a, u4 b, f4 c, uint32_t sa, uint32_t s
 template <int MT, int NT, bool YBF, bool EVEN>
 __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Product p, int mtiles, int ntiles) {
   constexpr int BM = 16 * MT, ROWS = BM + 64 * NT;  // activation rows, then weight rows
-  constexpr int STAGE = ROWS * 64;                   // bytes of 128 columns of their codes
+  constexpr int STAGE = ROWS * 128;                  // bytes of 256 columns of their codes
   constexpr int DMA = STAGE / 4096, SPT = (ROWS + 255) / 256;
-  static_assert(STAGE % 4096 == 0, "whole loads");
   __shared__ __attribute__((aligned(16))) char lds[3 * STAGE + 2 * ROWS * 16];
   char *const lsc = lds + 3 * STAGE;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
   int ti, nb;
   if (!tile_of(blockIdx.x, mtiles, ntiles, ti, nb)) return;
   const int64_t m0 = (int64_t)ti * BM, n0 = (int64_t)nb * 64 * NT;
-  const int nblk = (int)(p.K / 32), nst = (nblk + 3) / 4, last = nst - 1;
+  const int nblk = (int)(p.K / 32), last = (nblk + 7) / 8 - 1;
   const int64_t cb = p.K / 2;
 
   // a row of the tile: an activation row or a weight row (past the end the last one, never stored)
@@ -45,13 +47,15 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
     if (row < BM) return a + (m0 + row < p.M ? m0 + row : p.M - 1) * bytes;
     return w + (n0 + row - BM < p.N ? n0 + row - BM : p.N - 1) * bytes;
   };
-  // load q of a stage: 16 rows of 4 chunks, chunk c of row r at place
-  // c ^ (r / 4 % 4), so that 8 lanes of a read meet 8 banks
+  // load q of a stage: 8 rows of 8 chunks; a weight row's place goes by its row in the instruction
   const uint8_t *src[DMA];
-  const int ch = (lane & 3) ^ ((lane >> 4) & 3);
+  int ch[DMA];
 #pragma unroll
-  for (int q = 0; q < DMA; ++q)
-    src[q] = row_of((q * 4 + wave) * 16 + (lane >> 2), (const uint8_t *)p.a, p.w, cb) + ch * 16;
+  for (int q = 0; q < DMA; ++q) {
+    const int row = (q * 4 + wave) * 8 + (lane >> 3), wrow = row - BM;
+    ch[q] = (lane & 7) ^ place8(row < BM ? row & 15 : (wrow / (4 * NT) & 3) << 2 | (wrow & 3));
+    src[q] = row_of(row, (const uint8_t *)p.a, p.w, cb) + ch[q] * 16;
+  }
   const uint8_t *sx[SPT];
 #pragma unroll
   for (int q = 0; q < SPT; ++q) sx[q] = row_of(min(q * 256 + tid, ROWS - 1), p.a_scales, p.ws, nblk);
@@ -60,7 +64,7 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
 #pragma unroll
     for (int q = 0; q < DMA; ++q) {
       char *d = to + (q * 4 + wave) * 1024;
-      if (EVEN || st * 4 + 4 <= nblk || st * 4 + ch < nblk) load_lds16(src[q] + (int64_t)st * 64, d);
+      if (EVEN || st * 8 + 8 <= nblk || st * 8 + ch[q] < nblk) load_lds16(src[q] + (int64_t)st * 128, d);
       else *reinterpret_cast<u4 *>(d + lane * 16) = u4{0, 0, 0, 0};
     }
     asm volatile("" ::: "memory");
@@ -68,7 +72,7 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
   u4 sc[SPT];
   auto load_sc = [&](int st) {
 #pragma unroll
-    for (int q = 0; q < SPT; ++q) sc[q] = scales16(sx[q], st * 4, nblk);
+    for (int q = 0; q < SPT; ++q) sc[q] = scales16(sx[q], st * 8, nblk);
   };
   auto put_sc = [&](int buf) {
 #pragma unroll
@@ -81,7 +85,9 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[i][m] = f4{0, 0, 0, 0};
   uint32_t sa[MT], sw[NT];
-  const int fo = r * 64 + 16 * (g ^ ((r >> 2) & 3));
+  // this lane's row of the weights' first group; the chunk of a half goes to place (4 h + g) ^ f
+  const int wr = wave * 16 * NT + 4 * NT * (r >> 2) + (r & 3);
+  const int fa = r * 128, fw = (BM + wr) * 128, f0 = (g ^ place8(r)) * 16;
   load_sc(0);
   load(0, lds);
   load(min(1, last), lds + STAGE);
@@ -95,24 +101,28 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
   // are for a fixed number of loads.
   auto stage = [&](auto S) {
     if (S == 0) {
-      const char *const ls = lsc + (s & 4) / 4 * ROWS * 16;
+      const char *const ls = lsc + (s & 2) / 2 * ROWS * 16;
 #pragma unroll
       for (int m = 0; m < MT; ++m) sa[m] = *reinterpret_cast<const uint32_t *>(ls + (16 * m + r) * 16 + 4 * g);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) sw[i] = *reinterpret_cast<const uint32_t *>(ls + (BM + (wave * NT + i) * 16 + r) * 16 + 4 * g);
-      load_sc(min(s + 4, last / 4 * 4));
+      for (int i = 0; i < NT; ++i) sw[i] = *reinterpret_cast<const uint32_t *>(ls + (BM + wr + 4 * i) * 16 + 4 * g);
+      load_sc(min(s + 2, last / 2 * 2));
     }
     load(min(s + 2, last), in);
-    u4 w[NT], a[MT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) w[i] = *reinterpret_cast<const u4 *>(x + (BM + (wave * NT + i) * 16) * 64 + fo);
+    for (int h = 0; h < 2; ++h) {
+      u4 w[NT], a[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) a[m] = *reinterpret_cast<const u4 *>(x + m * 1024 + fo);
+      for (int i = 0; i < NT; ++i) w[i] = *reinterpret_cast<const u4 *>(x + fw + i * 512 + (f0 ^ 64 * h));
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m) a[m] = *reinterpret_cast<const u4 *>(x + fa + m * 2048 + (f0 ^ 64 * h));
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i][m] = mfma_sel<S>(w[i], a[m], acc[i][m], sw[i], sa[m]);
-    if (S == 3) put_sc((s & 4) / 4 ^ 1);
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          acc[i][m] = h ? mfma_sel<S + 1>(w[i], a[m], acc[i][m], sw[i], sa[m]) : mfma_sel<S>(w[i], a[m], acc[i][m], sw[i], sa[m]);
+    }
+    if (S == 2) put_sc((s & 2) / 2 ^ 1);
     wait_vm<DMA>();  // the next stage's codes have landed
     barrier_keep_loads();
     x = x + STAGE == lds + 3 * STAGE ? lds : x + STAGE;
@@ -121,17 +131,18 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
   };
   for (;;) {
     if (stage(std::integral_constant<int, 0>{})) break;
-    if (stage(std::integral_constant<int, 1>{})) break;
     if (stage(std::integral_constant<int, 2>{})) break;
-    if (stage(std::integral_constant<int, 3>{})) break;
   }
   wait_vm<0>();  // the last loads into LDS, before it is released
+  const bool wide = wide_rows(p);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int64_t row = m0 + 16 * m + r;
     if (row >= p.M) continue;
+    float v[4 * NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) store_row4<YBF>(p, row, n0 + (wave * NT + i) * 16 + 4 * g, acc[i][m]);
+    for (int i = 0; i < 4 * NT; ++i) v[i] = acc[i / 4][m][i % 4];
+    store_cols<YBF, 4 * NT>(p, wide, row, n0 + wave * 16 * NT + 4 * NT * g, v);
   }
 }
 
@@ -141,8 +152,8 @@ template <int MT, int NT>
 static hipError_t gemm4(const Mx4Product &p, hipStream_t s) {
   const int mt = (int)((p.M + 16 * MT - 1) / (16 * MT)), nt = (int)((p.N + 64 * NT - 1) / (64 * NT));
   const dim3 g(tile_grid(mt, nt)), b(256);
-  auto f = p.y_bf16 ? (p.K % 128 ? k_mx4_gemm4<MT, NT, true, false> : k_mx4_gemm4<MT, NT, true, true>)
-                    : (p.K % 128 ? k_mx4_gemm4<MT, NT, false, false> : k_mx4_gemm4<MT, NT, false, true>);
+  auto f = p.y_bf16 ? (p.K % 256 ? k_mx4_gemm4<MT, NT, true, false> : k_mx4_gemm4<MT, NT, true, true>)
+                    : (p.K % 256 ? k_mx4_gemm4<MT, NT, false, false> : k_mx4_gemm4<MT, NT, false, true>);
   hipLaunchKernelGGL(f, g, b, 0, s, p, mt, nt);
   return hipGetLastError();
 }
