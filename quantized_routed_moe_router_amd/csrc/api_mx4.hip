@@ -52,7 +52,7 @@ GateLayout gate_layout(const ds4moe_gating &g, int64_t T) {
     return o;
   };
   L.idx = take(4 * (size_t)T * g.top_k);
-  L.ccnt = take(2 * (size_t)gate_chunks_max(T) * g.n_experts);
+  L.ccnt = take(2 * (size_t)gate_chunks_max(T) * ((g.n_experts + 1) & ~1));
   L.lrank = take(2 * (size_t)T * g.top_k);
   L.total = off;
   return L;

@@ -54,39 +54,97 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return logit_key(v);
 }
 
-// maximum over the wave, in every lane
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const uint32_t u = (uint32_t)__shfl_xor((int)v, o);
-    v = v > u ? v : u;
-  }
-  return v;
+// Reductions by lane moves inside the vector unit: 4 steps in rows of 16
+// lanes, 2 across them, the result read from the last lane (a tenth of the
+// time of as many reads of another lane through the LDS unit).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t lane_move(uint32_t old, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS, 0xF, false);
 }
+template <typename F>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, uint32_t none, F f) {  // lane 15 of each row
+  v = f(v, lane_move<0x111, 0xF>(none, v));
+  v = f(v, lane_move<0x112, 0xF>(none, v));
+  v = f(v, lane_move<0x114, 0xF>(none, v));
+  return f(v, lane_move<0x118, 0xF>(none, v));
+}
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t none, F f) {  // in every lane
+  v = row_reduce(v, none, f);
+  v = f(v, lane_move<0x142, 0xA>(none, v));
+  v = f(v, lane_move<0x143, 0xC>(none, v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t max_f32(uint32_t a, uint32_t b) {
+  return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+}
+__device__ __forceinline__ uint32_t add_f32(uint32_t a, uint32_t b) {
+  return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+}
+constexpr uint32_t MINUS_INF = 0xFF800000u;
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) { return wave_reduce(v, 0u, max_u32); }
 __device__ __forceinline__ float wave_max_f(float v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+  return __uint_as_float(wave_reduce(__float_as_uint(v), MINUS_INF, max_f32));
 }
-__device__ __forceinline__ float wave_sum_f(float v) {
+__device__ __forceinline__ float wave_sum_f(float v) { return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, add_f32)); }
+// of the first 16 lanes
+__device__ __forceinline__ float first_max_f(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane((int)row_reduce(__float_as_uint(v), MINUS_INF, max_f32), 15));
+}
+__device__ __forceinline__ float first_sum_f(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane((int)row_reduce(__float_as_uint(v), 0u, add_f32), 15));
+}
+
+// the two largest of the lane's and another lane's two
+template <int CTRL>
+__device__ __forceinline__ void merge_move(float &m1, float &m2) {
+  const float o1 = __uint_as_float(lane_move<CTRL, 0xF>(__float_as_uint(m1), __float_as_uint(m1)));
+  const float o2 = __uint_as_float(lane_move<CTRL, 0xF>(__float_as_uint(m2), __float_as_uint(m2)));
+  m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+  m1 = fmaxf(m1, o1);
+}
+__device__ __forceinline__ void merge_xor(float &m1, float &m2, int o) {
+  const float o1 = __shfl_xor(m1, o), o2 = __shfl_xor(m2, o);
+  m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+  m1 = fmaxf(m1, o1);
+}
+
+// the NK logits of a lane; VEC: in one load
+template <int NK, bool BF16, bool VEC>
+__device__ __forceinline__ void load_logits(const GateArgs &a, int64_t t, float (&x)[NK]) {
+  const int e0 = NK * (threadIdx.x & 63);
+  const int64_t at = t * a.ld + e0;
+  if (VEC) {
 #pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+    for (int i = 0; i < NK; ++i) x[i] = -INFINITY;
+    if (e0 >= a.E) return;
+    if (BF16) {
+      uint16_t u[NK];
+      __builtin_memcpy(u, __builtin_assume_aligned((const uint16_t *)a.logits + at, 2 * NK), 2 * NK);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) x[i] = clean_logit(bf16_bits_to_float(u[i]));
+    } else {
+      float u[NK];
+      __builtin_memcpy(u, __builtin_assume_aligned((const float *)a.logits + at, NK < 4 ? 4 * NK : 16), 4 * NK);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) x[i] = clean_logit(u[i]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < NK; ++i) x[i] = e0 + i < a.E ? clean_logit(load_logit<BF16>(a.logits, at + i)) : -INFINITY;
 }
 
 // One token by one wave; lane l holds experts NK*l .. NK*l+NK-1.  Lane j < k
 // returns expert and weight of rank j.  xl, kl: wave-private LDS rows of NK*64
 // floats.
-template <int NK, bool BF16>
-__device__ __forceinline__ void gate_token(const GateArgs &a, int64_t t, float *xl, float *kl, int &my_e, float &my_w) {
+template <int NK>
+__device__ __forceinline__ void gate_token(const GateArgs &a, const float (&x)[NK], float *xl, float *kl, int &my_e,
+                                           float &my_w) {
   const int lane = threadIdx.x & 63;
-  float x[NK];
 #pragma unroll
-  for (int i = 0; i < NK; ++i) {
-    const int e = NK * lane + i;
-    x[i] = e < a.E ? clean_logit(load_logit<BF16>(a.logits, t * a.ld + e)) : -INFINITY;
-    xl[e] = x[i];
-  }
+  for (int i = 0; i < NK; ++i) xl[NK * lane + i] = x[i];
   // softmax over all experts: maximum and sum
   float mx = 0.0f, zinv = 1.0f;
   const bool soft = a.score == SC_SOFTMAX;
@@ -134,16 +192,17 @@ __device__ __forceinline__ void gate_token(const GateArgs &a, int64_t t, float *
         m2 = fmaxf(m2, fminf(m1, u));
         m1 = fmaxf(m1, u);
       }
-    for (int o = 1; o < lanes_per; o <<= 1) {
-      const float o1 = __shfl_xor(m1, o), o2 = __shfl_xor(m2, o);
-      m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
-      m1 = fmaxf(m1, o1);
-    }
+    if (lanes_per > 1) merge_move<0xB1>(m1, m2);   // neighbours
+    if (lanes_per > 2) merge_move<0x4E>(m1, m2);   // pairs of a quad
+    if (lanes_per > 4) merge_move<0x141>(m1, m2);  // quads of 8 lanes, mirrored
+    if (lanes_per > 8) merge_move<0x140>(m1, m2);  // halves of a row, mirrored
+    if (lanes_per > 16) merge_xor(m1, m2, 16);
+    if (lanes_per > 32) merge_xor(m1, m2, 32);
     // a second best that is masked adds nothing; a group with none live is last
     const float gs = (a.group_rank > 1 && m2 > -INFINITY) ? m1 + m2 : m1;
     int rank = 0;
     for (int h = 0; h < a.G; ++h) {
-      const float o = __shfl(gs, h * lanes_per);
+      const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gs), h * lanes_per));
       rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
     }
     stays = __ballot(g < a.G && j == 0 && rank < a.top_groups);
@@ -171,7 +230,7 @@ __device__ __forceinline__ void gate_token(const GateArgs &a, int64_t t, float *
     int at = 0;
 #pragma unroll
     for (int i = NK - 1; i >= 0; --i) at = key[i] == m ? i : at;
-    at = __shfl(at, win);
+    at = __builtin_amdgcn_readlane(at, win);
     if (lane == win) {
 #pragma unroll
       for (int i = 0; i < NK; ++i) key[i] = i == at ? 0u : key[i];
@@ -185,13 +244,13 @@ __device__ __forceinline__ void gate_token(const GateArgs &a, int64_t t, float *
   float s = 0.0f;
   const float l = lane < a.k ? xl[my_e] : -INFINITY;
   const bool live = lane < a.k && my_key > 1u && l != -INFINITY;
-  if (a.renorm) mx = wave_max_f(live ? l : -INFINITY);  // sums of the chosen alone
+  if (a.renorm) mx = first_max_f(live ? l : -INFINITY);  // sums of the chosen alone
   if (live) {
     if (soft) s = expf(l - mx) * (a.renorm ? 1.0f : zinv);
     else s = a.renorm ? relative_score(l, a.score, mx) : own_score(l, a.score);
   }
   if (a.renorm) {
-    const float S = wave_sum_f(s);
+    const float S = first_sum_f(s);
     s = S > 0.0f ? s / S : 0.0f;
   }
   my_w = a.scale * s;
@@ -225,16 +284,19 @@ __device__ __forceinline__ int wave_scan_512(const int32_t *c, int32_t *off, int
 // One workgroup per chunk of tokens, a wave per token; a chunk's tokens go in
 // blocks of 64 whose experts are marked in a 64-bit mask per expert, so the
 // rank of an assignment among its expert's (tokens ascending) is a popcount.
-template <int NK, bool BF16>
+// A chunk that is the whole call (up to 64 tokens) is finished here.
+template <int NK, bool BF16, bool VEC>
 __global__ __launch_bounds__(1024) void k_gate(GateArgs a) {
   __shared__ float xl[GATE_WAVES][NK * 64], kl[GATE_WAVES][NK * 64];
   __shared__ unsigned long long mask[GATE_MAXE];
-  __shared__ int32_t run[GATE_MAXE];
+  __shared__ int32_t run[GATE_MAXE], off[GATE_MAXE];
   __shared__ int32_t bi[64 * 16];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int64_t c0 = (int64_t)blockIdx.x * a.chunk;
   const int n = (int)(a.T - c0 < a.chunk ? a.T - c0 : a.chunk);
   const bool perm = a.perm != nullptr;
+  float x[NK];
+  if (wave < n) load_logits<NK, BF16, VEC>(a, c0 + wave, x);
   for (int e = tid; e < a.E; e += 1024) run[e] = 0;
   for (int b0 = 0; b0 < n; b0 += 64) {
     const int nb = n - b0 < 64 ? n - b0 : 64;
@@ -243,8 +305,13 @@ __global__ __launch_bounds__(1024) void k_gate(GateArgs a) {
     for (int q = wave; q < nb; q += GATE_WAVES) {
       const int64_t t = c0 + b0 + q;
       int e;
-      float w;
-      gate_token<NK, BF16>(a, t, xl[wave], kl[wave], e, w);
+      float w, next[NK];
+      // the wave's next token, while this one is worked on
+      const int nq = q + GATE_WAVES < nb ? b0 + q + GATE_WAVES : b0 + 64 + wave;
+      if (nq < n) load_logits<NK, BF16, VEC>(a, c0 + nq, next);
+      gate_token<NK>(a, x, xl[wave], kl[wave], e, w);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) x[i] = next[i];
       if (lane < a.k) {
         if (a.idx) a.idx[t * a.k + lane] = e;
         if (a.w) a.w[t * a.k + lane] = w;
@@ -256,6 +323,24 @@ __global__ __launch_bounds__(1024) void k_gate(GateArgs a) {
     }
     __syncthreads();
     if (!perm) continue;
+    if (a.nchunk == 1) {
+      for (int e = tid; e < a.E; e += 1024) {
+        run[e] = __popcll(mask[e]);
+        a.counts[e] = run[e];
+      }
+      __syncthreads();
+      if (wave == 0) {
+        const int all = wave_scan_512(run, off, a.E);
+        if (lane == 0) a.offsets[a.E] = all;
+      }
+      __syncthreads();
+      for (int e = tid; e < a.E; e += 1024) a.offsets[e] = off[e];
+      for (int i = tid; i < nb * a.k; i += 1024) {
+        const int q = i / a.k, e = bi[i];
+        a.perm[off[e] + __popcll(mask[e] & ((1ull << q) - 1))] = i;
+      }
+      return;
+    }
     for (int i = tid; i < nb * a.k; i += 1024) {
       const int q = i / a.k, e = bi[i];
       a.lrank[(c0 + b0) * a.k + i] = (uint16_t)(run[e] + __popcll(mask[e] & ((1ull << q) - 1)));
@@ -265,27 +350,52 @@ __global__ __launch_bounds__(1024) void k_gate(GateArgs a) {
     __syncthreads();
   }
   if (!perm) return;
-  for (int e = tid; e < a.E; e += 1024) a.ccnt[(int64_t)blockIdx.x * a.E + e] = (uint16_t)run[e];
+  const int epad = (a.E + 1) & ~1;
+  for (int e = tid; e < epad; e += 1024) a.ccnt[(int64_t)blockIdx.x * epad + e] = e < a.E ? (uint16_t)run[e] : 0;
 }
 
 // One workgroup per chunk: every expert's count in the chunks before this one
-// and in all, the offsets, and the places of the chunk's assignments.
+// and in all (a thread per two experts and every 1024 / columns-th chunk), the
+// offsets, and the places of the chunk's assignments.
 __global__ __launch_bounds__(1024) void k_gate_place(GateArgs a) {
+  __shared__ int32_t part[2][2048];
   __shared__ int32_t before[GATE_MAXE], total[GATE_MAXE], off[GATE_MAXE];
-  const int tid = threadIdx.x;
-  for (int e = tid; e < a.E; e += 1024) {
-    before[e] = 0;
-    total[e] = 0;
-  }
-  __syncthreads();
-  const int b = blockIdx.x;
-  for (int i = tid; i < a.nchunk * a.E; i += 1024) {
-    const int c = i / a.E, e = i - c * a.E;
-    const int v = a.ccnt[i];
-    if (v) {
-      atomicAdd(&total[e], v);
-      if (c < b) atomicAdd(&before[e], v);
+  const int tid = threadIdx.x, b = blockIdx.x, cols = (a.E + 1) / 2;
+  int wide = 32;  // threads side by side: a power of two
+  while (wide < cols) wide *= 2;
+  const int col = tid & (wide - 1), grp = tid / wide, ngrp = 1024 / wide;
+  const uint32_t *const cc = reinterpret_cast<const uint32_t *>(a.ccnt);
+  // two counts of up to 2^12 in the halves of a word: sums of at most 256 of
+  // them could carry, so they are added apart
+  int t0 = 0, t1 = 0, f0 = 0, f1 = 0;
+  for (int c = grp; c < a.nchunk; c += 8 * ngrp) {
+    uint32_t v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = col < cols && c + u * ngrp < a.nchunk ? cc[(c + u * ngrp) * cols + col] : 0u;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int lo = v[u] & 0xFFFF, hi = v[u] >> 16;
+      t0 += lo;
+      t1 += hi;
+      if (c + u * ngrp < b) {
+        f0 += lo;
+        f1 += hi;
+      }
     }
+  }
+  part[0][2 * tid] = t0;
+  part[0][2 * tid + 1] = t1;
+  part[1][2 * tid] = f0;
+  part[1][2 * tid + 1] = f1;
+  __syncthreads();
+  for (int e = tid; e < a.E; e += 1024) {
+    int t = 0, f = 0;
+    for (int q = 0; q < ngrp; ++q) {
+      t += part[0][2 * wide * q + e];
+      f += part[1][2 * wide * q + e];
+    }
+    total[e] = t;
+    before[e] = f;
   }
   __syncthreads();
   if (tid < 64) {
@@ -410,16 +520,18 @@ int gate_chunks_max(int64_t T) { return T >= 4096 ? 256 : (int)((T + 15) / 16); 
 
 hipError_t launch_gate(const GateArgs &a, hipStream_t s) {
   const dim3 g(a.nchunk), b(1024);
-  auto run = [&](auto f32, auto bf16) {
-    if (a.bf16) hipLaunchKernelGGL(bf16, g, b, 0, s, a);
-    else hipLaunchKernelGGL(f32, g, b, 0, s, a);
-  };
-  if (a.E <= 64) run(k_gate<1, false>, k_gate<1, true>);
-  else if (a.E <= 128) run(k_gate<2, false>, k_gate<2, true>);
-  else if (a.E <= 256) run(k_gate<4, false>, k_gate<4, true>);
-  else run(k_gate<8, false>, k_gate<8, true>);
+  // a lane's logits in one load where every row allows it
+  const int nk = a.E <= 64 ? 1 : a.E <= 128 ? 2 : a.E <= 256 ? 4 : 8, size = (a.bf16 ? 2 : 4) * nk, al = size < 16 ? size : 16;
+  const bool vec = nk > 1 && a.E % nk == 0 && a.ld * (a.bf16 ? 2 : 4) % al == 0 && (uintptr_t)a.logits % al == 0;
+  auto run = [&](auto f32, auto f32v, auto bf, auto bfv) { hipLaunchKernelGGL(a.bf16 ? (vec ? bfv : bf) : (vec ? f32v : f32), g, b, 0, s, a); };
+#define OF(NK) k_gate<NK, false, false>, k_gate<NK, false, true>, k_gate<NK, true, false>, k_gate<NK, true, true>
+  if (nk == 1) run(k_gate<1, false, false>, k_gate<1, false, false>, k_gate<1, true, false>, k_gate<1, true, false>);
+  else if (nk == 2) run(OF(2));
+  else if (nk == 4) run(OF(4));
+  else run(OF(8));
+#undef OF
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.perm) return e;
+  if (e != hipSuccess || !a.perm || a.nchunk == 1) return e;
   hipLaunchKernelGGL(k_gate_place, g, b, 0, s, a);
   return hipGetLastError();
 }

@@ -20,7 +20,7 @@ struct GateArgs {
   int32_t *idx;         // [T,k]
   float *w;             // [T,k]
   int32_t *counts, *offsets, *perm;  // all set, or all null
-  uint16_t *ccnt;       // [nchunk][E] counts of a chunk (more than one chunk)
+  uint16_t *ccnt;       // [nchunk][E, to an even number] counts of a chunk (more than one chunk)
   uint16_t *lrank;      // [T*k] an assignment's rank among its expert's in the chunk
   int32_t chunk, nchunk;
 };

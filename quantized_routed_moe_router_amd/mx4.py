@@ -15,6 +15,7 @@ import torch
 from . import binding as B
 
 _DTYPES = {torch.float32: B.DS4MOE_F32, torch.bfloat16: B.DS4MOE_BF16}
+_BF16 = (torch.bfloat16,)
 _SCORES = {"sqrt_softplus": B.SCORE_SQRT_SOFTPLUS, "sigmoid": B.SCORE_SIGMOID, "softmax": B.SCORE_SOFTMAX}
 
 
@@ -23,25 +24,46 @@ def _need(ok, what: str) -> None:
         raise ValueError(what)
 
 
-def _rows(t: torch.Tensor, what: str, dtypes=tuple(_DTYPES)) -> int:
+# The wrappers run once per layer and token, in the time of a kernel or two:
+# addresses go to the library as plain numbers, and a refusal's text is made
+# only when there is one.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_empty = torch.empty
+_L = B.lib()
+
+
+def _rows(t: torch.Tensor, what: str, dtypes=_DTYPES) -> int:
     """The distance of the rows of a matrix on the GPU whose columns are adjacent."""
-    _need(t.is_cuda and t.dim() == 2, f"{what}: a matrix on the GPU is wanted")
-    _need(t.dtype in dtypes, f"{what}: unsupported type {t.dtype}")
-    _need(t.stride(1) == 1 or t.shape[1] <= 1, f"{what}: columns have to be adjacent")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{what}: a matrix on the GPU is wanted")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: unsupported type {t.dtype}")
+    rows, cols = t.shape
+    d, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{what}: columns have to be adjacent")
+    return d if rows > 1 and d > cols else cols
 
 
 def _flat(t: torch.Tensor, what: str, dtype, shape=None) -> torch.Tensor:
-    _need(t.is_cuda and t.is_contiguous() and t.dtype == dtype, f"{what}: a contiguous {dtype} tensor on the GPU is wanted")
-    _need(shape is None or tuple(t.shape) == tuple(shape), f"{what}: shape {tuple(t.shape)}, not {shape}")
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor on the GPU is wanted")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
     return t
 
 
 def _packed(codes: torch.Tensor, scales: torch.Tensor, what: str, shape=None) -> tuple:
     _flat(codes, what, torch.uint8, None if shape is None else (*shape[:-1], shape[-1] // 2))
+    if codes.shape[-1] % 16:
+        raise ValueError(f"{what}: whole blocks of 32 are wanted")
     _flat(scales, what + " scales", torch.uint8, (*codes.shape[:-1], codes.shape[-1] // 16))
-    _need(codes.shape[-1] % 16 == 0, f"{what}: whole blocks of 32 are wanted")
     return codes, scales
+
+
+def _done(status: int, what: str) -> None:
+    if status:
+        raise B.Ds4MoeError(status, what)
 
 
 class Gate:
@@ -51,14 +73,16 @@ class Gate:
                  group_rank: int = 1, renorm: bool = True, scale: float = 1.0):
         _need(score in _SCORES, f"unknown score {score!r}: one of {sorted(_SCORES)}")
         self.E, self.k = E, k
-        self._gating = {t: B.make_gating(E, k, n_groups, top_groups, group_rank, _SCORES[score], renorm, d, scale)
-                        for t, d in _DTYPES.items()}
-        _need(B.ds4moe_gate_workspace_bytes(self._gating[torch.float32], 1) > 0,
+        gatings = {t: B.make_gating(E, k, n_groups, top_groups, group_rank, _SCORES[score], renorm, d, scale)
+                   for t, d in _DTYPES.items()}
+        _need(B.ds4moe_gate_workspace_bytes(gatings[torch.float32], 1) > 0,
               f"unsupported gate: E={E}, k={k}, {n_groups} groups, {top_groups} kept, rank {group_rank}, scale {scale}")
+        self._gating = {t: ctypes.byref(g) for t, g in gatings.items()}
 
     def _logits(self, logits: torch.Tensor, bias) -> int:
         ld = _rows(logits, "logits")
-        _need(logits.shape[1] == self.E, f"logits: {logits.shape[1]} columns, {self.E} experts")
+        if logits.shape[1] != self.E:
+            raise ValueError(f"logits: {logits.shape[1]} columns, {self.E} experts")
         if bias is not None:
             _flat(bias, "bias", torch.float32, (self.E,))
         return ld
@@ -66,39 +90,45 @@ class Gate:
     def forward(self, logits: torch.Tensor, bias: torch.Tensor | None = None) -> dict:
         """topk_idx [T,k], topk_w [T,k], counts [E], offsets [E+1] and perm [T*k] of logits [T,E]."""
         ld, g, dev = self._logits(logits, bias), self._gating[logits.dtype], logits.device
-        T = logits.shape[0]
-        new = torch.zeros if T == 0 else torch.empty
-        out = {"topk_idx": new((T, self.k), dtype=torch.int32, device=dev),
-               "topk_w": new((T, self.k), dtype=torch.float32, device=dev),
-               "counts": new(self.E, dtype=torch.int32, device=dev),
-               "offsets": new(self.E + 1, dtype=torch.int32, device=dev),
-               "perm": new(T * self.k, dtype=torch.int32, device=dev)}
-        n = B.ds4moe_gate_workspace_bytes(g, T)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        B.ds4moe_gate(g, logits, ld, bias, T, B.make_routing(**out), ws, n, torch.cuda.current_stream(dev))
-        return out
+        T, k, E = logits.shape[0], self.k, self.E
+        if T == 0:
+            return {n: torch.zeros(s, dtype=torch.float32 if n == "topk_w" else torch.int32, device=dev) for n, s in (
+                ("topk_idx", (0, k)), ("topk_w", (0, k)), ("counts", E), ("offsets", E + 1), ("perm", 0))}
+        idx = _empty((T, k), dtype=torch.int32, device=dev)
+        w = _empty((T, k), dtype=torch.float32, device=dev)
+        counts, offsets, perm = _empty(2 * E + 1 + T * k, dtype=torch.int32, device=dev).split((E, E + 1, T * k))
+        n = _L.ds4moe_gate_workspace_bytes(g, T)
+        ws = _empty(n, dtype=torch.uint8, device=dev)
+        _done(_L.ds4moe_gate(g, logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T,
+                             ctypes.byref(B.Routing(idx.data_ptr(), w.data_ptr(), counts.data_ptr(), offsets.data_ptr(),
+                                                    perm.data_ptr(), None)),
+                             ws.data_ptr(), n, _raw_stream(dev.index)), "gate")
+        return {"topk_idx": idx, "topk_w": w, "counts": counts, "offsets": offsets, "perm": perm}
 
     def backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, d_topk_w: torch.Tensor,
                  bias: torch.Tensor | None = None) -> torch.Tensor:
         """Gradient of the logits (in their type) from the gradient of topk_w."""
-        ld, g, dev = self._logits(logits, bias), self._gating[logits.dtype], logits.device
+        ld, dev = self._logits(logits, bias), logits.device
         T = logits.shape[0]
         _flat(topk_idx, "topk_idx", torch.int32, (T, self.k))
         _flat(d_topk_w, "d_topk_w", torch.float32, (T, self.k))
-        out = torch.empty((T, self.E), dtype=logits.dtype, device=dev)
-        B.ds4moe_gate_backward(g, logits, ld, bias, topk_idx, d_topk_w, T, out, self.E, torch.cuda.current_stream(dev))
+        out = _empty((T, self.E), dtype=logits.dtype, device=dev)
+        _done(_L.ds4moe_gate_backward(self._gating[logits.dtype], logits.data_ptr(), ld,
+                                      None if bias is None else bias.data_ptr(), topk_idx.data_ptr(),
+                                      d_topk_w.data_ptr(), T, out.data_ptr(), self.E, _raw_stream(dev.index)),
+              "gate_backward")
         return out
 
 
 def mx4_quantize(x: torch.Tensor) -> tuple:
     """(codes, scales) of a matrix [rows, cols] in fp32 or bf16; columns are filled up with zeros to blocks of 32."""
-    ld = _rows(x, "x")
+    ld, dev = _rows(x, "x"), x.device
     rows, cols = x.shape
     nb = (cols + 31) // 32
-    codes = torch.empty((rows, 16 * nb), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((rows, nb), dtype=torch.uint8, device=x.device)
-    B.ds4moe_mx4_quantize(codes, scales, x, _DTYPES[x.dtype], rows, cols, max(ld, cols),
-                          torch.cuda.current_stream(x.device))
+    codes = _empty((rows, 16 * nb), dtype=torch.uint8, device=dev)
+    scales = _empty((rows, nb), dtype=torch.uint8, device=dev)
+    _done(_L.ds4moe_mx4_quantize(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], rows, cols, ld,
+                                 _raw_stream(dev.index)), "mx4_quantize")
     return codes, scales
 
 
@@ -106,13 +136,15 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int | None =
                    dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """The values of a 4-bit matrix, the first `cols` of each row (all by default)."""
     _packed(codes, scales, "codes")
-    _need(codes.dim() == 2 and dtype in _DTYPES, f"a matrix and fp32 or bf16 are wanted, not {dtype}")
+    if codes.dim() != 2 or dtype not in _DTYPES:
+        raise ValueError(f"a matrix and fp32 or bf16 are wanted, not {dtype}")
     rows, nb = scales.shape
     cols = 32 * nb if cols is None else cols
-    _need((cols + 31) // 32 == nb, f"{cols} columns are not {nb} blocks")
-    out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
-    B.ds4moe_mx4_dequantize(out, _DTYPES[dtype], max(cols, 1), codes, scales, rows, cols,
-                            torch.cuda.current_stream(codes.device))
+    if (cols + 31) // 32 != nb:
+        raise ValueError(f"{cols} columns are not {nb} blocks")
+    out = _empty((rows, cols), dtype=dtype, device=codes.device)
+    _done(_L.ds4moe_mx4_dequantize(out.data_ptr(), _DTYPES[dtype], cols, codes.data_ptr(), scales.data_ptr(), rows,
+                                   cols, _raw_stream(codes.device.index)), "mx4_dequantize")
     return out
 
 
@@ -120,18 +152,23 @@ def mx4_matmul(a: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, a_scale
                y_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """a [M,K] times w [N,K]^T: w in 4-bit form, a bf16, or in 4-bit form with a_scales."""
     _packed(w, w_scales, "w")
-    _need(w.dim() == 2 and y_dtype in _DTYPES, f"w: a matrix is wanted, and an fp32 or bf16 result, not {y_dtype}")
-    N, K = w.shape[0], 2 * w.shape[1]
+    if w.dim() != 2 or y_dtype not in _DTYPES:
+        raise ValueError(f"w: a matrix is wanted, and an fp32 or bf16 result, not {y_dtype}")
+    N, K = w.shape
+    K *= 2
     if a_scales is None:
-        lda, kind = max(_rows(a, "a", (torch.bfloat16,)), K), B.DS4MOE_BF16
-        _need(a.shape[1] == K, f"a: {a.shape[1]} columns, w has {K}")
+        lda, kind, sa = _rows(a, "a", _BF16), B.DS4MOE_BF16, None
+        if a.shape[1] != K:
+            raise ValueError(f"a: {a.shape[1]} columns, w has {K}")
     else:
         _packed(a, a_scales, "a")
-        _need(a.dim() == 2 and 2 * a.shape[1] == K, f"a: shape {tuple(a.shape)}, w has {K} columns")
-        lda, kind = K, B.DS4MOE_MX4
-    y = torch.empty((a.shape[0], N), dtype=y_dtype, device=a.device)
-    B.ds4moe_mx4_matmul(y, _DTYPES[y_dtype], max(N, 1), a, a_scales, kind, lda, w, w_scales, a.shape[0], N, K,
-                        torch.cuda.current_stream(a.device))
+        if a.dim() != 2 or 2 * a.shape[1] != K:
+            raise ValueError(f"a: shape {tuple(a.shape)}, w has {K} columns")
+        lda, kind, sa = K, B.DS4MOE_MX4, a_scales.data_ptr()
+    M, dev = a.shape[0], a.device
+    y = _empty((M, N), dtype=y_dtype, device=dev)
+    _done(_L.ds4moe_mx4_matmul(y.data_ptr(), _DTYPES[y_dtype], N, a.data_ptr(), sa, kind, lda, w.data_ptr(),
+                               w_scales.data_ptr(), M, N, K, _raw_stream(dev.index)), "mx4_matmul")
     return y
 
 
@@ -148,21 +185,26 @@ class Mx4Experts:
         self.gate = _packed(*gate, "gate", (E, I, H))
         self.up = _packed(*up, "up", (E, I, H))
         self.down = _packed(*down, "down", (E, H, I))
-        self._weights = B.make_mx4_weights(*self.gate, *self.up, *self.down)
+        self._dims = ctypes.byref(self.dims)
+        self._weights = ctypes.byref(B.make_mx4_weights(*self.gate, *self.up, *self.down))
 
     def forward(self, x: torch.Tensor, routing: dict) -> torch.Tensor:
         """y [T,H] of bf16 x [T,H]; routing: the dict of Gate.forward or DeviceLayer.route."""
-        ldx = max(_rows(x, "x", (torch.bfloat16,)), self.H)
-        T, dev = x.shape[0], x.device
-        _need(x.shape[1] == self.H, f"x: {x.shape[1]} columns, hidden size {self.H}")
-        r = B.Routing(*(ctypes.c_void_p(_flat(routing[n], n, t, s).data_ptr()) for n, t, s in (
-            ("topk_idx", torch.int32, (T, self.k)), ("topk_w", torch.float32, (T, self.k)),
-            ("counts", torch.int32, (self.E,)), ("offsets", torch.int32, (self.E + 1,)),
-            ("perm", torch.int32, (T * self.k,)))))
-        n = B.ds4moe_mx4_workspace_bytes(self.dims, T)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        y = torch.empty((T, self.H), dtype=self.y_dtype, device=dev)
-        B.ds4moe_mx4_experts(self.dims, self._weights, x, ldx, T, r, y, ws, n, torch.cuda.current_stream(dev))
+        ldx, dev = _rows(x, "x", _BF16), x.device
+        T, H = x.shape
+        if H != self.H:
+            raise ValueError(f"x: {H} columns, hidden size {self.H}")
+        i32, k, E = torch.int32, self.k, self.E
+        r = B.Routing(_flat(routing["topk_idx"], "topk_idx", i32, (T, k)).data_ptr(),
+                      _flat(routing["topk_w"], "topk_w", torch.float32, (T, k)).data_ptr(),
+                      _flat(routing["counts"], "counts", i32, (E,)).data_ptr(),
+                      _flat(routing["offsets"], "offsets", i32, (E + 1,)).data_ptr(),
+                      _flat(routing["perm"], "perm", i32, (T * k,)).data_ptr(), None)
+        n = _L.ds4moe_mx4_workspace_bytes(self._dims, T)
+        ws = _empty(n, dtype=torch.uint8, device=dev)
+        y = _empty((T, H), dtype=self.y_dtype, device=dev)
+        _done(_L.ds4moe_mx4_experts(self._dims, self._weights, x.data_ptr(), ldx, T, ctypes.byref(r), y.data_ptr(),
+                                    ws.data_ptr(), n, _raw_stream(dev.index)), "mx4_experts")
         return y
 
 
