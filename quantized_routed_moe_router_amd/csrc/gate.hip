@@ -139,9 +139,12 @@ __device__ __forceinline__ void load_logits(const GateArgs &a, int64_t t, float 
 // One token by one wave; lane l holds experts NK*l .. NK*l+NK-1.  Lane j < k
 // returns expert and weight of rank j.  xl, kl: wave-private LDS rows of NK*64
 // floats.
+// b: the bias of the lane's experts.  Selection goes by scores of the
+// hardware's exponential and reciprocal (a few ulp); the weights of the k
+// chosen are computed again with the library's.
 template <int NK>
-__device__ __forceinline__ void gate_token(const GateArgs &a, const float (&x)[NK], float *xl, float *kl, int &my_e,
-                                           float &my_w) {
+__device__ __forceinline__ void gate_token(const GateArgs &a, const float (&x)[NK], const float (&b)[NK], float *xl,
+                                           float *kl, int &my_e, float &my_w) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int i = 0; i < NK; ++i) xl[NK * lane + i] = x[i];
@@ -166,14 +169,14 @@ __device__ __forceinline__ void gate_token(const GateArgs &a, const float (&x)[N
   float v[NK];
 #pragma unroll
   for (int i = 0; i < NK; ++i) {
-    const int e = NK * lane + i;
     v[i] = x[i];
-    if (need_scores && x[i] != -INFINITY) {
-      v[i] = soft ? expf(x[i] - mx) * zinv : own_score(x[i], a.score);
-      if (a.bias && e < a.E) {
-        v[i] += a.bias[e];
-        if (v[i] != v[i]) v[i] = -INFINITY;
-      }
+    if (need_scores) {
+      float c;
+      if (soft) c = __expf(x[i] - mx) * zinv;
+      else if (a.score == SC_SIGMOID) c = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
+      else c = own_score(x[i], a.score);
+      c += a.bias ? b[i] : 0.0f;
+      v[i] = x[i] == -INFINITY || c != c ? -INFINITY : c;
     }
   }
   uint64_t stays = ~0ull;
@@ -200,10 +203,12 @@ __device__ __forceinline__ void gate_token(const GateArgs &a, const float (&x)[N
     if (lanes_per > 32) merge_xor(m1, m2, 32);
     // a second best that is masked adds nothing; a group with none live is last
     const float gs = (a.group_rank > 1 && m2 > -INFINITY) ? m1 + m2 : m1;
+    // groups before this one: a larger score, or an equal one and a lower index
+    const uint32_t gk = order_key(gs);
     int rank = 0;
     for (int h = 0; h < a.G; ++h) {
-      const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gs), h * lanes_per));
-      rank += (o > gs || (o == gs && h < g)) ? 1 : 0;
+      const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)gk, h * lanes_per);
+      rank += o > (h < g ? gk - 1 : gk) ? 1 : 0;
     }
     stays = __ballot(g < a.G && j == 0 && rank < a.top_groups);
   }
@@ -217,29 +222,42 @@ __device__ __forceinline__ void gate_token(const GateArgs &a, const float (&x)[N
       if (a.G <= 1 || ((stays >> (g * lanes_per)) & 1)) key[i] = order_key(a.bias ? v[i] : x[i]);
     }
   }
-  // k rounds of the wave's largest key, ties to the lowest lane and slot, that
-  // is to the lowest expert
-  my_e = 0;
+  // The lane's keys in descending order (equal ones as they are), then k
+  // rounds of the wave's largest head: ties to the lowest lane, that is to the
+  // lowest expert; the lane that has it moves its keys up.
+  uint32_t slot[NK];
+#pragma unroll
+  for (int i = 0; i < NK; ++i) slot[i] = i;
+#pragma unroll
+  for (int p = 0; p < NK - 1; ++p)
+#pragma unroll
+    for (int i = 0; i < NK - 1 - p; ++i) {
+      const bool up = key[i + 1] > key[i];
+      const uint32_t k0 = key[i], s0 = slot[i];
+      key[i] = up ? key[i + 1] : k0;
+      key[i + 1] = up ? k0 : key[i + 1];
+      slot[i] = up ? slot[i + 1] : s0;
+      slot[i + 1] = up ? s0 : slot[i + 1];
+    }
+  int mine = 0;  // lane r: rank r's expert
   uint32_t my_key = 0u;
   for (int r = 0; r < a.k; ++r) {
-    uint32_t h = key[0];
-#pragma unroll
-    for (int i = 1; i < NK; ++i) h = h > key[i] ? h : key[i];
-    const uint32_t m = wave_max_u32(h);
-    const int win = __ffsll((unsigned long long)__ballot(h == m)) - 1;
-    int at = 0;
-#pragma unroll
-    for (int i = NK - 1; i >= 0; --i) at = key[i] == m ? i : at;
-    at = __builtin_amdgcn_readlane(at, win);
+    const uint32_t m = wave_max_u32(key[0]);
+    const uint64_t at = __ballot(key[0] == m);
+    const int win = __builtin_ctzll(at);
+    const int e = NK * win + __builtin_amdgcn_readlane((int)slot[0], win);
+    mine = lane == r ? e : mine;
+    my_key = lane == r ? m : my_key;
     if (lane == win) {
 #pragma unroll
-      for (int i = 0; i < NK; ++i) key[i] = i == at ? 0u : key[i];
-    }
-    if (lane == r) {
-      my_e = NK * win + at;
-      my_key = m;
+      for (int i = 0; i < NK - 1; ++i) {
+        key[i] = key[i + 1];
+        slot[i] = slot[i + 1];
+      }
+      key[NK - 1] = 0u;
     }
   }
+  my_e = mine;
   wave_lds_order();
   float s = 0.0f;
   const float l = lane < a.k ? xl[my_e] : -INFINITY;
@@ -295,8 +313,10 @@ __global__ __launch_bounds__(1024) void k_gate(GateArgs a) {
   const int64_t c0 = (int64_t)blockIdx.x * a.chunk;
   const int n = (int)(a.T - c0 < a.chunk ? a.T - c0 : a.chunk);
   const bool perm = a.perm != nullptr;
-  float x[NK];
+  float x[NK], bias[NK];
   if (wave < n) load_logits<NK, BF16, VEC>(a, c0 + wave, x);
+#pragma unroll
+  for (int i = 0; i < NK; ++i) bias[i] = a.bias && NK * lane + i < a.E ? a.bias[NK * lane + i] : 0.0f;
   for (int e = tid; e < a.E; e += 1024) run[e] = 0;
   for (int b0 = 0; b0 < n; b0 += 64) {
     const int nb = n - b0 < 64 ? n - b0 : 64;
@@ -309,7 +329,7 @@ __global__ __launch_bounds__(1024) void k_gate(GateArgs a) {
       // the wave's next token, while this one is worked on
       const int nq = q + GATE_WAVES < nb ? b0 + q + GATE_WAVES : b0 + 64 + wave;
       if (nq < n) load_logits<NK, BF16, VEC>(a, c0 + nq, next);
-      gate_token<NK>(a, x, xl[wave], kl[wave], e, w);
+      gate_token<NK>(a, x, bias, xl[wave], kl[wave], e, w);
 #pragma unroll
       for (int i = 0; i < NK; ++i) x[i] = next[i];
       if (lane < a.k) {

@@ -42,7 +42,9 @@ def _rows(t: torch.Tensor, what: str, dtypes=_DTYPES) -> int:
     d, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{what}: columns have to be adjacent")
-    return d if rows > 1 and d > cols else cols
+    if rows > 1 and d < cols:
+        raise ValueError(f"{what}: rows overlap")
+    return d if rows > 1 else cols
 
 
 def _flat(t: torch.Tensor, what: str, dtype, shape=None) -> torch.Tensor:

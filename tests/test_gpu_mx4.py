@@ -161,6 +161,17 @@ def test_product_of_strange_rows_stays_in_its_rows(kind, M):
     assert (np.abs(y[rows, :N] - av[rows] @ wv.T) <= EPS * (K + 2) * (np.abs(av[rows]) @ np.abs(wv).T)).all()
 
 
+def test_rows_that_overlap_are_refused():
+    """A row repeated by a stride of 0 is not a matrix of rows that lie apart."""
+    q = _q()
+    w = matrix(32, 64, 0)
+    x = torch.ones(1, 64, dtype=torch.bfloat16, device="cuda").expand(4, 64)
+    for call in (lambda: q.mx4_quantize(x), lambda: q.mx4_matmul(x, dev(w[0]), dev(w[1])), lambda: q.Gate(64, 2).forward(x),
+                 lambda: q.mx4_quantize(torch.ones(64, 4, device="cuda").t())):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_product_without_rows():
     q = _q()
     w = matrix(32, 64, 0)
