@@ -134,12 +134,26 @@ __device__ __forceinline__ void small_dot(f4 (&acc)[NM], const Rows<NM> &R, int6
   }
 }
 
+// column r of a product plus columns r + D, ... r + (PL - 1) D
+template <int D, int PL>
+__device__ __forceinline__ f4 add_columns(f4 v) {
+  f4 s = v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int u = __float_as_int(v[i]);
+    if (PL > 1) s[i] += __int_as_float(__builtin_amdgcn_update_dpp(0, u, 0x100 + D, 0xF, 0xF, true));
+    if (PL > 2) s[i] += __int_as_float(__builtin_amdgcn_update_dpp(0, u, 0x100 + 2 * D, 0xF, 0xF, true));
+  }
+  return s;
+}
+
 // acc += 16 weight rows times one activation row over all of k.  lds: PL * KT * 256 bytes of this wave.
 // WIDE: K a multiple of 512, the scales of 4 tiles are loaded at once.
 template <int KT, int PL, bool WIDE>
 __device__ __forceinline__ void one_dot(f4 &acc, const Rows<1> &R, int64_t K, const uint8_t *x, int64_t plane, char *lds) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int nblk = (int)(K / 32), nt = (nblk + 3) / 4;
+  const uint32_t lw = (uint32_t)(lane >> 2) * (uint32_t)(K / 2);  // rows come in whole groups of 16
   for (int c = 0; c < nt; c += KT) {
     __builtin_amdgcn_s_waitcnt(0xC07F);
 #pragma unroll
@@ -155,9 +169,9 @@ __device__ __forceinline__ void one_dot(f4 &acc, const Rows<1> &R, int64_t K, co
     uint32_t sc[KT / 4][4];
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-      const int blk = (c + t) * 4 + g, b = blk < nblk ? blk : nblk - 1;
-      w[t] = load16(R.w[0] + (R.wo[0] + (uint32_t)b * 16u));
-      if (!WIDE) sc[t / 4][t % 4] = R.s[0][R.so[0] + (uint32_t)b];
+      const int blk = (c + t) * 4 + (lane & 3), sb = (c + t) * 4 + g;
+      w[t] = load16(R.w[0] + (lw + (uint32_t)(blk < nblk ? blk : nblk - 1) * 16u));
+      if (!WIDE) sc[t / 4][t % 4] = R.s[0][R.so[0] + (uint32_t)(sb < nblk ? sb : nblk - 1)];
     }
     if (WIDE)
 #pragma unroll
@@ -174,18 +188,17 @@ __device__ __forceinline__ void one_dot(f4 &acc, const Rows<1> &R, int64_t K, co
       const bool out = !WIDE && (c + t) * 4 + g >= nblk;
       const uint32_t sb = sc[t / 4][t % 4];
       const float sf = WIDE ? scale_float((sb >> (8 * g)) & 255u) : scale_float(out ? 127 : sb);
+      const u4 wl = to_lanes(w[t]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bf8 a = codes_bf16(out ? 0 : w[t][j], sf);
-#pragma unroll
-        for (int q = 0; q < PL; ++q) {
-          bf8 x8 = zero_bf8();
-          if (r == 0) x8 = *reinterpret_cast<const bf8 *>(lds + ((q * KT + t) * 16 + 4 * g + j) * 16);
-          acc = mfma_bf16(a, x8, acc);
-        }
+        const bf8 a = codes_bf16(out ? 0 : wl[j], sf);
+        bf8 x8 = zero_bf8();  // column q: term q
+        if (r < PL) x8 = *reinterpret_cast<const bf8 *>(lds + ((r * KT + t) * 16 + 4 * g + j) * 16);
+        acc = mfma_bf16(a, x8, acc);
       }
     }
   }
+  acc = add_columns<1, PL>(acc);
 }
 
 // the workgroup's sum of acc, wave by wave, in wave 0
@@ -211,7 +224,9 @@ __device__ __forceinline__ void join_waves(f4 *part, f4 (&acc)[NM]) {
 // alternate, and each stages its own part; with SPL = 1 every wave has row
 // tiles of its own over all of k, and nothing to wait for.  Where a row's
 // scales allow it (WIDE: their number a multiple of 4 KT) a lane loads those
-// of a step at once and picks its block's.  xs: PL * 4 rows of nti * 256
+// of a step at once and picks its block's.  The terms of the activations take
+// columns of the matrix instruction that the few tokens leave free: column r
+// is term r / 4 of token r % 4, and the terms' columns are added at the end.  xs: PL * 4 rows of nti * 256
 // bytes of LDS, this wave's or (SPL = 1) the workgroup's.
 template <int KT, int SPL>
 inline __host__ __device__ int few_tiles(int64_t K) {  // staged tiles, whole steps
@@ -251,7 +266,7 @@ template <int NM, int KT, int PL, int SPL, bool WIDE, typename B, typename D>
 __device__ __forceinline__ void stream_rows(int64_t K, int wave, int nrt, int n, const char *xs, B base, D done) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int nblk = (int)(K / 32), nt = (nblk + 3) / 4, nti = few_tiles<KT, SPL>(K), nch = nti / KT, steps = nrt * nch;
-  const uint32_t wo = (uint32_t)r * (uint32_t)(K / 2), so = (uint32_t)r * (uint32_t)(K / 32);
+  const uint32_t wo = (uint32_t)(lane >> 2) * (uint32_t)(K / 2), so = (uint32_t)r * (uint32_t)(K / 32);
   int rl = 0, cl = 0;  // row tile and step of the next loads
   auto load = [&](Ahead<NM, KT, WIDE> &a) {
     const int t0 = SPL == 1 ? KT * cl : KT * (wave + SW * cl);
@@ -261,9 +276,10 @@ __device__ __forceinline__ void stream_rows(int64_t K, int wave, int nrt, int n,
       base(i, rl, w, s);
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
-        const int blk = (t0 + t) * 4 + g, b = blk < nblk ? blk : nblk - 1;
+        const int blk = (t0 + t) * 4 + (lane & 3), b = blk < nblk ? blk : nblk - 1;
         a.w[i][t] = load16(w + (wo + (uint32_t)b * 16u));
-        if (!WIDE) a.s[i][t] = s[so + (uint32_t)b];
+        const int sb = (t0 + t) * 4 + g;
+        if (!WIDE) a.s[i][t] = s[so + (uint32_t)(sb < nblk ? sb : nblk - 1)];
       }
       if (WIDE) load_scales<KT>(s + (so + (uint32_t)(t0 * 4 < nblk ? t0 * 4 : 0)), a.s[i]);
     }
@@ -286,24 +302,21 @@ __device__ __forceinline__ void stream_rows(int64_t K, int wave, int nrt, int n,
       float sf[NM];
 #pragma unroll
       for (int i = 0; i < NM; ++i) sf[i] = WIDE ? scale_float((a.s[i][t] >> (8 * g)) & 255u) : scale_float(out ? 127 : a.s[i][t]);
+      u4 wl[NM];
+#pragma unroll
+      for (int i = 0; i < NM; ++i) wl[i] = to_lanes(a.w[i][t]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        bf8 x[PL];
+        bf8 x = zero_bf8();
+        if (r < 4 * PL && (r & 3) < n) x = *reinterpret_cast<const bf8 *>(xs + (r * nti + c * KT + t) * 256 + (4 * g + j) * 16);
 #pragma unroll
-        for (int q = 0; q < PL; ++q) {
-          x[q] = zero_bf8();
-          if (r < n) x[q] = *reinterpret_cast<const bf8 *>(xs + ((q * 4 + r) * nti + c * KT + t) * 256 + (4 * g + j) * 16);
-        }
-#pragma unroll
-        for (int i = 0; i < NM; ++i) {
-          const bf8 w = codes_bf16(out ? 0 : a.w[i][t][j], sf[i]);
-#pragma unroll
-          for (int q = 0; q < PL; ++q) acc[i] = mfma_bf16(w, x[q], acc[i]);
-        }
+        for (int i = 0; i < NM; ++i) acc[i] = mfma_bf16(codes_bf16(out ? 0 : wl[i][j], sf[i]), x, acc[i]);
       }
     }
     if (++c == nch) {
       c = 0;
+#pragma unroll
+      for (int i = 0; i < NM; ++i) acc[i] = add_columns<4, PL>(acc[i]);
       done(rt++, acc);
     }
   };
