@@ -8,6 +8,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -35,16 +37,27 @@ def sources():
 
 
 def build(verbose: bool = False) -> str:
+    """Compile the sources side by side (each is a whole device program) and link them."""
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, *sources(), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    msgs = [l for l in (r.stdout + r.stderr).splitlines() if "packed-fp32-ops" not in l and l.strip()]
-    if r.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
-    if verbose and msgs:
-        print("\n".join(msgs))
+    flags = [f for f in FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory(dir=PKG, prefix="_build") as objs:
+        def compile_one(src):
+            obj = os.path.join(objs, os.path.basename(src) + ".o")
+            cmd = [HIPCC, *flags, "-c", src, "-o", obj]
+            return cmd, obj, subprocess.run(cmd, capture_output=True, text=True)
+
+        with ThreadPoolExecutor(max_workers=8) as pool:
+            done = list(pool.map(compile_one, sources()))
+        link = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *(obj for _, obj, _ in done), "-o", tmp]
+        for cmd, r in [(c, r) for c, _, r in done] + [(link, None)]:
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            r = r if r is not None else subprocess.run(cmd, capture_output=True, text=True)
+            msgs = [l for l in (r.stdout + r.stderr).splitlines() if "packed-fp32-ops" not in l and l.strip()]
+            if r.returncode != 0:
+                raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
+            if verbose and msgs:
+                print("\n".join(msgs))
     os.replace(tmp, LIB)
     return LIB
 

@@ -90,11 +90,18 @@ int64_t mx4_max_tiles(int64_t assignments, int64_t experts);
 hipError_t launch_mx4_gemm_experts(const Mx4Experts &p, hipStream_t s);  // h and ya; more than a few tokens
 hipError_t launch_mx4_gemm(const Mx4Product &p, hipStream_t s);          // bf16 activations, many rows
 hipError_t launch_mx4_gemm4(const Mx4Product &p, hipStream_t s);         // 4-bit activations, many rows
-constexpr int MX4_FEW = 16;  // tokens (and rows of a product) that the kernels for few rows take
+constexpr int MX4_FEW = 16;       // tokens that the experts' kernels for few of them take
+// Rows of a product that its kernels for few take: bf16 activations of 64 rows
+// (N = K = 4096) 23 us there, 25 in the tiled kernel; 4-bit ones of 64 rows
+// 16 us, 10 in the tiled kernel, of 32 rows 10 in both.
+constexpr int MX4_FEW_ROWS = 64, MX4_FEW_ROWS4 = 32;
 constexpr int MX4_ONE = 4;   // tokens whose down projection adds the experts up itself
 // bf16 terms that the SwiGLU intermediate is held in: 24 bits for an fp32
 // result; for a bf16 one 16 bits where the second term costs nothing
-inline int mx4_h_planes(bool y_bf16, int64_t T) { return !y_bf16 ? 3 : T <= MX4_FEW ? 2 : 1; }
+inline int mx4_h_planes(bool y_bf16, bool few) { return !y_bf16 ? 3 : few ? 2 : 1; }
+// Whether a call takes the experts' kernels for few tokens: few each, that is
+// (16 tokens with 2 of 8 experts: 103 us there, 44 in the tiled kernels).
+inline bool mx4_few(int64_t T, int64_t k, int64_t E) { return T <= MX4_ONE || (T <= MX4_FEW && T * k <= 2 * E); }
 hipError_t launch_mx4_product_few(const Mx4Product &p, hipStream_t s);
 hipError_t launch_mx4_experts_few(const Mx4Experts &p, hipStream_t s);  // h, then ya, or y for up to MX4_ONE tokens
 hipError_t launch_mx4_experts(const Mx4Experts &p, hipStream_t s);

@@ -207,12 +207,12 @@ hipError_t launch_mx4_dequantize(void *dst, bool bf16, int64_t ld, const uint8_t
 }
 
 hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t s) {
-  if (p.M <= MX4_FEW) return launch_mx4_product_few(p, s);
+  if (p.M <= (p.a_scales ? MX4_FEW_ROWS4 : MX4_FEW_ROWS)) return launch_mx4_product_few(p, s);
   return p.a_scales ? launch_mx4_gemm4(p, s) : launch_mx4_gemm(p, s);
 }
 
 hipError_t launch_mx4_experts(const Mx4Experts &p, hipStream_t s) {
-  const hipError_t e = p.T <= MX4_FEW ? launch_mx4_experts_few(p, s) : launch_mx4_gemm_experts(p, s);
+  const hipError_t e = mx4_few(p.T, p.k, p.E) ? launch_mx4_experts_few(p, s) : launch_mx4_gemm_experts(p, s);
   if (e != hipSuccess || p.T <= MX4_ONE) return e;
   const dim3 g(p.T, (p.H / 4 + 255) / 256), b(256);
   if (p.y_bf16) hipLaunchKernelGGL((k_mx4_combine<true>), g, b, 0, s, p);

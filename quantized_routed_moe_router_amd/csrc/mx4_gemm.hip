@@ -2,7 +2,7 @@
 // the routed experts' gate/up and down products and the dense product.
 //
 // A workgroup of four waves takes up to 96 activation rows (one expert's
-// tokens, or rows of a matrix) and 256 weight rows.  Each wave owns 64 weight
+// tokens, or rows of a matrix) and 64 G weight rows.  Each wave owns 16 G weight
 // rows: their codes go from memory to its registers, 16 bytes (one block of
 // 32, one scale) per lane, and become exact bf16 operands there by one
 // conversion instruction per pair, so a weight is read and converted once per
@@ -23,31 +23,32 @@ namespace {
 
 constexpr int GM_ROWS = 96;              // activation rows of a tile
 constexpr int GM_STAGE = GM_ROWS * 256;  // bytes of one stage: 128 bf16 columns
-constexpr int GM_WROWS = 256;            // weight rows of a workgroup
 
 // what a workgroup multiplies
+template <int G>
 struct GemmTile {
-  const uint8_t *w[4];         // codes of the wave's four groups of 16 weight rows (wave-uniform)
-  uint32_t wo[4];              // the row in them that this lane loads
-  const uint8_t *srow;         // scales of row l of the 64
+  const uint8_t *w[G];         // codes of the wave's groups of 16 weight rows (wave-uniform)
+  uint32_t wo[G];              // the row in them that this lane loads
+  const uint8_t *srow;         // scales of row l of the 16 G
   int64_t K;
   int nblk, nst;               // blocks of 32 and stages of 128 columns
 };
 
+template <int G>
 struct Codes {
-  u4 c[4];
+  u4 c[G];
 };
 
 // EVEN: K is a multiple of 128, and no stage ends early
-template <bool EVEN>
-__device__ __forceinline__ void load_codes(const GemmTile &t, int st, Codes &c) {
+template <int G, bool EVEN>
+__device__ __forceinline__ void load_codes(const GemmTile<G> &t, int st, Codes<G> &c) {
   const int blk = 4 * st + (threadIdx.x & 3);
   if (EVEN || 4 * st + 4 <= t.nblk) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c.c[i] = load16(t.w[i] + (t.wo[i] + (uint32_t)blk * 16u));
+    for (int i = 0; i < G; ++i) c.c[i] = load16(t.w[i] + (t.wo[i] + (uint32_t)blk * 16u));
   } else {  // the last stage of a length that is no multiple of 128: zeros past the end
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < G; ++i) {
       c.c[i] = u4{0, 0, 0, 0};
       if (blk < t.nblk) c.c[i] = load16(t.w[i] + (t.wo[i] + (uint32_t)blk * 16u));
     }
@@ -59,48 +60,53 @@ __device__ __forceinline__ void load_codes(const GemmTile &t, int st, Codes &c) 
 template <int MT, bool EVEN>
 __device__ __forceinline__ void load_rows(const uint8_t *const *rows, int64_t K, int st, char *lds) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = (lane & 15) ^ place16(4 * wave + (lane >> 4));
+  const int64_t k = (int64_t)st * 128 + c * 8;
+  char *const to = lds + 4 * wave * 256;
+  if (EVEN || (int64_t)st * 128 + 128 <= K) {
+#pragma unroll
+    for (int q = 0; q < MT; ++q) load_lds16(rows[q] + k * 2, to + 16 * q * 256);
+    return;
+  }
 #pragma unroll
   for (int q = 0; q < MT; ++q) {
-    const int c = (lane & 15) ^ place16(4 * wave + (lane >> 4));
-    const int64_t k = (int64_t)st * 128 + c * 8;
-    char *to = lds + (16 * q + 4 * wave) * 256;
-    if (EVEN || (int64_t)st * 128 + 128 <= K || k < K) load_lds16(rows[q] + k * 2, to);
-    else *reinterpret_cast<u4 *>(to + lane * 16) = u4{0, 0, 0, 0};
+    if (k < K) load_lds16(rows[q] + k * 2, to + 16 * q * 256);
+    else *reinterpret_cast<u4 *>(to + 16 * q * 256 + lane * 16) = u4{0, 0, 0, 0};
   }
 }
 
 // acc[i][m] += weight rows of group i times activation rows 16 m .. over the
 // K columns.  lds: three stages, then 1 KB of scales per wave.
-template <int MT, bool EVEN>
-__device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *const *rows, char *lds, f4 (&acc)[4][MT]) {
+template <int G, int MT, bool EVEN>
+__device__ __forceinline__ void gemm_columns(const GemmTile<G> &t, const uint8_t *const *rows, char *lds, f4 (&acc)[G][MT]) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   char *const lsc = lds + 3 * GM_STAGE + wave * 1024;
   const int last = t.nst - 1;
-  // scales of 512 columns of the wave's 64 rows, one row per lane, turned in
+  // scales of 512 columns of the wave's 16 G rows, one row per lane, turned in
   // LDS into one dword per lane and group: byte s is the lane's block of stage s
   u4 sc;
-  uint32_t sd[4];
+  uint32_t sd[G];
   auto turn_scales = [&]() {
     *reinterpret_cast<u4 *>(lsc + lane * 16) = transpose_bytes(sc);
     lds_order();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sd[i] = *reinterpret_cast<const uint32_t *>(lsc + (16 * i + r) * 16 + 4 * g);
+    for (int i = 0; i < G; ++i) sd[i] = *reinterpret_cast<const uint32_t *>(lsc + (16 * i + r) * 16 + 4 * g);
     lds_order();
   };
-  Codes c0, c1, c2, c3;  // stages s % 4, turned to the lanes' order one stage before they are used
-  auto turn_codes = [&](Codes &c) {
+  Codes<G> c0, c1, c2, c3;  // stages s % 4, turned to the lanes' order one stage before they are used
+  auto turn_codes = [&](Codes<G> &c) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c.c[i] = to_lanes(c.c[i]);
+    for (int i = 0; i < G; ++i) c.c[i] = to_lanes(c.c[i]);
   };
   sc = scales16(t.srow, 0, t.nblk);
   load_rows<MT, EVEN>(rows, t.K, 0, lds);
   asm volatile("" ::: "memory");  // the waits count the loads issued after these
-  load_codes<EVEN>(t, 0, c0);
-  load_codes<EVEN>(t, min(1, last), c1);
+  load_codes<G, EVEN>(t, 0, c0);
+  load_codes<G, EVEN>(t, min(1, last), c1);
   load_rows<MT, EVEN>(rows, t.K, min(1, last), lds + GM_STAGE);
   turn_codes(c0);
   turn_scales();
-  wait_vm<4 + MT>();
+  wait_vm<G + MT>();
   barrier_keep_loads();
   int s = 0;
   const char *x = lds;             // this stage's buffer
@@ -110,13 +116,13 @@ __device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *c
   // two stages (adjacent halves of 128-byte lines), then the products.  Past
   // the end the last stage is loaded again: with no condition on the loads
   // every wait is for a fixed number of them.
-  auto stage = [&](auto S, const Codes &now, Codes &next, Codes &l0, Codes &l1) {
+  auto stage = [&](auto S, const Codes<G> &now, Codes<G> &next, Codes<G> &l0, Codes<G> &l1) {
     if (S == 0) sc = scales16(t.srow, min(s + 4, last / 4 * 4) * 4, t.nblk);
     load_rows<MT, EVEN>(rows, t.K, min(s + 2, last), in);
     asm volatile("" ::: "memory");
     if (S % 2 == 0) {
-      load_codes<EVEN>(t, min(s + 2, last), l0);
-      load_codes<EVEN>(t, min(s + 3, last), l1);
+      load_codes<G, EVEN>(t, min(s + 2, last), l0);
+      load_codes<G, EVEN>(t, min(s + 3, last), l1);
       asm volatile("" ::: "memory");
     }
 #pragma unroll
@@ -126,7 +132,7 @@ __device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *c
       for (int m = 0; m < MT; ++m)
         b[m] = *reinterpret_cast<const bf8 *>(x + (16 * m + r) * 256 + (((4 * g + j) ^ place16(r)) << 4));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < G; ++i) {
         const bf8 a = codes_bf16(now.c[i][j], scale_float((sd[i] >> (8 * S)) & 255u));
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[i][m] = mfma_bf16(a, b[m], acc[i][m]);
@@ -136,7 +142,7 @@ __device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *c
     turn_codes(next);
     // the next stage's rows have landed; on their way may be the rows after
     // them and one pair of stages' codes
-    wait_vm<8 + MT>();
+    wait_vm<2 * G + MT>();
     barrier_keep_loads();
     x = x + GM_STAGE == end ? lds : x + GM_STAGE;
     in = in + GM_STAGE == end ? lds : in + GM_STAGE;
@@ -153,43 +159,45 @@ __device__ __forceinline__ void gemm_columns(const GemmTile &t, const uint8_t *c
 }
 
 // ... over `planes` terms of the activations, plane bytes apart
-template <int MT, bool EVEN>
-__device__ __forceinline__ void gemm_tile(const GemmTile &t, const uint8_t **rows, int planes, int64_t plane, char *lds,
-                                          f4 (&acc)[4][MT]) {
+template <int G, int MT, bool EVEN>
+__device__ __forceinline__ void gemm_tile(const GemmTile<G> &t, const uint8_t **rows, int planes, int64_t plane, char *lds,
+                                          f4 (&acc)[G][MT]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < G; ++i)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[i][m] = f4{0, 0, 0, 0};
   for (int q = 0; q < planes; ++q) {
-    gemm_columns<MT, EVEN>(t, rows, lds, acc);
+    gemm_columns<G, MT, EVEN>(t, rows, lds, acc);
 #pragma unroll
     for (int m = 0; m < MT; ++m) rows[m] += plane;
   }
 }
 
 // group i of the wave: 16 rows of the matrix (w, s) from row0 on
-__device__ __forceinline__ void weight_rows(GemmTile &t, int i, const uint8_t *w, const uint8_t *s, int64_t row0, int64_t N) {
+template <int G>
+__device__ __forceinline__ void weight_rows(GemmTile<G> &t, int i, const uint8_t *w, const uint8_t *s, int64_t row0, int64_t N) {
   if (row0 >= N) row0 = 0;  // a group past the end: read, never stored
   t.w[i] = w + row0 * (t.K / 2);
   const int lane = threadIdx.x & 63, c = lane >> 2, r = lane & 15;  // rows of this lane's codes and scales
   t.wo[i] = (uint32_t)(row0 + c < N ? c : N - 1 - row0) * (uint32_t)(t.K / 2);
-  if (lane >> 4 == i) t.srow = s + (row0 + r < N ? row0 + r : N - 1) * (t.K / 32);
+  if ((lane >> 4) % G == i) t.srow = s + (row0 + r < N ? row0 + r : N - 1) * (t.K / 32);
 }
 
-template <int MT, int PL, bool EVEN>
+template <int G, int MT, int PL, bool EVEN>
 __device__ __forceinline__ void gateup_tile(const Mx4Experts &p, const Mx4Tile &tl, int nb, char *lds) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
   const int A = p.T * p.k;
-  GemmTile t;
+  GemmTile<G> t;
   t.K = p.H;
   t.nblk = p.H / 32;
   t.nst = (t.nblk + 3) / 4;
-  const int n0 = nb * (GM_WROWS / 2) + wave * 32;
+  const int n0 = nb * 32 * G + wave * 8 * G;
   const int64_t eo = (int64_t)tl.e * p.I;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint8_t *w = (i < 2 ? p.gate : p.up) + eo * (p.H / 2), *s = (i < 2 ? p.gate_s : p.up_s) + eo * (p.H / 32);
-    weight_rows(t, i, w, s, n0 + 16 * (i & 1), p.I);
+  for (int i = 0; i < G; ++i) {  // gate, then up
+    const bool up = i >= G / 2;
+    const uint8_t *w = (up ? p.up : p.gate) + eo * (p.H / 2), *s = (up ? p.up_s : p.gate_s) + eo * (p.H / 32);
+    weight_rows(t, i, w, s, n0 + 16 * (i % (G / 2)), p.I);
   }
   const uint8_t *rows[MT];
 #pragma unroll
@@ -199,35 +207,35 @@ __device__ __forceinline__ void gateup_tile(const Mx4Experts &p, const Mx4Tile &
     a = a < 0 ? 0 : a >= A ? A - 1 : a;
     rows[q] = (const uint8_t *)(p.x + (int64_t)(a / p.k) * p.ldx);
   }
-  f4 acc[4][MT];
-  gemm_tile<MT, EVEN>(t, rows, 1, 0, lds, acc);
+  f4 acc[G][MT];
+  gemm_tile<G, MT, EVEN>(t, rows, 1, 0, lds, acc);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = 16 * m + r;
     if (row >= tl.n) continue;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < G / 2; ++i) {
       const int n = n0 + 16 * i + 4 * g;
       if (n >= p.I) continue;
-      const f4 u = acc[i][m], v = acc[2 + i][m];
+      const f4 u = acc[i][m], v = acc[G / 2 + i][m];
       store_terms<PL>(p.h + (int64_t)(tl.p0 + row) * p.I + n, (int64_t)A * p.I, silu_mul(u[0], v[0]), silu_mul(u[1], v[1]),
                       silu_mul(u[2], v[2]), silu_mul(u[3], v[3]));
     }
   }
 }
 
-template <int MT, int PL, bool EVEN>
+template <int G, int MT, int PL, bool EVEN>
 __device__ __forceinline__ void down_tile(const Mx4Experts &p, const Mx4Tile &tl, int nb, char *lds) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
   const int A = p.T * p.k;
-  GemmTile t;
+  GemmTile<G> t;
   t.K = p.I;
   t.nblk = p.I / 32;
   t.nst = (t.nblk + 3) / 4;
-  const int n0 = nb * GM_WROWS + wave * 64;
+  const int n0 = nb * 64 * G + wave * 16 * G;
   const int64_t eo = (int64_t)tl.e * p.H;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < G; ++i)
     weight_rows(t, i, p.down + eo * (p.I / 2), p.down_s + eo * (p.I / 32), n0 + 16 * i, p.H);
   const uint8_t *rows[MT];
 #pragma unroll
@@ -235,8 +243,8 @@ __device__ __forceinline__ void down_tile(const Mx4Experts &p, const Mx4Tile &tl
     const int row = 16 * q + 4 * wave + (lane >> 4);
     rows[q] = (const uint8_t *)(p.h + (int64_t)(tl.p0 + (row < tl.n ? row : 0)) * p.I);
   }
-  f4 acc[4][MT];
-  gemm_tile<MT, EVEN>(t, rows, PL, (int64_t)A * p.I * 2, lds, acc);
+  f4 acc[G][MT];
+  gemm_tile<G, MT, EVEN>(t, rows, PL, (int64_t)A * p.I * 2, lds, acc);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = 16 * m + r;
@@ -244,7 +252,7 @@ __device__ __forceinline__ void down_tile(const Mx4Experts &p, const Mx4Tile &tl
     const int a = p.perm[tl.p0 + row];
     if (a < 0 || a >= A) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < G; ++i) {
       const int n = n0 + 16 * i + 4 * g;
       if (n < p.H) *reinterpret_cast<f4 *>(p.ya + (int64_t)a * p.H + n) = acc[i][m];
     }
@@ -263,15 +271,18 @@ __device__ __forceinline__ void down_tile(const Mx4Experts &p, const Mx4Tile &tl
     default: CALL(6); break;    \
   }
 
-template <int PL, bool DOWN, bool EVEN>
+template <int G, int PL, bool DOWN, bool EVEN>
 __global__ __launch_bounds__(256, 2) void k_mx4_gemm_experts(Mx4Experts p, int nrows) {
   __shared__ __attribute__((aligned(16))) char lds[3 * GM_STAGE + 4096];
   int ti, nb;
   if (!tile_of(blockIdx.x, p.tiles->count, nrows, ti, nb)) return;
   const Mx4Tile tl = p.tiles->tile[ti];
-#define CALL(MT) (DOWN ? down_tile<MT, PL, EVEN>(p, tl, nb, lds) : gateup_tile<MT, PL, EVEN>(p, tl, nb, lds))
-  BY_GROUPS(tl.n, CALL)
-#undef CALL
+#define UP(MT) gateup_tile<G, MT, PL, EVEN>(p, tl, nb, lds)
+#define DN(MT) down_tile<G, MT, PL, EVEN>(p, tl, nb, lds)
+  if constexpr (DOWN) BY_GROUPS(tl.n, DN)
+  else BY_GROUPS(tl.n, UP)
+#undef UP
+#undef DN
 }
 
 // The list of tiles, experts ascending: one workgroup, a thread per expert.
@@ -302,40 +313,44 @@ __global__ __launch_bounds__(512) void k_mx4_plan(Mx4Experts p) {
   }
 }
 
-template <int MT, bool YBF, bool EVEN>
+template <int G, int MT, bool YBF, bool EVEN>
 __device__ __forceinline__ void product_tile(const Mx4Product &p, int64_t m0, int64_t n, int nb, char *lds) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-  GemmTile t;
+  GemmTile<G> t;
   t.K = p.K;
   t.nblk = (int)(p.K / 32);
   t.nst = (t.nblk + 3) / 4;
-  const int64_t n0 = (int64_t)nb * GM_WROWS + wave * 64;
+  const int64_t n0 = (int64_t)nb * 64 * G + wave * 16 * G;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) weight_rows(t, i, p.w, p.ws, n0 + 16 * i, p.N);
+  for (int i = 0; i < G; ++i) weight_rows(t, i, p.w, p.ws, n0 + 16 * i, p.N);
   const uint8_t *rows[MT];
 #pragma unroll
   for (int q = 0; q < MT; ++q) {
     const int64_t row = 16 * q + 4 * wave + (lane >> 4);
     rows[q] = (const uint8_t *)p.a + (m0 + (row < n ? row : 0)) * p.lda * 2;
   }
-  f4 acc[4][MT];
-  gemm_tile<MT, EVEN>(t, rows, 1, 0, lds, acc);
+  f4 acc[G][MT];
+  gemm_tile<G, MT, EVEN>(t, rows, 1, 0, lds, acc);
+  const bool wide = wide_rows(p);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = 16 * m + r;
     if (row >= n) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) store_row4<YBF>(p, m0 + row, n0 + 16 * i + 4 * g, acc[i][m]);
+    for (int i = 0; i < G; ++i) {
+      const float v[4] = {acc[i][m][0], acc[i][m][1], acc[i][m][2], acc[i][m][3]};
+      store_cols<YBF, 4>(p, wide, m0 + row, n0 + 16 * i + 4 * g, v);
+    }
   }
 }
 
-template <bool YBF, bool EVEN>
+template <int G, bool YBF, bool EVEN>
 __global__ __launch_bounds__(256, 2) void k_mx4_gemm(Mx4Product p, int mtiles, int nrows) {
   __shared__ __attribute__((aligned(16))) char lds[3 * GM_STAGE + 4096];
   int ti, nb;
   if (!tile_of(blockIdx.x, mtiles, nrows, ti, nb)) return;
   const int64_t m0 = (int64_t)ti * GM_ROWS, n = p.M - m0 < GM_ROWS ? p.M - m0 : GM_ROWS;
-#define CALL(MT) product_tile<MT, YBF, EVEN>(p, m0, n, nb, lds)
+#define CALL(MT) product_tile<G, MT, YBF, EVEN>(p, m0, n, nb, lds)
   BY_GROUPS((int)n, CALL)
 #undef CALL
 }
@@ -344,23 +359,32 @@ __global__ __launch_bounds__(256, 2) void k_mx4_gemm(Mx4Product p, int mtiles, i
 
 int64_t mx4_max_tiles(int64_t A, int64_t E) { return A / GM_ROWS + (A < E ? A : E); }
 
+// Weight rows per wave: 64, or 32 (gate and up together) or 16 where these
+// would leave CUs without a workgroup.  The number of tiles is known on the
+// device alone; every expert with tokens has one at least.
 hipError_t launch_mx4_gemm_experts(const Mx4Experts &p, hipStream_t s) {
-  const int nu = (p.I + GM_WROWS / 2 - 1) / (GM_WROWS / 2), nd = (p.H + GM_WROWS - 1) / GM_WROWS;
-  const dim3 b(256), gu(tile_grid(p.max_tiles, nu)), gd(tile_grid(p.max_tiles, nd));
+  auto rows = [&](int n, int per) { return (n + per - 1) / per; };
+  const int64_t A = (int64_t)p.T * p.k, used = A < p.E ? A : p.E, tiles = A / GM_ROWS > used ? A / GM_ROWS : used;
+  const bool gu_small = tiles * rows(p.I, 128) < 256, dn_small = tiles * rows(p.H, 256) < 256;
   hipLaunchKernelGGL(k_mx4_plan, dim3(1), dim3(512), 0, s, p);
-  auto up = p.y_bf16 ? (p.H % 128 ? k_mx4_gemm_experts<1, false, false> : k_mx4_gemm_experts<1, false, true>)
-                     : (p.H % 128 ? k_mx4_gemm_experts<3, false, false> : k_mx4_gemm_experts<3, false, true>);
-  auto down = p.y_bf16 ? (p.I % 128 ? k_mx4_gemm_experts<1, true, false> : k_mx4_gemm_experts<1, true, true>)
-                       : (p.I % 128 ? k_mx4_gemm_experts<3, true, false> : k_mx4_gemm_experts<3, true, true>);
-  hipLaunchKernelGGL(up, gu, b, 0, s, p, nu);
-  hipLaunchKernelGGL(down, gd, b, 0, s, p, nd);
+  const bool hu = p.H % 128 != 0, iu = p.I % 128 != 0;
+#define PICK(G, PL, D, U) (U ? k_mx4_gemm_experts<G, PL, D, false> : k_mx4_gemm_experts<G, PL, D, true>)
+  auto up = p.y_bf16 ? (gu_small ? PICK(2, 1, false, hu) : PICK(4, 1, false, hu)) : (gu_small ? PICK(2, 3, false, hu) : PICK(4, 3, false, hu));
+  auto down = p.y_bf16 ? (dn_small ? PICK(1, 1, true, iu) : PICK(4, 1, true, iu)) : (dn_small ? PICK(1, 3, true, iu) : PICK(4, 3, true, iu));
+#undef PICK
+  const int nu = rows(p.I, gu_small ? 64 : 128), nd = rows(p.H, dn_small ? 64 : 256);
+  hipLaunchKernelGGL(up, dim3(tile_grid(p.max_tiles, nu)), dim3(256), 0, s, p, nu);
+  hipLaunchKernelGGL(down, dim3(tile_grid(p.max_tiles, nd)), dim3(256), 0, s, p, nd);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_gemm(const Mx4Product &p, hipStream_t s) {
-  const int64_t mt = (p.M + GM_ROWS - 1) / GM_ROWS, nr = (p.N + GM_WROWS - 1) / GM_WROWS;
-  auto f = p.y_bf16 ? (p.K % 128 ? k_mx4_gemm<true, false> : k_mx4_gemm<true, true>)
-                    : (p.K % 128 ? k_mx4_gemm<false, false> : k_mx4_gemm<false, true>);
+  const int64_t mt = (p.M + GM_ROWS - 1) / GM_ROWS;
+  const bool small = mt * ((p.N + 255) / 256) < 256, u = p.K % 128 != 0;
+#define PICK(G, Y) (u ? k_mx4_gemm<G, Y, false> : k_mx4_gemm<G, Y, true>)
+  auto f = p.y_bf16 ? (small ? PICK(1, true) : PICK(4, true)) : (small ? PICK(1, false) : PICK(4, false));
+#undef PICK
+  const int64_t nr = (p.N + (small ? 63 : 255)) / (small ? 64 : 256);
   hipLaunchKernelGGL(f, dim3(tile_grid(mt, nr)), dim3(256), 0, s, p, (int)mt, (int)nr);
   return hipGetLastError();
 }

@@ -61,11 +61,16 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
   for (int q = 0; q < SPT; ++q) sx[q] = row_of(min(q * 256 + tid, ROWS - 1), p.a_scales, p.ws, nblk);
 
   auto load = [&](int st, char *to) {
+    if (EVEN || st * 8 + 8 <= nblk) {
 #pragma unroll
-    for (int q = 0; q < DMA; ++q) {
-      char *d = to + (q * 4 + wave) * 1024;
-      if (EVEN || st * 8 + 8 <= nblk || st * 8 + ch[q] < nblk) load_lds16(src[q] + (int64_t)st * 128, d);
-      else *reinterpret_cast<u4 *>(d + lane * 16) = u4{0, 0, 0, 0};
+      for (int q = 0; q < DMA; ++q) load_lds16(src[q] + (int64_t)st * 128, to + (q * 4 + wave) * 1024);
+    } else {
+#pragma unroll
+      for (int q = 0; q < DMA; ++q) {
+        char *d = to + (q * 4 + wave) * 1024;
+        if (st * 8 + ch[q] < nblk) load_lds16(src[q] + (int64_t)st * 128, d);
+        else *reinterpret_cast<u4 *>(d + lane * 16) = u4{0, 0, 0, 0};
+      }
     }
     asm volatile("" ::: "memory");
   };

@@ -495,19 +495,44 @@ __global__ __launch_bounds__(64 * SW) void k_mx4_down_one(Mx4Experts p) {
 }
 
 // ---------------------------------------------------------------- product of up to 16 rows
+// 16 activation rows from memory (L2 after the first workgroup) as the matrix
+// instruction wants them, and 16 weight rows per workgroup; the waves share k.
 template <bool YBF>
 __global__ __launch_bounds__(64 * SW) void k_mx4_product_few(Mx4Product p) {
   constexpr int KT = 4;
-  __shared__ __attribute__((aligned(16))) char lds[SW * KT * 1024];
+  __shared__ f4 part[(SW - 1) * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * 16;
+  const int nblk = (int)(p.K / 32), nt = (nblk + 3) / 4;
   Rows<1> R;
   set_rows(R, 0, p.w, p.ws, n0, p.N, p.K);
+  const bool in = m0 + r < p.M;
+  const uint8_t *const a = (const uint8_t *)p.a + (m0 + r < p.M ? m0 + r : p.M - 1) * p.lda * 2;
   f4 acc[1] = {{0, 0, 0, 0}};
-  small_dot<1, KT, 1>(acc, R, p.K, wave, SW, (int)p.M, [&](int m) { return (const uint8_t *)p.a + m * p.lda * 2; }, 0,
-                      lds + wave * KT * 1024);
-  join_waves<1>(reinterpret_cast<f4 *>(lds), acc);
-  if (wave == 0 && r < p.M) store_row4<YBF>(p, r, n0 + 4 * g, acc[0]);
+  for (int c = KT * wave; c < nt; c += SW * KT) {  // KT adjacent tiles
+    u4 w[KT], x[KT][4];
+    uint32_t sc[KT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const int blk = (c + t) * 4 + g, b = blk < nblk ? blk : nblk - 1;
+      w[t] = load16(R.w[0] + (R.wo[0] + (uint32_t)b * 16u));
+      sc[t] = R.s[0][R.so[0] + (uint32_t)b];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[t][j] = load16(a + (int64_t)b * 64 + j * 16);
+    }
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const bool out = (c + t) * 4 + g >= nblk;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bf8 v = __builtin_bit_cast(bf8, x[t][j]);
+        if (out || !in) v = zero_bf8();
+        acc[0] = mfma_bf16(codes_bf16(out ? 0 : w[t][j], scale_float(out ? 127 : sc[t])), v, acc[0]);
+      }
+    }
+  }
+  join_waves<1>(part, acc);
+  if (wave == 0 && in) store_row4<YBF>(p, m0 + r, n0 + 4 * g, acc[0]);
 }
 
 // both operands in 4 bits: one scaled matrix instruction per k-tile
@@ -520,7 +545,8 @@ __global__ __launch_bounds__(64 * SW) void k_mx4_product_few4(Mx4Product p) {
   const int nblk = (int)(p.K / 32), nt = (nblk + 3) / 4;
   Rows<2> R;
   set_rows(R, 0, p.w, p.ws, n0, p.N, p.K);
-  set_rows(R, 1, (const uint8_t *)p.a, p.a_scales, 0, p.M, p.K);
+  const int64_t m0 = (int64_t)blockIdx.y * 16;
+  set_rows(R, 1, (const uint8_t *)p.a, p.a_scales, m0, p.M, p.K);
   f4 acc[1] = {{0, 0, 0, 0}};
   for (int c = wave; c < nt; c += SW * KT) {
     u4 w[2][KT];
@@ -548,13 +574,13 @@ __global__ __launch_bounds__(64 * SW) void k_mx4_product_few4(Mx4Product p) {
     }
   }
   join_waves<1>(part, acc);
-  if (wave == 0 && r < p.M) store_row4<YBF>(p, r, n0 + 4 * g, acc[0]);
+  if (wave == 0 && m0 + r < p.M) store_row4<YBF>(p, m0 + r, n0 + 4 * g, acc[0]);
 }
 
 }  // namespace
 
 hipError_t launch_mx4_product_few(const Mx4Product &p, hipStream_t s) {
-  const dim3 g((unsigned)((p.N + 15) / 16)), b(64 * SW);
+  const dim3 g((unsigned)((p.N + 15) / 16), (unsigned)((p.M + 15) / 16)), b(64 * SW);
   if (p.a_scales && p.y_bf16) hipLaunchKernelGGL(k_mx4_product_few4<true>, g, b, 0, s, p);
   else if (p.a_scales) hipLaunchKernelGGL(k_mx4_product_few4<false>, g, b, 0, s, p);
   else if (p.y_bf16) hipLaunchKernelGGL(k_mx4_product_few<true>, g, b, 0, s, p);
