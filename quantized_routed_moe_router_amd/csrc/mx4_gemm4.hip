@@ -4,8 +4,8 @@
 //
 // A workgroup of four waves has 16 MT activation rows and 64 NT weight rows.
 // Both operands' codes are staged in LDS, 256 columns (whole lines of memory)
-// at a time and three buffers deep, by loads that bypass the registers; a wave multiplies all the
-// activation rows with its own 16 NT weight rows.  (Weights straight to
+// at a time and NB buffers deep, by loads that bypass the registers; a wave
+// multiplies all the activation rows with its own 16 NT weight rows.  (Weights straight to
 // registers come in the wrong order: a lane's row is not its neighbour's, and
 // 64 lookups a load or as many cross-lane reads cost more than the LDS does.)
 // Row 4 g' + v of its i-th group of 16 is row 4 NT g' + 4 i + v of them: a
@@ -15,6 +15,15 @@
 // lanes on their way through LDS: lane (r, g) then reads one dword with the
 // scales of its block of four successive instructions, each of which picks
 // its byte.
+//
+// 2048 x 4096 x 4096 takes 28.7 us (2.4 Pflop/s), of which a launch with no
+// columns takes about 5; each further 128 columns cost 0.7 us, where the
+// matrix instructions of the whole card need 0.31.  Two buffers leave room for
+// two workgroups on a CU, one of which multiplies while the other waits for
+// its stage: 128 x 128 with two buffers 28.7 us, 128 x 256 with two 31.1 and
+// with three 31.0, 64 x 128 with three 37.9.  What is left is the wait for LDS
+// and the barriers between stages: the matrix units are busy a quarter of the
+// time.
 #include "mx4_dev.h"
 
 namespace ds4 {
@@ -28,13 +37,13 @@ __device__ __forceinline__ f4 mfma_sel(u4 a, u4 b, f4 c, uint32_t sa, uint32_t s
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
-template <int MT, int NT, bool YBF, bool EVEN>
-__global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Product p, int mtiles, int ntiles) {
+template <int MT, int NT, int NB, bool YBF, bool EVEN>
+__global__ __launch_bounds__(256, 2) void k_mx4_gemm4(Mx4Product p, int mtiles, int ntiles) {
   constexpr int BM = 16 * MT, ROWS = BM + 64 * NT;  // activation rows, then weight rows
   constexpr int STAGE = ROWS * 128;                  // bytes of 256 columns of their codes
   constexpr int DMA = STAGE / 4096, SPT = (ROWS + 255) / 256;
-  __shared__ __attribute__((aligned(16))) char lds[3 * STAGE + 2 * ROWS * 16];
-  char *const lsc = lds + 3 * STAGE;
+  __shared__ __attribute__((aligned(16))) char lds[NB * STAGE + 2 * ROWS * 16];
+  char *const lsc = lds + NB * STAGE;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
   int ti, nb;
   if (!tile_of(blockIdx.x, mtiles, ntiles, ti, nb)) return;
@@ -95,13 +104,13 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
   const int fa = r * 128, fw = (BM + wr) * 128, f0 = (g ^ place8(r)) * 16;
   load_sc(0);
   load(0, lds);
-  load(min(1, last), lds + STAGE);
+  if (NB > 2) load(min(1, last), lds + STAGE);
   put_sc(0);
-  wait_vm<DMA>();
+  wait_vm<(NB - 2) * DMA>();
   barrier_keep_loads();
   int s = 0;
   const char *x = lds;
-  char *in = lds + 2 * STAGE;
+  char *in = lds + (NB - 1) * STAGE;
   // One stage.  Past the end the last one is loaded again, so that the waits
   // are for a fixed number of loads.
   auto stage = [&](auto S) {
@@ -113,7 +122,7 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
       for (int i = 0; i < NT; ++i) sw[i] = *reinterpret_cast<const uint32_t *>(ls + (BM + wr + 4 * i) * 16 + 4 * g);
       load_sc(min(s + 2, last / 2 * 2));
     }
-    load(min(s + 2, last), in);
+    load(min(s + NB - 1, last), in);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       u4 w[NT], a[MT];
@@ -128,10 +137,10 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
           acc[i][m] = h ? mfma_sel<S + 1>(w[i], a[m], acc[i][m], sw[i], sa[m]) : mfma_sel<S>(w[i], a[m], acc[i][m], sw[i], sa[m]);
     }
     if (S == 2) put_sc((s & 2) / 2 ^ 1);
-    wait_vm<DMA>();  // the next stage's codes have landed
+    wait_vm<(NB - 2) * DMA>();  // the next stage's codes have landed
     barrier_keep_loads();
-    x = x + STAGE == lds + 3 * STAGE ? lds : x + STAGE;
-    in = in + STAGE == lds + 3 * STAGE ? lds : in + STAGE;
+    x = x + STAGE == lds + NB * STAGE ? lds : x + STAGE;
+    in = in + STAGE == lds + NB * STAGE ? lds : in + STAGE;
     return ++s > last;
   };
   for (;;) {
@@ -153,21 +162,24 @@ __global__ __launch_bounds__(256, MT *NT >= 32 ? 1 : 2) void k_mx4_gemm4(Mx4Prod
 
 }  // namespace
 
-template <int MT, int NT>
+template <int MT, int NT, int NB>
 static hipError_t gemm4(const Mx4Product &p, hipStream_t s) {
   const int mt = (int)((p.M + 16 * MT - 1) / (16 * MT)), nt = (int)((p.N + 64 * NT - 1) / (64 * NT));
   const dim3 g(tile_grid(mt, nt)), b(256);
-  auto f = p.y_bf16 ? (p.K % 256 ? k_mx4_gemm4<MT, NT, true, false> : k_mx4_gemm4<MT, NT, true, true>)
-                    : (p.K % 256 ? k_mx4_gemm4<MT, NT, false, false> : k_mx4_gemm4<MT, NT, false, true>);
+  auto f = p.y_bf16 ? (p.K % 256 ? k_mx4_gemm4<MT, NT, NB, true, false> : k_mx4_gemm4<MT, NT, NB, true, true>)
+                    : (p.K % 256 ? k_mx4_gemm4<MT, NT, NB, false, false> : k_mx4_gemm4<MT, NT, NB, false, true>);
   hipLaunchKernelGGL(f, g, b, 0, s, p, mt, nt);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_gemm4(const Mx4Product &p, hipStream_t s) {
   auto groups = [&](int mt, int nt) { return ((p.M + 16 * mt - 1) / (16 * mt)) * ((p.N + 64 * nt - 1) / (64 * nt)); };
-  if (groups(8, 4) >= 192) return gemm4<8, 4>(p, s);
-  if (groups(4, 2) >= 192) return gemm4<4, 2>(p, s);
-  return gemm4<4, 1>(p, s);
+  // N = K = 4096, in us, this tile against the next: 2048 rows (512 groups of 128 x 128) 27.7 and 37.9, 1024 rows
+  // (256) 19.4 and 19.4, 512 rows (128) 17.2 and 14.4.
+  if (groups(8, 2) > 256) return gemm4<8, 2, 2>(p, s);
+  // 1024 rows (512 groups of 64 x 128) 19.4 and 25.1, 512 rows (256) 14.4 and 14.6, 256 rows (128) 11.1 and 9.8.
+  if (groups(4, 2) >= 192) return gemm4<4, 2, 3>(p, s);
+  return gemm4<4, 1, 3>(p, s);
 }
 
 }  // namespace ds4

@@ -73,8 +73,8 @@ def gate(logits, bias, k, score, G=1, top_groups=1, rank=1, renorm=True, scale=1
         order = cand[np.lexsort((cand, -key[t][cand]))]
         idx[t] = order[:k]
         v = key[t][order[:k + 1]]
-        d = v[:-1] - v[1:]
         with np.errstate(all="ignore"):
+            d = v[:-1] - v[1:]
             ok = (d != 0) & np.isfinite(v[:-1]) & np.isfinite(v[1:])
             rel = d[ok] / np.maximum(np.abs(v[:-1][ok]), 0.05 if bias is not None else 1e-30)
         if bias is not None and rel.size:

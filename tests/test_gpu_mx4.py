@@ -103,7 +103,8 @@ def product_case(M, N, K, kind, seed, pad=0):
 @pytest.mark.parametrize("kind", ["bf16", "mx4"])
 @pytest.mark.parametrize("M,N,K", [
     (1, 16, 32), (1, 512, 4096), (2, 17, 96), (3, 1, 32), (15, 33, 160), (16, 64, 128), (17, 100, 1056), (37, 1000, 2080),
-    (64, 128, 256), (65, 129, 288), (128, 256, 512), (130, 500, 96), (200, 80, 4128), (257, 272, 640), (513, 384, 384)])
+    (64, 128, 256), (65, 129, 288), (128, 256, 512), (130, 500, 96), (200, 80, 4128), (257, 272, 640), (513, 384, 384),
+    (513, 3000, 96), (1600, 4096, 96), (1600, 4096, 128), (2048, 3100, 256), (2047, 3101, 640)])
 def test_product(kind, M, N, K):
     q = _q()
     (a, sa), av, w = product_case(M, N, K, kind, M + N + K, pad=8 if M % 2 else 0)
@@ -222,7 +223,13 @@ def experts_bound(x, idx, w, vals, bf16_y):
 @pytest.mark.parametrize("T,H,I,E,k,skew", [
     (1, 256, 128, 8, 2, 0.0), (1, 32, 32, 1, 1, 0.0), (2, 96, 160, 5, 3, 0.0), (7, 1024, 352, 6, 4, 0.5), (16, 320, 64, 16, 4, 0.0),
     (33, 160, 96, 3, 2, 1.0), (70, 512, 256, 9, 2, 0.4), (150, 256, 288, 4, 3, 1.0), (300, 128, 128, 40, 4, 0.1),
-    (520, 96, 96, 2, 1, 1.0)])
+    (520, 96, 96, 2, 1, 1.0),
+    # few tokens of many experts; experts of more than four of them; rows longer than one pass holds
+    (8, 256, 128, 16, 2, 0.0), (16, 512, 256, 32, 2, 0.0), (12, 1024, 352, 64, 4, 0.1), (16, 256, 128, 64, 4, 1.0),
+    (16, 8224, 96, 64, 2, 0.2), (1, 8224, 64, 8, 2, 0.0), (3, 9216, 32, 4, 2, 0.0), (1, 64, 2080, 4, 2, 0.0),
+    (1, 32, 8192, 4, 2, 0.0), (4, 64, 2080, 6, 3, 0.0), (6, 32, 4128, 16, 2, 0.0),
+    # tiles of 256 weight rows
+    (200, 1024, 512, 64, 4, 0.0), (230, 1056, 544, 64, 4, 0.3)])
 def test_experts(dtype, T, H, I, E, k, skew):
     q = _q()
     x, ws, idx, w = experts_case(T, H, I, E, k, T + H, skew)
