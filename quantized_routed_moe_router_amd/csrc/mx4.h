@@ -91,13 +91,14 @@ hipError_t launch_mx4_gemm_experts(const Mx4Experts &p, hipStream_t s);  // h an
 hipError_t launch_mx4_gemm(const Mx4Product &p, hipStream_t s);          // bf16 activations, many rows
 hipError_t launch_mx4_gemm4(const Mx4Product &p, hipStream_t s);         // 4-bit activations, many rows
 constexpr int MX4_FEW = 16;       // tokens that the experts' kernels for few of them take
-// Rows of a product that its kernels for few take: bf16 activations of 64 rows
-// (N = K = 4096) 23 us there, 25 in the tiled kernel; 4-bit ones of 64 rows
-// 16 us, 10 in the tiled kernel, of 32 rows 10 in both.
+// Rows of a product that its kernels for few take (N = K = 4096): bf16
+// activations of 64 rows 23 us there, 25 in the tiled kernel; 4-bit ones of 64
+// rows 16 us, 10 in the tiled kernel, of 32 rows 10 in both.
 constexpr int MX4_FEW_ROWS = 64, MX4_FEW_ROWS4 = 32;
 constexpr int MX4_ONE = 4;   // tokens whose down projection adds the experts up itself
-// bf16 terms that the SwiGLU intermediate is held in: 24 bits for an fp32
-// result; for a bf16 one 16 bits where the second term costs nothing
+// bf16 terms that the SwiGLU intermediate is held in: three, 24 bits, for an
+// fp32 result; for a bf16 one two where the second costs nothing, else one,
+// whose rounding (2^-9 of each value) is below that of the result itself
 inline int mx4_h_planes(bool y_bf16, bool few) { return !y_bf16 ? 3 : few ? 2 : 1; }
 // Whether a call takes the experts' kernels for few tokens: few each, that is
 // (16 tokens with 2 of 8 experts: 103 us there, 44 in the tiled kernels).

@@ -30,7 +30,9 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv &f) {
 // floor(log2 max) - 2 (the block's largest value lands in [4, 8), the grid
 // ends at 6 and the conversion saturates), round to nearest even on the grid
 // by the conversion instruction.  A block with a NaN or an infinity has scale
-// NaN; a block of zeros the smallest scale.
+// NaN; a block of zeros the smallest scale.  16 bytes of bf16 and 4 of codes
+// per lane, adjacent for adjacent lanes: memory bounds it.  8192 x 4096 in
+// bf16, 85 MB, takes 18.1 us (4.7 TB/s), and as long to dequantise.
 template <bool BF16, bool VEC>
 __global__ __launch_bounds__(256) void k_mx4_quantize(uint8_t *codes, uint8_t *scales, const void *src, int64_t cols,
                                                       int64_t ld, FastDiv quads, uint32_t total) {
@@ -136,7 +138,10 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize(void *dst, int64_t ld, c
 }
 
 // ---------------------------------------------------------------- routed experts: the sum
-// y[t] = sum_j w[t,j] ya[t*k+j], in the order of the ranks
+// y[t] = sum_j w[t,j] ya[t*k+j], in the order of the ranks: fp32 results of
+// the experts, each read once.  2048 tokens, k = 8, H = 4096: 268 MB read and
+// 17 written in 54 us (5.2 TB/s).  (Sums in place by atomics would save the
+// pass and give results that change from call to call.)
 template <bool YBF>
 __global__ __launch_bounds__(256) void k_mx4_combine(Mx4Experts p) {
   const int64_t t = blockIdx.x;

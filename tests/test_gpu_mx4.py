@@ -267,6 +267,22 @@ def test_experts_of_no_tokens_and_of_indices_out_of_range():
     assert (np.abs(y - want)[whole] <= bound[whole]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 3, 12, 60])
+def test_index_out_of_range_adds_nothing_to_its_token(dtype, T):
+    q = _q()
+    H, I, E, k = 96, 64, 16, 2
+    x, ws, idx, w = experts_case(T, H, I, E, k, T)
+    r = routing_of(idx, w, E)
+    bad = idx.copy()
+    bad[::3, 0], bad[1::5, 1] = -1, E
+    r["topk_idx"] = dev(bad.astype(np.int32))
+    ex = q.Mx4Experts(H, I, E, k, *[tuple(dev(v) for v in m) for m in ws], y_dtype=DT[dtype])
+    y = ex.forward(torch.from_numpy(x).cuda().to(torch.bfloat16), r).double().cpu().numpy()
+    want, bound = experts_bound(x, bad, w, [R.values(*m) for m in ws], dtype == "bf16")
+    assert (np.abs(y - want) <= bound).all()
+
+
 def test_experts_beyond_32_bit_offsets():
     """A gate matrix whose last experts' codes lie past 2^31 bytes."""
     q = _q()
