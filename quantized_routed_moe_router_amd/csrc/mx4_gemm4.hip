@@ -21,9 +21,9 @@
 // matrix instructions of the whole card need 0.31.  Two buffers leave room for
 // two workgroups on a CU, one of which multiplies while the other waits for
 // its stage: 128 x 128 with two buffers 28.7 us, 128 x 256 with two 31.1 and
-// with three 31.0, 64 x 128 with three 37.9.  What is left is the wait for LDS
-// and the barriers between stages: the matrix units are busy a quarter of the
-// time.
+// with three 31.0, 64 x 128 with three 37.9; with the waves two by two, which
+// reads a fifth less from LDS, 28.  What is left are the loads into LDS and the
+// barriers between stages: the matrix units are busy a fifth of the time.
 #include "mx4_dev.h"
 
 namespace ds4 {

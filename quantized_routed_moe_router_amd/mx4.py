@@ -29,6 +29,7 @@ def _need(ok, what: str) -> None:
 # only when there is one.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _empty = torch.empty
+_split = torch.split_with_sizes
 _L = B.lib()
 
 
@@ -96,15 +97,18 @@ class Gate:
         if T == 0:
             return {n: torch.zeros(s, dtype=torch.float32 if n == "topk_w" else torch.int32, device=dev) for n, s in (
                 ("topk_idx", (0, k)), ("topk_w", (0, k)), ("counts", E), ("offsets", E + 1), ("perm", 0))}
-        idx = _empty((T, k), dtype=torch.int32, device=dev)
+        # one allocation for the workspace (first: it wants the alignment) and the indices; each costs as much as a
+        # tenth of a call for one token
+        n, A = _L.ds4moe_gate_workspace_bytes(g, T), T * k
         w = _empty((T, k), dtype=torch.float32, device=dev)
-        counts, offsets, perm = _empty(2 * E + 1 + T * k, dtype=torch.int32, device=dev).split((E, E + 1, T * k))
-        n = _L.ds4moe_gate_workspace_bytes(g, T)
-        ws = _empty(n, dtype=torch.uint8, device=dev)
+        buf = _empty(n // 4 + 2 * A + 2 * E + 1, dtype=torch.int32, device=dev)
+        _, idx, perm, counts, offsets = _split(buf, (n // 4, A, A, E, E + 1))
+        ws = buf.data_ptr()
+        at = ws + n
         _done(_L.ds4moe_gate(g, logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T,
-                             ctypes.byref(B.Routing(idx.data_ptr(), w.data_ptr(), counts.data_ptr(), offsets.data_ptr(),
-                                                    perm.data_ptr(), None)),
-                             ws.data_ptr(), n, _raw_stream(dev.index)), "gate")
+                             ctypes.byref(B.Routing(at, w.data_ptr(), at + 8 * A, at + 8 * A + 4 * E, at + 4 * A, None)),
+                             ws, n, _raw_stream(dev.index)), "gate")
+        idx = idx.view(T, k)
         return {"topk_idx": idx, "topk_w": w, "counts": counts, "offsets": offsets, "perm": perm}
 
     def backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, d_topk_w: torch.Tensor,
