@@ -100,7 +100,7 @@ class Gate:
         # one allocation for the workspace (first: it wants the alignment) and the indices; each costs as much as a
         # tenth of a call for one token
         n, A = _L.ds4moe_gate_workspace_bytes(g, T), T * k
-        w = _empty((T, k), dtype=torch.float32, device=dev)
+        w = _empty(T, k, dtype=torch.float32, device=dev)
         buf = _empty(n // 4 + 2 * A + 2 * E + 1, dtype=torch.int32, device=dev)
         _, idx, perm, counts, offsets = _split(buf, (n // 4, A, A, E, E + 1))
         ws = buf.data_ptr()
@@ -118,7 +118,7 @@ class Gate:
         T = logits.shape[0]
         _flat(topk_idx, "topk_idx", torch.int32, (T, self.k))
         _flat(d_topk_w, "d_topk_w", torch.float32, (T, self.k))
-        out = _empty((T, self.E), dtype=logits.dtype, device=dev)
+        out = _empty(T, self.E, dtype=logits.dtype, device=dev)
         _done(_L.ds4moe_gate_backward(self._gating[logits.dtype], logits.data_ptr(), ld,
                                       None if bias is None else bias.data_ptr(), topk_idx.data_ptr(),
                                       d_topk_w.data_ptr(), T, out.data_ptr(), self.E, _raw_stream(dev.index)),
@@ -131,8 +131,8 @@ def mx4_quantize(x: torch.Tensor) -> tuple:
     ld, dev = _rows(x, "x"), x.device
     rows, cols = x.shape
     nb = (cols + 31) // 32
-    codes = _empty((rows, 16 * nb), dtype=torch.uint8, device=dev)
-    scales = _empty((rows, nb), dtype=torch.uint8, device=dev)
+    codes = _empty(rows, 16 * nb, dtype=torch.uint8, device=dev)
+    scales = _empty(rows, nb, dtype=torch.uint8, device=dev)
     _done(_L.ds4moe_mx4_quantize(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], rows, cols, ld,
                                  _raw_stream(dev.index)), "mx4_quantize")
     return codes, scales
@@ -148,7 +148,7 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int | None =
     cols = 32 * nb if cols is None else cols
     if (cols + 31) // 32 != nb:
         raise ValueError(f"{cols} columns are not {nb} blocks")
-    out = _empty((rows, cols), dtype=dtype, device=codes.device)
+    out = _empty(rows, cols, dtype=dtype, device=codes.device)
     _done(_L.ds4moe_mx4_dequantize(out.data_ptr(), _DTYPES[dtype], cols, codes.data_ptr(), scales.data_ptr(), rows,
                                    cols, _raw_stream(codes.device.index)), "mx4_dequantize")
     return out
@@ -172,7 +172,7 @@ def mx4_matmul(a: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, a_scale
             raise ValueError(f"a: shape {tuple(a.shape)}, w has {K} columns")
         lda, kind, sa = K, B.DS4MOE_MX4, a_scales.data_ptr()
     M, dev = a.shape[0], a.device
-    y = _empty((M, N), dtype=y_dtype, device=dev)
+    y = _empty(M, N, dtype=y_dtype, device=dev)
     _done(_L.ds4moe_mx4_matmul(y.data_ptr(), _DTYPES[y_dtype], N, a.data_ptr(), sa, kind, lda, w.data_ptr(),
                                w_scales.data_ptr(), M, N, K, _raw_stream(dev.index)), "mx4_matmul")
     return y
@@ -208,7 +208,7 @@ class Mx4Experts:
                       _flat(routing["perm"], "perm", i32, (T * k,)).data_ptr(), None)
         n = _L.ds4moe_mx4_workspace_bytes(self._dims, T)
         ws = _empty(n, dtype=torch.uint8, device=dev)
-        y = _empty((T, H), dtype=self.y_dtype, device=dev)
+        y = _empty(T, H, dtype=self.y_dtype, device=dev)
         _done(_L.ds4moe_mx4_experts(self._dims, self._weights, x.data_ptr(), ldx, T, ctypes.byref(r), y.data_ptr(),
                                     ws.data_ptr(), n, _raw_stream(dev.index)), "mx4_experts")
         return y

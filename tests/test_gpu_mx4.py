@@ -104,7 +104,8 @@ def product_case(M, N, K, kind, seed, pad=0):
 @pytest.mark.parametrize("M,N,K", [
     (1, 16, 32), (1, 512, 4096), (2, 17, 96), (3, 1, 32), (15, 33, 160), (16, 64, 128), (17, 100, 1056), (37, 1000, 2080),
     (64, 128, 256), (65, 129, 288), (128, 256, 512), (130, 500, 96), (200, 80, 4128), (257, 272, 640), (513, 384, 384),
-    (513, 3000, 96), (1600, 4096, 96), (1600, 4096, 128), (2048, 3100, 256), (2047, 3101, 640)])
+    (513, 3000, 96), (1600, 4096, 96), (1600, 4096, 128), (2048, 3100, 256), (2047, 3101, 640),
+    (2048, 3100, 768), (600, 384, 768)])
 def test_product(kind, M, N, K):
     q = _q()
     (a, sa), av, w = product_case(M, N, K, kind, M + N + K, pad=8 if M % 2 else 0)
@@ -265,6 +266,28 @@ def test_experts_of_no_tokens_and_of_indices_out_of_range():
     whole = [t for t in range(4) if all(bad.reshape(-1)[first[int(e)]] == e for e in idx[t])]
     assert np.isfinite(y[whole]).all()
     assert (np.abs(y - want)[whole] <= bound[whole]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_too_far_apart_for_32_bits(dtype):
+    """Tokens that span more than 2^32 bytes of their buffer."""
+    q = _q()
+    T, H, I, E, k = 140, 96, 64, 4, 2
+    x, ws, idx, w = experts_case(T, H, I, E, k, 1)
+    buf = torch.empty(T, 2**24, dtype=torch.bfloat16, device="cuda")
+    far = buf[:, :H]
+    far.copy_(torch.from_numpy(x))
+    ex = q.Mx4Experts(H, I, E, k, *[tuple(dev(v) for v in m) for m in ws], y_dtype=DT[dtype])
+    r = routing_of(idx, w, E)
+    assert torch.equal(ex.forward(far, r), ex.forward(far.contiguous(), r))
+    wc, sc = dev(ws[0][0][0]), dev(ws[0][1][0])
+    assert torch.equal(q.mx4_matmul(far, wc, sc, y_dtype=DT[dtype]), q.mx4_matmul(far.contiguous(), wc, sc, y_dtype=DT[dtype]))
+    del far, buf
+    farther = torch.empty(70, 2**24 + 8, dtype=torch.bfloat16, device="cuda")[:, :H]
+    farther.copy_(torch.from_numpy(x[:70]))
+    got, want = (q.mx4_matmul(a, wc, sc, y_dtype=torch.float32) for a in (farther, farther.contiguous()))
+    mag = np.abs(x[:70].astype(np.float64)) @ np.abs(R.values(ws[0][0][0], ws[0][1][0])).T
+    assert (np.abs((got - want).double().cpu().numpy()) <= 2 * EPS * (H + 2) * mag).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
