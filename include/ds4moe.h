@@ -527,8 +527,7 @@ size_t ds4moe_mx4_workspace_bytes(const ds4moe_mx4_dims *dims, int32_t T);
  * topk_idx, topk_w, counts, offsets and perm, all set, as ds4moe_gate or
  * ds4moe_route leave them (logits is not read).  y [T,hidden] of y_dtype.
  * Products have exact bf16 operands and fp32 sums; the SwiGLU intermediate is
- * rounded to bf16 for a bf16 y (to 16 bits in a call of few tokens), and held
- * to 24 bits for an fp32 y.  A weight beyond bf16 (a scale of 2^126 and up)
+ * held to 16 bits for a bf16 y and to 24 bits for an fp32 y.  A weight beyond bf16 (a scale of 2^126 and up)
  * counts as an infinity.  An index outside 0..E-1 adds nothing to its token. */
 int ds4moe_mx4_experts(const ds4moe_mx4_dims *dims, const ds4moe_mx4_weights *w, const void *x, int64_t ldx, int32_t T,
                        const ds4moe_routing *routing, void *y, void *ws, size_t ws_bytes, void *stream);

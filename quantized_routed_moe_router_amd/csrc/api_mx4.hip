@@ -81,11 +81,7 @@ Mx4Layout mx4_layout(const ds4moe_mx4_dims &d, int64_t T) {
     return o;
   };
   const size_t A = (size_t)T * d.top_k;
-  // never less than for fewer tokens, whose intermediate may have more terms
-  const bool bf16 = d.y_dtype == DS4MOE_BF16;
-  const size_t few = (size_t)(T < MX4_FEW ? T : MX4_FEW) * d.top_k * mx4_h_planes(bf16, true);
-  const size_t rows = A * mx4_h_planes(bf16, mx4_few(T, d.top_k, d.n_experts));
-  L.h = take(2 * (rows > few ? rows : few) * d.inter);
+  L.h = take(2 * A * mx4_h_planes(d.y_dtype == DS4MOE_BF16) * d.inter);
   L.ya = take(4 * A * d.hidden);
   L.tiles = take(sizeof(Mx4Tiles) + sizeof(Mx4Tile) * (size_t)mx4_max_tiles((int64_t)A, d.n_experts));
   L.total = off;

@@ -96,10 +96,11 @@ constexpr int MX4_FEW = 16;       // tokens that the experts' kernels for few of
 // rows 16 us, 10 in the tiled kernel, of 32 rows 10 in both.
 constexpr int MX4_FEW_ROWS = 64, MX4_FEW_ROWS4 = 32;
 constexpr int MX4_ONE = 4;   // tokens whose down projection adds the experts up itself
-// bf16 terms that the SwiGLU intermediate is held in: three, 24 bits, for an
-// fp32 result; for a bf16 one two where the second costs nothing, else one,
-// whose rounding (2^-9 of each value) is below that of the result itself
-inline int mx4_h_planes(bool y_bf16, bool few) { return !y_bf16 ? 3 : few ? 2 : 1; }
+// bf16 terms that the SwiGLU intermediate is held in, however many tokens a
+// call has: three, 24 bits, for an fp32 result, two, 16 bits, for a bf16 one
+// (one term's rounding, 2^-8 of a value, adds as much to the result as the
+// result's own: 2.3e-3 off the 64-bit values where two leave 1.7e-3)
+inline int mx4_h_planes(bool y_bf16) { return y_bf16 ? 2 : 3; }
 // Whether a call takes the experts' kernels for few tokens: few each, that is
 // (16 tokens with 2 of 8 experts: 103 us there, 44 in the tiled kernels).
 inline bool mx4_few(int64_t T, int64_t k, int64_t E) { return T <= MX4_ONE || (T <= MX4_FEW && T * k <= 2 * E); }

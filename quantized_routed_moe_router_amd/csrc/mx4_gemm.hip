@@ -378,8 +378,8 @@ hipError_t launch_mx4_gemm_experts(const Mx4Experts &p, hipStream_t s) {
   hipLaunchKernelGGL(k_mx4_plan, dim3(1), dim3(512), 0, s, p);
   const bool hu = p.H % 128 != 0, iu = p.I % 128 != 0;
 #define PICK(G, PL, D, U) (U ? k_mx4_gemm_experts<G, PL, D, false> : k_mx4_gemm_experts<G, PL, D, true>)
-  auto up = p.y_bf16 ? (gu_small ? PICK(2, 1, false, hu) : PICK(4, 1, false, hu)) : (gu_small ? PICK(2, 3, false, hu) : PICK(4, 3, false, hu));
-  auto down = p.y_bf16 ? (dn_small ? PICK(1, 1, true, iu) : PICK(4, 1, true, iu)) : (dn_small ? PICK(1, 3, true, iu) : PICK(4, 3, true, iu));
+  auto up = p.y_bf16 ? (gu_small ? PICK(2, 2, false, hu) : PICK(4, 2, false, hu)) : (gu_small ? PICK(2, 3, false, hu) : PICK(4, 3, false, hu));
+  auto down = p.y_bf16 ? (dn_small ? PICK(1, 2, true, iu) : PICK(4, 2, true, iu)) : (dn_small ? PICK(1, 3, true, iu) : PICK(4, 3, true, iu));
 #undef PICK
   const int nu = rows(p.I, gu_small ? 64 : 128), nd = rows(p.H, dn_small ? 64 : 256);
   hipLaunchKernelGGL(up, dim3(tile_grid(p.max_tiles, nu)), dim3(256), 0, s, p, nu);
