@@ -47,13 +47,14 @@ __device__ __forceinline__ float own_score(float l, int score) {
 }
 
 // Scores of chosen logits up to one common factor, for their quotients by
-// their sum: where the largest is far below 0 every score is about e^l (its
-// root for the root form) and would end among the subnormals, so the factor
-// e^-max is taken out of them.
+// their sum: below 0 a score goes with e^l (the root form with its root) and
+// would end among the subnormals, so the factor e^max (its root) of the
+// largest is taken out of all where that is below 0.  What is subnormal then
+// has a subnormal weight.
 __device__ __forceinline__ float relative_score(float l, int score, float max) {
-  const float m = max < -60.0f ? max : 0.0f;
+  const float m = fminf(max, 0.0f);
   if (score == SC_SIGMOID) return expf(fminf(l, 0.0f) - m) / (1.0f + expf(-fabsf(l)));
-  return m < 0.0f ? expf(0.5f * (l - m)) : router_score(l);
+  return l < -17.0f ? expf(0.5f * (l - m)) : router_score(l) * expf(-0.5f * m);
 }
 
 // order-preserving key of a float: every number >= 2, masked (-inf) 1
@@ -506,8 +507,10 @@ __global__ __launch_bounds__(256) void k_gate_backward(GateGradArgs a) {
       if (soft) s = expf(l - m);
       else s = a.renorm ? relative_score(l, a.score, m) : own_score(l, a.score);
       if (a.score == SC_SIGMOID) slope = 1.0f / (1.0f + expf(l));
-      if (a.score == SC_SQRT_SOFTPLUS && l < -17.0f) slope = 0.5f;  // sigmoid / (2 softplus) in the limit
-      else if (a.score == SC_SQRT_SOFTPLUS) slope = 0.5f / (s * s * (1.0f + expf(-l)));
+      if (a.score == SC_SQRT_SOFTPLUS) {  // sigmoid / (2 softplus), below -17 the limit of that
+        const float r = router_score(l);
+        slope = l < -17.0f ? 0.5f : 0.5f / (r * r * (1.0f + expf(-l)));
+      }
     }
     float q = s;
     const float ds = live ? dw : 0.0f;
