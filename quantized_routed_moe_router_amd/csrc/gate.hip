@@ -149,9 +149,9 @@ __device__ __forceinline__ void load_logits(const GateArgs &a, int64_t t, float 
 // One token by one wave; lane l holds experts NK*l .. NK*l+NK-1.  Lane j < k
 // returns expert and weight of rank j.  xl, kl: wave-private LDS rows of NK*64
 // floats.
-// b: the bias of the lane's experts.  Selection goes by scores of the
-// hardware's exponential and reciprocal (a few ulp); the weights of the k
-// chosen are computed again with the library's.
+// b: the bias of the lane's experts.  Selection goes by scores of an ulp or
+// two, as the weights do: the hardware's exponential alone, off by the
+// rounding of its argument, is 16 ulp off at a logit of -40.
 template <int NK>
 __device__ __forceinline__ void gate_token(const GateArgs &a, const float (&x)[NK], const float (&b)[NK], float *xl,
                                            float *kl, int &my_e, float &my_w) {
@@ -159,7 +159,7 @@ __device__ __forceinline__ void gate_token(const GateArgs &a, const float (&x)[N
 #pragma unroll
   for (int i = 0; i < NK; ++i) xl[NK * lane + i] = x[i];
   // softmax over all experts: maximum and sum
-  float mx = 0.0f, zinv = 1.0f;
+  float mx = 0.0f, zinv = 1.0f, p[NK];
   const bool soft = a.score == SC_SOFTMAX;
   if (soft) {
     float m = x[0];
@@ -169,7 +169,10 @@ __device__ __forceinline__ void gate_token(const GateArgs &a, const float (&x)[N
     float z = 0.0f;
     if (mx == -INFINITY) mx = 0.0f;  // every expert masked
 #pragma unroll
-    for (int i = 0; i < NK; ++i) z += expf(x[i] - mx);
+    for (int i = 0; i < NK; ++i) {
+      p[i] = expf(x[i] - mx);
+      z += p[i];
+    }
     z = wave_sum_f(z);
     zinv = z > 0.0f ? 1.0f / z : 0.0f;
   }
@@ -181,10 +184,7 @@ __device__ __forceinline__ void gate_token(const GateArgs &a, const float (&x)[N
   for (int i = 0; i < NK; ++i) {
     v[i] = x[i];
     if (need_scores) {
-      float c;
-      if (soft) c = __expf(x[i] - mx) * zinv;
-      else if (a.score == SC_SIGMOID) c = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
-      else c = own_score(x[i], a.score);
+      float c = soft ? p[i] * zinv : own_score(x[i], a.score);
       c += a.bias ? b[i] : 0.0f;
       v[i] = x[i] == -INFINITY || c != c ? -INFINITY : c;
     }

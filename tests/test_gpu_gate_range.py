@@ -93,3 +93,24 @@ def check_gradient(t, l, bias, k, score, renorm, scale, seed):
 @pytest.mark.parametrize("renorm", [True, False])
 def test_gradient_of_logits_far_apart(score, renorm):
     check_gradient(torch.from_numpy(APART).cuda(), APART, None, 4, score, renorm, 2.5, 1)
+
+
+# ------------------------------------------------------------------ selection
+@pytest.mark.parametrize("score", SCORES)
+def test_selection_tells_keys_apart_that_differ_by_a_millionth(score):
+    """Two keys of which one is a score far below 1 and the other a bias, 1e-6 of it above or below: eight ulp, where the
+    score's exponential, sum and quotient are off by an ulp each."""
+    q = _q()
+    g = q.Gate(3, 2, score)
+    wrong = []
+    for x in np.linspace(-84.0, -18.0, 60).astype(np.float32):
+        s = float(R.scores(np.array([[0.0, float(x), -400.0]]), score)[0, 1])
+        for sign in (1, -1):
+            bias = np.float32(s * (1 + sign * 1e-6))
+            t = torch.tensor([[0.0, float(x), -400.0]], device="cuda")
+            b = torch.tensor([0.0, 0.0, float(bias)], device="cuda")
+            first, second = g.forward(t, b)["topk_idx"][0].tolist()
+            assert first == 0
+            if second != (2 if float(bias) > s else 1):
+                wrong.append((float(x), sign))
+    assert not wrong, (len(wrong), wrong[:8])
