@@ -1,8 +1,9 @@
 """The expert gate and the 4-bit microscaled (MXFP4) operators on torch tensors.
 
-Plumbing around the C ABI only: shapes and types are checked here, torch
-allocates outputs and workspaces (on the current stream, so a workspace is
-never shared by calls that overlap), and every step runs in libds4moe.so.
+Plumbing around the C ABI only: shapes, types and devices are checked here,
+torch allocates outputs and workspaces (on the current stream, so a workspace
+is never shared by calls that overlap), and every step runs in libds4moe.so,
+on the device of the call's tensors and its current stream.
 A matrix in 4-bit form is a pair of uint8 tensors: codes [..., cols/2] and
 scales [..., cols/32], rows without gaps.
 """
@@ -28,6 +29,7 @@ def _need(ok, what: str) -> None:
 # addresses go to the library as plain numbers, and a refusal's text is made
 # only when there is one.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_device = torch._C._cuda_getDevice
 _empty = torch.empty
 _split = torch.split_with_sizes
 _L = B.lib()
@@ -48,23 +50,32 @@ def _rows(t: torch.Tensor, what: str, dtypes=_DTYPES) -> int:
     return d if rows > 1 else cols
 
 
-def _flat(t: torch.Tensor, what: str, dtype, shape=None) -> torch.Tensor:
+def _flat(t: torch.Tensor, what: str, dtype, shape=None, dev=None) -> torch.Tensor:
     if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous {dtype} tensor on the GPU is wanted")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{what}: on {t.device}, the call's other tensors on {dev}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
     return t
 
 
-def _packed(codes: torch.Tensor, scales: torch.Tensor, what: str, shape=None) -> tuple:
-    _flat(codes, what, torch.uint8, None if shape is None else (*shape[:-1], shape[-1] // 2))
+def _packed(codes: torch.Tensor, scales: torch.Tensor, what: str, shape=None, dev=None) -> tuple:
+    _flat(codes, what, torch.uint8, None if shape is None else (*shape[:-1], shape[-1] // 2), dev)
     if codes.shape[-1] % 16:
         raise ValueError(f"{what}: whole blocks of 32 are wanted")
-    _flat(scales, what + " scales", torch.uint8, (*codes.shape[:-1], codes.shape[-1] // 16))
+    _flat(scales, what + " scales", torch.uint8, (*codes.shape[:-1], codes.shape[-1] // 16), codes.device)
     return codes, scales
 
 
-def _done(status: int, what: str) -> None:
+def _call(entry, what: str, dev: torch.device, *args) -> None:
+    """A call of the library on a device's current stream, with that device the current one."""
+    i = dev.index
+    if i == _device():
+        status = entry(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            status = entry(*args, _raw_stream(i))
     if status:
         raise B.Ds4MoeError(status, what)
 
@@ -87,7 +98,7 @@ class Gate:
         if logits.shape[1] != self.E:
             raise ValueError(f"logits: {logits.shape[1]} columns, {self.E} experts")
         if bias is not None:
-            _flat(bias, "bias", torch.float32, (self.E,))
+            _flat(bias, "bias", torch.float32, (self.E,), logits.device)
         return ld
 
     def forward(self, logits: torch.Tensor, bias: torch.Tensor | None = None) -> dict:
@@ -105,9 +116,8 @@ class Gate:
         _, idx, perm, counts, offsets = _split(buf, (n // 4, A, A, E, E + 1))
         ws = buf.data_ptr()
         at = ws + n
-        _done(_L.ds4moe_gate(g, logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T,
-                             ctypes.byref(B.Routing(at, w.data_ptr(), at + 8 * A, at + 8 * A + 4 * E, at + 4 * A, None)),
-                             ws, n, _raw_stream(dev.index)), "gate")
+        _call(_L.ds4moe_gate, "gate", dev, g, logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T,
+              ctypes.byref(B.Routing(at, w.data_ptr(), at + 8 * A, at + 8 * A + 4 * E, at + 4 * A, None)), ws, n)
         idx = idx.view(T, k)
         return {"topk_idx": idx, "topk_w": w, "counts": counts, "offsets": offsets, "perm": perm}
 
@@ -116,13 +126,12 @@ class Gate:
         """Gradient of the logits (in their type) from the gradient of topk_w."""
         ld, dev = self._logits(logits, bias), logits.device
         T = logits.shape[0]
-        _flat(topk_idx, "topk_idx", torch.int32, (T, self.k))
-        _flat(d_topk_w, "d_topk_w", torch.float32, (T, self.k))
+        _flat(topk_idx, "topk_idx", torch.int32, (T, self.k), dev)
+        _flat(d_topk_w, "d_topk_w", torch.float32, (T, self.k), dev)
         out = _empty(T, self.E, dtype=logits.dtype, device=dev)
-        _done(_L.ds4moe_gate_backward(self._gating[logits.dtype], logits.data_ptr(), ld,
-                                      None if bias is None else bias.data_ptr(), topk_idx.data_ptr(),
-                                      d_topk_w.data_ptr(), T, out.data_ptr(), self.E, _raw_stream(dev.index)),
-              "gate_backward")
+        _call(_L.ds4moe_gate_backward, "gate_backward", dev, self._gating[logits.dtype], logits.data_ptr(), ld,
+              None if bias is None else bias.data_ptr(), topk_idx.data_ptr(), d_topk_w.data_ptr(), T, out.data_ptr(),
+              self.E)
         return out
 
 
@@ -133,8 +142,8 @@ def mx4_quantize(x: torch.Tensor) -> tuple:
     nb = (cols + 31) // 32
     codes = _empty(rows, 16 * nb, dtype=torch.uint8, device=dev)
     scales = _empty(rows, nb, dtype=torch.uint8, device=dev)
-    _done(_L.ds4moe_mx4_quantize(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], rows, cols, ld,
-                                 _raw_stream(dev.index)), "mx4_quantize")
+    _call(_L.ds4moe_mx4_quantize, "mx4_quantize", dev, codes.data_ptr(), scales.data_ptr(), x.data_ptr(),
+          _DTYPES[x.dtype], rows, cols, ld)
     return codes, scales
 
 
@@ -148,9 +157,10 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int | None =
     cols = 32 * nb if cols is None else cols
     if (cols + 31) // 32 != nb:
         raise ValueError(f"{cols} columns are not {nb} blocks")
-    out = _empty(rows, cols, dtype=dtype, device=codes.device)
-    _done(_L.ds4moe_mx4_dequantize(out.data_ptr(), _DTYPES[dtype], cols, codes.data_ptr(), scales.data_ptr(), rows,
-                                   cols, _raw_stream(codes.device.index)), "mx4_dequantize")
+    dev = codes.device
+    out = _empty(rows, cols, dtype=dtype, device=dev)
+    _call(_L.ds4moe_mx4_dequantize, "mx4_dequantize", dev, out.data_ptr(), _DTYPES[dtype], cols, codes.data_ptr(),
+          scales.data_ptr(), rows, cols)
     return out
 
 
@@ -166,15 +176,17 @@ def mx4_matmul(a: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, a_scale
         lda, kind, sa = _rows(a, "a", _BF16), B.DS4MOE_BF16, None
         if a.shape[1] != K:
             raise ValueError(f"a: {a.shape[1]} columns, w has {K}")
+        if a.device != w.device:
+            raise ValueError(f"a: on {a.device}, w on {w.device}")
     else:
-        _packed(a, a_scales, "a")
+        _packed(a, a_scales, "a", None, w.device)
         if a.dim() != 2 or 2 * a.shape[1] != K:
             raise ValueError(f"a: shape {tuple(a.shape)}, w has {K} columns")
         lda, kind, sa = K, B.DS4MOE_MX4, a_scales.data_ptr()
     M, dev = a.shape[0], a.device
     y = _empty(M, N, dtype=y_dtype, device=dev)
-    _done(_L.ds4moe_mx4_matmul(y.data_ptr(), _DTYPES[y_dtype], N, a.data_ptr(), sa, kind, lda, w.data_ptr(),
-                               w_scales.data_ptr(), M, N, K, _raw_stream(dev.index)), "mx4_matmul")
+    _call(_L.ds4moe_mx4_matmul, "mx4_matmul", dev, y.data_ptr(), _DTYPES[y_dtype], N, a.data_ptr(), sa, kind, lda,
+          w.data_ptr(), w_scales.data_ptr(), M, N, K)
     return y
 
 
@@ -189,28 +201,31 @@ class Mx4Experts:
         self.dims = B.make_mx4_dims(H, I, E, k, _DTYPES[y_dtype])
         _need(B.ds4moe_mx4_workspace_bytes(self.dims, 1) > 0, f"unsupported experts: H={H}, I={I}, E={E}, k={k}")
         self.gate = _packed(*gate, "gate", (E, I, H))
-        self.up = _packed(*up, "up", (E, I, H))
-        self.down = _packed(*down, "down", (E, H, I))
+        self.device = self.gate[0].device
+        self.up = _packed(*up, "up", (E, I, H), self.device)
+        self.down = _packed(*down, "down", (E, H, I), self.device)
         self._dims = ctypes.byref(self.dims)
         self._weights = ctypes.byref(B.make_mx4_weights(*self.gate, *self.up, *self.down))
 
     def forward(self, x: torch.Tensor, routing: dict) -> torch.Tensor:
         """y [T,H] of bf16 x [T,H]; routing: the dict of Gate.forward or DeviceLayer.route."""
-        ldx, dev = _rows(x, "x", _BF16), x.device
+        ldx, dev = _rows(x, "x", _BF16), self.device
         T, H = x.shape
         if H != self.H:
             raise ValueError(f"x: {H} columns, hidden size {self.H}")
+        if x.device != dev:
+            raise ValueError(f"x: on {x.device}, the experts on {dev}")
         i32, k, E = torch.int32, self.k, self.E
-        r = B.Routing(_flat(routing["topk_idx"], "topk_idx", i32, (T, k)).data_ptr(),
-                      _flat(routing["topk_w"], "topk_w", torch.float32, (T, k)).data_ptr(),
-                      _flat(routing["counts"], "counts", i32, (E,)).data_ptr(),
-                      _flat(routing["offsets"], "offsets", i32, (E + 1,)).data_ptr(),
-                      _flat(routing["perm"], "perm", i32, (T * k,)).data_ptr(), None)
+        r = B.Routing(_flat(routing["topk_idx"], "topk_idx", i32, (T, k), dev).data_ptr(),
+                      _flat(routing["topk_w"], "topk_w", torch.float32, (T, k), dev).data_ptr(),
+                      _flat(routing["counts"], "counts", i32, (E,), dev).data_ptr(),
+                      _flat(routing["offsets"], "offsets", i32, (E + 1,), dev).data_ptr(),
+                      _flat(routing["perm"], "perm", i32, (T * k,), dev).data_ptr(), None)
         n = _L.ds4moe_mx4_workspace_bytes(self._dims, T)
         ws = _empty(n, dtype=torch.uint8, device=dev)
         y = _empty(T, H, dtype=self.y_dtype, device=dev)
-        _done(_L.ds4moe_mx4_experts(self._dims, self._weights, x.data_ptr(), ldx, T, ctypes.byref(r), y.data_ptr(),
-                                    ws.data_ptr(), n, _raw_stream(dev.index)), "mx4_experts")
+        _call(_L.ds4moe_mx4_experts, "mx4_experts", dev, self._dims, self._weights, x.data_ptr(), ldx, T,
+              ctypes.byref(r), y.data_ptr(), ws.data_ptr(), n)
         return y
 
 
@@ -218,7 +233,7 @@ class Mx4Layer:
     """A routed layer on 4-bit experts: router logits (accumulated in fp64, as ds4moe_route), gate, experts."""
 
     def __init__(self, router_w: torch.Tensor, gate: Gate, experts: Mx4Experts, bias: torch.Tensor | None = None):
-        _flat(router_w, "router_w", router_w.dtype, (experts.E, experts.H))
+        _flat(router_w, "router_w", router_w.dtype, (experts.E, experts.H), experts.device)
         _need(router_w.dtype in _DTYPES, f"router_w: unsupported type {router_w.dtype}")
         _need((gate.E, gate.k) == (experts.E, experts.k), "gate and experts differ in their numbers of experts or choices")
         self.router_w, self.gate, self.experts, self.bias = router_w, gate, experts, bias
@@ -227,13 +242,14 @@ class Mx4Layer:
               f"unsupported router: hidden size {experts.H}, {experts.E} experts")
 
     def logits(self, x: torch.Tensor) -> torch.Tensor:
-        T, dev = x.shape[0], x.device
-        _flat(x, "x", torch.bfloat16, (T, self.experts.H))
+        T, dev = x.shape[0], self.experts.device
+        _flat(x, "x", torch.bfloat16, (T, self.experts.H), dev)
         out = torch.empty((T, self.experts.E), dtype=torch.float32, device=dev)
         n = B.ds4moe_workspace_bytes(self._dims, T, B.MODE_ROUTE)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        B.ds4moe_route(self._dims, B.make_weights(self.router_w, None, None, None), x, T, B.make_routing(logits=out),
-                       ws, n, torch.cuda.current_stream(dev))
+        w, r = B.make_weights(self.router_w, None, None, None), B.make_routing(logits=out)
+        _call(_L.ds4moe_route, "route", dev, ctypes.byref(self._dims), ctypes.byref(w), x.data_ptr(), T, ctypes.byref(r),
+              ws.data_ptr(), n)
         return out
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
