@@ -4,6 +4,8 @@ Plumbing around the C ABI only: shapes, types and devices are checked here,
 torch allocates outputs and workspaces (on the current stream, so a workspace
 is never shared by calls that overlap), and every step runs in libds4moe.so,
 on the device of the call's tensors and its current stream.
+Nothing here is recorded by autograd: a tensor that requires a gradient is
+refused while gradients are on, and Gate.backward is the gradient that there is.
 A matrix in 4-bit form is a pair of uint8 tensors: codes [..., cols/2] and
 scales [..., cols/32], rows without gaps.
 """
@@ -48,6 +50,14 @@ def _rows(t: torch.Tensor, what: str, dtypes=_DTYPES) -> int:
     if rows > 1 and d < cols:
         raise ValueError(f"{what}: rows overlap")
     return d if rows > 1 else cols
+
+
+def _untracked(what: str, *tensors) -> None:
+    """No tensor here asks for a gradient that these calls would lose without a word."""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{what} asks for a gradient, which autograd does not get from this call: detach it, or call "
+                             "under torch.no_grad() (Gate.backward gives the gradient of a gate's logits)")
 
 
 def _flat(t: torch.Tensor, what: str, dtype, shape=None, dev=None) -> torch.Tensor:
@@ -103,6 +113,7 @@ class Gate:
 
     def forward(self, logits: torch.Tensor, bias: torch.Tensor | None = None) -> dict:
         """topk_idx [T,k], topk_w [T,k], counts [E], offsets [E+1] and perm [T*k] of logits [T,E]."""
+        _untracked("logits or bias", logits, bias)
         ld, g, dev = self._logits(logits, bias), self._gating[logits.dtype], logits.device
         T, k, E = logits.shape[0], self.k, self.E
         if T == 0:
@@ -137,6 +148,7 @@ class Gate:
 
 def mx4_quantize(x: torch.Tensor) -> tuple:
     """(codes, scales) of a matrix [rows, cols] in fp32 or bf16; columns are filled up with zeros to blocks of 32."""
+    _untracked("x", x)
     ld, dev = _rows(x, "x"), x.device
     rows, cols = x.shape
     nb = (cols + 31) // 32
@@ -167,6 +179,7 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int | None =
 def mx4_matmul(a: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, a_scales: torch.Tensor | None = None,
                y_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """a [M,K] times w [N,K]^T: w in 4-bit form, a bf16, or in 4-bit form with a_scales."""
+    _untracked("a", a)
     _packed(w, w_scales, "w")
     if w.dim() != 2 or y_dtype not in _DTYPES:
         raise ValueError(f"w: a matrix is wanted, and an fp32 or bf16 result, not {y_dtype}")
@@ -209,6 +222,7 @@ class Mx4Experts:
 
     def forward(self, x: torch.Tensor, routing: dict) -> torch.Tensor:
         """y [T,H] of bf16 x [T,H]; routing: the dict of Gate.forward or DeviceLayer.route."""
+        _untracked("x or topk_w", x, routing["topk_w"])
         ldx, dev = _rows(x, "x", _BF16), self.device
         T, H = x.shape
         if H != self.H:
@@ -242,6 +256,7 @@ class Mx4Layer:
               f"unsupported router: hidden size {experts.H}, {experts.E} experts")
 
     def logits(self, x: torch.Tensor) -> torch.Tensor:
+        _untracked("x or router_w", x, self.router_w)
         T, dev = x.shape[0], self.experts.device
         _flat(x, "x", torch.bfloat16, (T, self.experts.H), dev)
         out = torch.empty((T, self.experts.E), dtype=torch.float32, device=dev)

@@ -96,3 +96,31 @@ def test_the_library_is_called_with_the_tensors_device_as_the_current_one(monkey
     with pytest.raises(q.Ds4MoeError):
         mx4._call(lambda *a: 2, "x", torch.device("cuda", 1))
     assert seen[-1] == ("off", 1)
+
+
+def test_a_gradient_that_would_be_lost_is_refused():
+    def asks(shape, dtype):
+        t = Tensor(shape, dtype)
+        t.requires_grad = True
+        return t
+
+    r = routing(4)
+    r["topk_w"] = asks((4, 2), F32)
+    calls = [
+        lambda: q.Gate(8, 2).forward(asks((4, 8), F32)),
+        lambda: q.Gate(8, 2).forward(Tensor((4, 8), F32), asks((8,), F32)),
+        lambda: q.mx4_quantize(asks((4, 64), BF16)),
+        lambda: q.mx4_matmul(asks((4, 256), BF16), *packed(16, 256)),
+        lambda: experts().forward(asks((4, 256), BF16), routing(4)),
+        lambda: experts().forward(Tensor((4, 256), BF16), r),
+        lambda: q.Mx4Layer(Tensor((8, 256), F32), q.Gate(8, 2), experts()).forward(asks((4, 256), BF16)),
+        lambda: q.Mx4Layer(asks((8, 256), F32), q.Gate(8, 2), experts()).forward(Tensor((4, 256), BF16)),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    with torch.no_grad():  # nothing to lose: the next check speaks
+        with pytest.raises(ValueError, match="7 columns"):
+            q.Gate(8, 2).forward(asks((4, 7), F32))
+    with pytest.raises(ValueError, match="topk_idx"):  # the gradient itself may have logits that ask for one
+        q.Gate(8, 2).backward(asks((4, 8), F32), Tensor((4, 3), I32), Tensor((4, 2), F32))
