@@ -19,6 +19,7 @@ from . import binding as B
 
 _DTYPES = {torch.float32: B.DS4MOE_F32, torch.bfloat16: B.DS4MOE_BF16}
 _BF16 = (torch.bfloat16,)
+GATE_JOINT = 2048  # tokens up to which a gate's workspace and its indices are one allocation
 _SCORES = {"sqrt_softplus": B.SCORE_SQRT_SOFTPLUS, "sigmoid": B.SCORE_SIGMOID, "softmax": B.SCORE_SOFTMAX}
 
 
@@ -112,21 +113,26 @@ class Gate:
         return ld
 
     def forward(self, logits: torch.Tensor, bias: torch.Tensor | None = None) -> dict:
-        """topk_idx [T,k], topk_w [T,k], counts [E], offsets [E+1] and perm [T*k] of logits [T,E]."""
+        """topk_idx [T,k], topk_w [T,k], counts [E], offsets [E+1] and perm [T*k] of logits [T,E].  All but topk_w are
+        parts of one allocation, which holds as long as one of them does."""
         _untracked("logits or bias", logits, bias)
         ld, g, dev = self._logits(logits, bias), self._gating[logits.dtype], logits.device
         T, k, E = logits.shape[0], self.k, self.E
         if T == 0:
             return {n: torch.zeros(s, dtype=torch.float32 if n == "topk_w" else torch.int32, device=dev) for n, s in (
                 ("topk_idx", (0, k)), ("topk_w", (0, k)), ("counts", E), ("offsets", E + 1), ("perm", 0))}
-        # one allocation for the workspace (first: it wants the alignment) and the indices; each costs as much as a
-        # tenth of a call for one token
+        # One allocation for the indices; an allocation costs as much as a tenth of a call for one token.  Up to
+        # GATE_JOINT tokens the workspace is part of it (first: it wants the alignment): 2048 tokens 13.0 us, 14.2 with
+        # one of its own.  Of more tokens the kernels take longer than the call (4096: 14.4 us both ways), and whoever
+        # keeps the choice for a backward pass would keep the workspace with it, as much again as the indices.
         n, A = _L.ds4moe_gate_workspace_bytes(g, T), T * k
         w = _empty(T, k, dtype=torch.float32, device=dev)
-        buf = _empty(n // 4 + 2 * A + 2 * E + 1, dtype=torch.int32, device=dev)
-        _, idx, perm, counts, offsets = _split(buf, (n // 4, A, A, E, E + 1))
-        ws = buf.data_ptr()
-        at = ws + n
+        held = n // 4 if T <= GATE_JOINT else 0
+        buf = _empty(held + 2 * A + 2 * E + 1, dtype=torch.int32, device=dev)
+        _, idx, perm, counts, offsets = _split(buf, (held, A, A, E, E + 1))
+        at = buf.data_ptr() + 4 * held
+        own = None if held else _empty(n, dtype=torch.uint8, device=dev)
+        ws = buf.data_ptr() if held else own.data_ptr()
         _call(_L.ds4moe_gate, "gate", dev, g, logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T,
               ctypes.byref(B.Routing(at, w.data_ptr(), at + 8 * A, at + 8 * A + 4 * E, at + 4 * A, None)), ws, n)
         idx = idx.view(T, k)

@@ -124,3 +124,22 @@ def test_a_gradient_that_would_be_lost_is_refused():
             q.Gate(8, 2).forward(asks((4, 7), F32))
     with pytest.raises(ValueError, match="topk_idx"):  # the gradient itself may have logits that ask for one
         q.Gate(8, 2).backward(asks((4, 8), F32), Tensor((4, 3), I32), Tensor((4, 2), F32))
+
+
+@pytest.mark.parametrize("T,k,E", [(1, 8, 256), (64, 16, 512), (4096, 8, 256), (4096, 16, 512), (4097, 8, 256), (8192, 8, 256), (1 << 17, 4, 16)])
+def test_outputs_of_the_gate_keep_little_beside_themselves(monkeypatch, T, k, E):
+    """Kept for a backward pass, the choice of many tokens does not keep the workspace, that of few at most 0.7 MB of it."""
+    seen = []
+    monkeypatch.setattr(mx4, "_empty", lambda *shape, dtype, device: torch.empty(*shape, dtype=dtype))
+    monkeypatch.setattr(mx4, "_call", lambda entry, what, dev, *args: seen.append(args))
+    gate = q.Gate(E, k)
+    out = gate.forward(Tensor((T, E), F32))
+    kept = {out[n].untyped_storage().data_ptr(): out[n].untyped_storage().nbytes() for n in out}
+    need = sum(out[n].numel() * 4 for n in out)
+    assert sum(kept.values()) - need <= (700_000 if T <= 4096 else 0)
+    _, _, _, _, _, r, ws, ws_bytes = seen[0]
+    r = r._obj
+    assert (r.topk_idx, r.perm, r.counts, r.offsets, r.topk_w) == tuple(out[n].data_ptr() for n in ("topk_idx", "perm", "counts", "offsets", "topk_w"))
+    # the workspace is its own piece of memory
+    spans = sorted([(ws, ws + ws_bytes)] + [(out[n].data_ptr(), out[n].data_ptr() + 4 * out[n].numel()) for n in out])
+    assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
