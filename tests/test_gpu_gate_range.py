@@ -95,6 +95,25 @@ def test_gradient_of_logits_far_apart(score, renorm):
     check_gradient(torch.from_numpy(APART).cuda(), APART, None, 4, score, renorm, 2.5, 1)
 
 
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k,use_bias", [(1, 256, 8, True), (400, 256, 8, False), (9, 130, 16, True), (3, 512, 3, False), (300, 96, 4, True),
+                                            (5, 60, 4, False)])
+def test_every_element_of_the_gradient(score, renorm, dtype, T, E, k, use_bias):
+    """The small gradients of the logits that were not chosen among them, each to 1e-5 of what it is made of."""
+    t, l, bias = make(T, E, 3 * T + E, dtype, pad=3)
+    check_gradient(t, l, bias if use_bias else None, k, score, renorm, 2.5, E)
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("renorm", [True, False])
+def test_every_element_of_the_gradient_of_low_and_high_rows(score, renorm):
+    rng = np.random.default_rng(2)
+    l = (rng.standard_normal((40, 64)) + rng.choice([-60.0, -30.0, -17.0, 17.0, 60.0], (40, 1))).astype(np.float32)
+    check_gradient(torch.from_numpy(l).cuda(), l, None, 6, score, renorm, 1.0, 5)
+
+
 # ------------------------------------------------------------------ selection
 @pytest.mark.parametrize("score", SCORES)
 def test_selection_tells_keys_apart_that_differ_by_a_millionth(score):
