@@ -441,11 +441,12 @@ typedef struct {
  * invalid arguments. */
 size_t ds4moe_gate_workspace_bytes(const ds4moe_gating *g, int32_t T);
 
-/* Gate T >= 0 tokens (0 = no-op, which leaves every output as it is).  logits: rows of E values, ld
- * elements apart (ld >= E), aligned to their type; bias: [E] fp32 or NULL.  out (host struct):
- * topk_idx, topk_w, counts, offsets and perm as in ds4moe_route, each may be
- * NULL; counts, offsets and perm are either all set or all NULL.  out->logits
- * must be NULL (DS4MOE_ERR_UNSUPPORTED).  ws: ds4moe_gate_workspace_bytes. */
+/* Gate T >= 0 tokens (0 = no-op, which leaves every output as it is).
+ * logits: rows of E values, ld elements apart (E <= ld <= 2^24), aligned to
+ * their type; bias: [E] fp32 or NULL.  out (host struct): topk_idx, topk_w,
+ * counts, offsets and perm as in ds4moe_route, each may be NULL; counts,
+ * offsets and perm are either all set or all NULL.  out->logits must be NULL
+ * (DS4MOE_ERR_UNSUPPORTED).  ws: ds4moe_gate_workspace_bytes. */
 int ds4moe_gate(const ds4moe_gating *g, const void *logits, int64_t ld, const float *bias, int32_t T,
                 ds4moe_routing *out, void *ws, size_t ws_bytes, void *stream);
 
@@ -454,8 +455,9 @@ int ds4moe_gate(const ds4moe_gating *g, const void *logits, int64_t ld, const fl
  * as the gate had them (the bias only says which experts are masked: it has no
  * gradient), topk_idx [T,k] the gate's choice (an index outside 0..E-1 takes
  * no part), d_topk_w [T,k] fp32.  d_logits: rows of E values of logits_dtype,
- * ldd elements apart, every one of which is written; computed in fp32 and
- * rounded once.  It must not overlap the logits.  No workspace. */
+ * ldd elements apart (E <= ldd <= 2^24), every one of which is written;
+ * computed in fp32 and rounded once.  It must not overlap the logits.  No
+ * workspace. */
 int ds4moe_gate_backward(const ds4moe_gating *g, const void *logits, int64_t ld, const float *bias,
                          const int32_t *topk_idx, const float *d_topk_w, int32_t T, void *d_logits, int64_t ldd,
                          void *stream);
@@ -488,8 +490,10 @@ int ds4moe_mx4_dequantize(void *dst, int32_t dst_dtype, int64_t ld, const uint8_
  * apart (a multiple of 8, >= K), a_scales NULL.  a_dtype DS4MOE_MX4: codes
  * [M,K/2] and a_scales [M,K/32], lda = K.  K: a multiple of 32 (a quantised
  * matrix of other lengths is filled up to one), 32..2^24; M, N: 0..2^24 (0 =
- * no-op).  y: rows of N values, ldy elements apart, aligned to 16 bytes with
- * ldy free.  a, w 16-byte aligned.  y must not overlap the operands. */
+ * no-op).  A weight beyond bf16 (a magnitude of 2^128 and up) counts as an
+ * infinity against bf16 activations and as its value against 4-bit ones.
+ * y: rows of N values, ldy elements apart, aligned to 16 bytes with ldy free.
+ * a, w 16-byte aligned.  y must not overlap the operands. */
 int ds4moe_mx4_matmul(void *y, int32_t y_dtype, int64_t ldy, const void *a, const uint8_t *a_scales, int32_t a_dtype,
                       int64_t lda, const uint8_t *w, const uint8_t *w_scales, int64_t M, int64_t N, int64_t K,
                       void *stream);
@@ -523,12 +527,14 @@ size_t ds4moe_mx4_workspace_bytes(const ds4moe_mx4_dims *dims, int32_t T);
 
 /* y[t] = sum_j topk_w[t,j] Wd_e (silu(Wg_e x_t) * (Wu_e x_t)), e =
  * topk_idx[t,j], summed in the order of the ranks.  x: bf16 rows of hidden
- * values, ldx elements apart (a multiple of 8); routing (host struct):
- * topk_idx, topk_w, counts, offsets and perm, all set, as ds4moe_gate or
- * ds4moe_route leave them (logits is not read).  y [T,hidden] of y_dtype.
+ * values, ldx elements apart (a multiple of 8, at most 2^24); routing (host
+ * struct): topk_idx, topk_w, counts, offsets and perm, all set, as ds4moe_gate
+ * or ds4moe_route leave them (logits is not read).  y [T,hidden] of y_dtype.
  * Products have exact bf16 operands and fp32 sums; the SwiGLU intermediate is
- * held to 16 bits for a bf16 y and to 24 bits for an fp32 y.  A weight beyond bf16 (a scale of 2^126 and up)
- * counts as an infinity.  An index outside 0..E-1 adds nothing to its token. */
+ * held to 16 bits for a bf16 y and to 24 bits for an fp32 y.  A weight beyond
+ * bf16 (a magnitude of 2^128 and up) counts as an infinity, and the results
+ * that it reaches are not finite.  An index outside 0..E-1 adds nothing to its
+ * token. */
 int ds4moe_mx4_experts(const ds4moe_mx4_dims *dims, const ds4moe_mx4_weights *w, const void *x, int64_t ldx, int32_t T,
                        const ds4moe_routing *routing, void *y, void *ws, size_t ws_bytes, void *stream);
 
