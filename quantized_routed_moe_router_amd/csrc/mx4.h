@@ -91,9 +91,10 @@ hipError_t launch_mx4_gemm_experts(const Mx4Experts &p, hipStream_t s);  // h an
 hipError_t launch_mx4_gemm(const Mx4Product &p, hipStream_t s);          // bf16 activations, many rows
 hipError_t launch_mx4_gemm4(const Mx4Product &p, hipStream_t s);         // 4-bit activations, many rows
 constexpr int MX4_FEW = 16;       // tokens that the experts' kernels for few of them take
-// Rows of a product that its kernels for few take (N = K = 4096): bf16
-// activations of 64 rows 23 us there, 25 in the tiled kernel; 4-bit ones of 64
-// rows 16 us, 10 in the tiled kernel, of 32 rows 10 in both.
+// Rows of a product that its kernels for few take.  The rule goes by rows
+// alone, as measured at N = K = 4096: bf16 activations of 64 rows 23 us there,
+// 25 in the tiled kernel; 4-bit ones of 64 rows 16 us, 10 in the tiled kernel,
+// of 32 rows 10 in both.
 constexpr int MX4_FEW_ROWS = 64, MX4_FEW_ROWS4 = 32;
 constexpr int MX4_ONE = 4;   // tokens whose down projection adds the experts up itself
 // bf16 terms that the SwiGLU intermediate is held in, however many tokens a
@@ -102,7 +103,7 @@ constexpr int MX4_ONE = 4;   // tokens whose down projection adds the experts up
 // result's own: 2.3e-3 off the 64-bit values where two leave 1.7e-3)
 inline int mx4_h_planes(bool y_bf16) { return y_bf16 ? 2 : 3; }
 // Whether a call takes the experts' kernels for few tokens: few each, that is
-// (16 tokens with 2 of 8 experts: 103 us there, 44 in the tiled kernels).
+// (16 tokens with 2 of 8 experts: 103 us there, 47 in the tiled kernels).
 inline bool mx4_few(int64_t T, int64_t k, int64_t E) { return T <= MX4_ONE || (T <= MX4_FEW && T * k <= 2 * E); }
 hipError_t launch_mx4_product_few(const Mx4Product &p, hipStream_t s);
 hipError_t launch_mx4_experts_few(const Mx4Experts &p, hipStream_t s);  // h, then ya, or y for up to MX4_ONE tokens

@@ -155,7 +155,8 @@ inline unsigned tile_grid(int64_t ntiles, int64_t nrows) { return (unsigned)((nt
 // read takes them there: with the lanes' own order every lane is a piece of
 // its own.  For the gate/up product of 2048 tokens that halved the L1's
 // lookups (205 to 94 million), but they were not what bounds it: with the
-// codes of two stages asked for together the experts took 1108 us for 1117.
+// codes of two stages asked for together the experts took 1108 us for 1117
+// (with one term of the intermediate).
 __device__ __forceinline__ u4 to_lanes(u4 v) {
   const int l = threadIdx.x & 63, from = ((l & 15) * 4 + (l >> 4)) * 4;
   u4 o;

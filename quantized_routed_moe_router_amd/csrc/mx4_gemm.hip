@@ -17,13 +17,19 @@
 // order, so a wait for activations lets the later codes fly.
 //
 // 2048 tokens, 8 of 256 experts, H = 4096, I = 2048 (64 tokens an expert, a
-// tile each): gate and up 702 us, down 398 (0.8 and 0.7 Pflop/s, 3.3 TB/s of
-// codes); with 8192 tokens 0.94 Pflop/s.  Without their products the kernels
-// take 577 and 348 us, without their loads 600 and 340: both are near what
-// they cost alone, the matrix units are busy 45% of the time, and the clock
-// falls under them (activations of zeros: 10% less time).  Asking for the next
-// tile's codes ahead in L2 made gate and up 817 us; with activations two
-// buffers deep instead of three the whole took 1316 us, not 1117.
+// tile each): gate and up 710 us (0.77 Pflop/s), down 680, which goes over its
+// codes once for each of the intermediate's two terms (0.8 Pflop/s of products
+// issued); for an fp32 result, three terms, the whole takes 1.66 ms, not 1.38.
+// With one term alone down took 398 us.  Without their products gate and up
+// and one term of down take 577 and 348 us, without their loads 600 and 340:
+// both are near what they cost alone, the matrix units are busy 45% of the
+// time, and the clock falls under them (activations of zeros: 10% less time).
+// Gate and up read 3.3 GB for 2.3 GB of codes and scales; the excess fits
+// lines of scales that come again, which are asked for 16 bytes a row at a
+// time, four stages apart (asking for 32 or 64 changed nothing: 742 us, 740).
+// Asking for the next tile's codes ahead in L2 made gate and up 817 us; with
+// activations two buffers deep instead of three the whole, with one term, took
+// 1316 us and not 1117.
 #include "mx4_dev.h"
 
 namespace ds4 {

@@ -10,8 +10,11 @@
 //
 // H = 4096, I = 2048, k = 8 of 256 experts, 13.4 MB each: 16 tokens (about 102
 // experts, fp32 results) take 169 us for gate and up (5.3 TB/s) and 122 for
-// down (3.7 TB/s; 93 in the best call); one token 18.4 us (3.9 TB/s) and 11.8,
-// where the launch and the first loads' latency are 5 us of each.
+// down (3.7 TB/s; from 93 to 173 by the call, with LDS conflicts in 18% of the
+// cycles); one token 18.8 us (3.8 TB/s) and 11.9, where the launch and the
+// first loads' latency are 5 us of each.  H = 7168, two steps of the staged
+// rows of gate and up and 98 KB of LDS, one workgroup a CU: 16 tokens 469 us
+// (474 for their bytes at 5 TB/s), one token 55 (37).
 #include "mx4_dev.h"
 
 namespace ds4 {

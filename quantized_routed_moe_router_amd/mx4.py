@@ -250,7 +250,8 @@ class Mx4Experts:
 
 
 class Mx4Layer:
-    """A routed layer on 4-bit experts: router logits (accumulated in fp64, as ds4moe_route), gate, experts."""
+    """A routed layer on 4-bit experts: router logits (accumulated in fp64, as ds4moe_route), gate, experts.  The router
+    takes hidden sizes that are multiples of 256 and up to 256 experts; gate and experts go further on their own."""
 
     def __init__(self, router_w: torch.Tensor, gate: Gate, experts: Mx4Experts, bias: torch.Tensor | None = None):
         _flat(router_w, "router_w", router_w.dtype, (experts.E, experts.H), experts.device)
