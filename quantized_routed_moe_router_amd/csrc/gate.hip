@@ -14,8 +14,8 @@
 // SIMD instructions issue in less than half of the cycles.  A wave has the
 // whole token in registers, so that no step waits for another wave, and two
 // tokens of 8192.  Measured with 8 of 256 in 8 groups: 1 token 6.9 us, 8192
-// tokens 16.4 us and 7.1 for the places, where each of 256 workgroups reads
-// all of them the counts of 256 chunks; 2048 tokens by softmax 8.3 and 5.2.
+// tokens 16 us and 7 for the places, where each of 256 workgroups reads the
+// counts of all 256 chunks again; 2048 tokens by softmax 8.3 and 5.2.
 #include "mx4.h"
 #include "route_dev.h"
 
@@ -456,7 +456,7 @@ __global__ __launch_bounds__(1024) void k_gate_place(GateArgs a) {
 // and d l = ds * ds/dl; softmax without renormalisation reaches every logit:
 // d l_e = p_e (ds_e - sum_j ds_j p_j).  Softmax with it is a softmax over the
 // chosen logits alone.  A row is read (for the dense form) and written once:
-// 8192 x 256 in fp32, 17 MB, takes 8.3 us for 3.4 us of memory: 2048 short
+// 8192 x 256 in fp32, 17 MB, takes 8.4 us for 3.4 us of memory: 2048 short
 // workgroups of one row a wave, 4 bytes a lane and load and nothing loaded
 // ahead; 1237 x 60 3.9 us.
 template <int NK, bool BF16>

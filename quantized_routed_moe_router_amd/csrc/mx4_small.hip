@@ -9,7 +9,7 @@
 // the tokens; four tokens at a time are staged in LDS and fill four of them.
 //
 // H = 4096, I = 2048, k = 8 of 256 experts, 13.4 MB each: 16 tokens (about 102
-// experts, fp32 results) take 169 us for gate and up (5.3 TB/s) and 122 for
+// experts, fp32 results) take 168 us for gate and up (5.3 TB/s) and 121 for
 // down (3.7 TB/s; from 93 to 173 by the call, with LDS conflicts in 18% of the
 // cycles); one token 18.8 us (3.8 TB/s) and 11.9, where the launch and the
 // first loads' latency are 5 us of each.  H = 7168, two steps of the staged

@@ -53,35 +53,40 @@ def _rows(t: torch.Tensor, what: str, dtypes=_DTYPES) -> int:
     return d if rows > 1 else cols
 
 
-def _untracked(what: str, *tensors) -> None:
-    """No tensor here asks for a gradient that these calls would lose without a word."""
-    for t in tensors:
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{what} asks for a gradient, which autograd does not get from this call: detach it, or call "
-                             "under torch.no_grad() (Gate.backward gives the gradient of a gate's logits)")
+def _tracked(what: str) -> None:
+    """A tensor asks for a gradient: not one that these calls would lose without a word."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{what} asks for a gradient, which autograd does not get from this call: detach it, or call "
+                         "under torch.no_grad() (Gate.backward gives the gradient of a gate's logits)")
 
 
-def _flat(t: torch.Tensor, what: str, dtype, shape=None, dev=None) -> torch.Tensor:
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+def _elsewhere(t: torch.Tensor, what: str, i: int) -> None:
+    raise ValueError(f"{what}: on {t.device}, the call's other tensors on cuda:{i}")
+
+
+def _flat(t: torch.Tensor, what: str, dtype, shape=None, i=None) -> torch.Tensor:
+    """Checked: contiguous, of a type and shape, on a GPU (of index i)."""
+    at = t.get_device()
+    if t.dtype is not dtype or at < 0 or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous {dtype} tensor on the GPU is wanted")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{what}: on {t.device}, the call's other tensors on {dev}")
+    if i is not None and at != i:
+        _elsewhere(t, what, i)
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
     return t
 
 
-def _packed(codes: torch.Tensor, scales: torch.Tensor, what: str, shape=None, dev=None) -> tuple:
-    _flat(codes, what, torch.uint8, None if shape is None else (*shape[:-1], shape[-1] // 2), dev)
-    if codes.shape[-1] % 16:
+def _packed(codes: torch.Tensor, scales: torch.Tensor, what: str, shape=None, i=None) -> tuple:
+    _flat(codes, what, torch.uint8, None if shape is None else (*shape[:-1], shape[-1] // 2), i)
+    *rows, n = codes.shape
+    if n % 16:
         raise ValueError(f"{what}: whole blocks of 32 are wanted")
-    _flat(scales, what + " scales", torch.uint8, (*codes.shape[:-1], codes.shape[-1] // 16), codes.device)
+    _flat(scales, what + " scales", torch.uint8, (*rows, n // 16), codes.get_device())
     return codes, scales
 
 
-def _call(entry, what: str, dev: torch.device, *args) -> None:
-    """A call of the library on a device's current stream, with that device the current one."""
-    i = dev.index
+def _call(entry, what: str, i: int, *args) -> None:
+    """A call of the library on the current stream of device i, with that device the current one."""
     if i == _device():
         status = entry(*args, _raw_stream(i))
     else:
@@ -109,31 +114,32 @@ class Gate:
         if logits.shape[1] != self.E:
             raise ValueError(f"logits: {logits.shape[1]} columns, {self.E} experts")
         if bias is not None:
-            _flat(bias, "bias", torch.float32, (self.E,), logits.device)
+            _flat(bias, "bias", torch.float32, (self.E,), logits.get_device())
         return ld
 
     def forward(self, logits: torch.Tensor, bias: torch.Tensor | None = None) -> dict:
         """topk_idx [T,k], topk_w [T,k], counts [E], offsets [E+1] and perm [T*k] of logits [T,E].  All but topk_w are
         parts of one allocation, which holds as long as one of them does."""
-        _untracked("logits or bias", logits, bias)
-        ld, g, dev = self._logits(logits, bias), self._gating[logits.dtype], logits.device
+        if logits.requires_grad or (bias is not None and bias.requires_grad):
+            _tracked("logits or bias")
+        ld, g, i = self._logits(logits, bias), self._gating[logits.dtype], logits.get_device()
         T, k, E = logits.shape[0], self.k, self.E
         if T == 0:
-            return {n: torch.zeros(s, dtype=torch.float32 if n == "topk_w" else torch.int32, device=dev) for n, s in (
+            return {n: torch.zeros(s, dtype=torch.float32 if n == "topk_w" else torch.int32, device=i) for n, s in (
                 ("topk_idx", (0, k)), ("topk_w", (0, k)), ("counts", E), ("offsets", E + 1), ("perm", 0))}
         # One allocation for the indices; an allocation costs as much as a tenth of a call for one token.  Up to
         # GATE_JOINT tokens the workspace is part of it (first: it wants the alignment): 2048 tokens 13.0 us, 14.2 with
         # one of its own.  Of more tokens the kernels take longer than the call (4096: 14.4 us both ways), and whoever
         # keeps the choice for a backward pass would keep the workspace with it, as much again as the indices.
         n, A = _L.ds4moe_gate_workspace_bytes(g, T), T * k
-        w = _empty(T, k, dtype=torch.float32, device=dev)
+        w = _empty(T, k, dtype=torch.float32, device=i)
         held = n // 4 if T <= GATE_JOINT else 0
-        buf = _empty(held + 2 * A + 2 * E + 1, dtype=torch.int32, device=dev)
+        buf = _empty(held + 2 * A + 2 * E + 1, dtype=torch.int32, device=i)
         _, idx, perm, counts, offsets = _split(buf, (held, A, A, E, E + 1))
         at = buf.data_ptr() + 4 * held
-        own = None if held else _empty(n, dtype=torch.uint8, device=dev)
+        own = None if held else _empty(n, dtype=torch.uint8, device=i)
         ws = buf.data_ptr() if held else own.data_ptr()
-        _call(_L.ds4moe_gate, "gate", dev, g, logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T,
+        _call(_L.ds4moe_gate, "gate", i, g, logits.data_ptr(), ld, None if bias is None else bias.data_ptr(), T,
               ctypes.byref(B.Routing(at, w.data_ptr(), at + 8 * A, at + 8 * A + 4 * E, at + 4 * A, None)), ws, n)
         idx = idx.view(T, k)
         return {"topk_idx": idx, "topk_w": w, "counts": counts, "offsets": offsets, "perm": perm}
@@ -141,12 +147,12 @@ class Gate:
     def backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, d_topk_w: torch.Tensor,
                  bias: torch.Tensor | None = None) -> torch.Tensor:
         """Gradient of the logits (in their type) from the gradient of topk_w."""
-        ld, dev = self._logits(logits, bias), logits.device
+        ld, i = self._logits(logits, bias), logits.get_device()
         T = logits.shape[0]
-        _flat(topk_idx, "topk_idx", torch.int32, (T, self.k), dev)
-        _flat(d_topk_w, "d_topk_w", torch.float32, (T, self.k), dev)
-        out = _empty(T, self.E, dtype=logits.dtype, device=dev)
-        _call(_L.ds4moe_gate_backward, "gate_backward", dev, self._gating[logits.dtype], logits.data_ptr(), ld,
+        _flat(topk_idx, "topk_idx", torch.int32, (T, self.k), i)
+        _flat(d_topk_w, "d_topk_w", torch.float32, (T, self.k), i)
+        out = _empty(T, self.E, dtype=logits.dtype, device=i)
+        _call(_L.ds4moe_gate_backward, "gate_backward", i, self._gating[logits.dtype], logits.data_ptr(), ld,
               None if bias is None else bias.data_ptr(), topk_idx.data_ptr(), d_topk_w.data_ptr(), T, out.data_ptr(),
               self.E)
         return out
@@ -154,13 +160,14 @@ class Gate:
 
 def mx4_quantize(x: torch.Tensor) -> tuple:
     """(codes, scales) of a matrix [rows, cols] in fp32 or bf16; columns are filled up with zeros to blocks of 32."""
-    _untracked("x", x)
-    ld, dev = _rows(x, "x"), x.device
+    if x.requires_grad:
+        _tracked("x")
+    ld, i = _rows(x, "x"), x.get_device()
     rows, cols = x.shape
     nb = (cols + 31) // 32
-    codes = _empty(rows, 16 * nb, dtype=torch.uint8, device=dev)
-    scales = _empty(rows, nb, dtype=torch.uint8, device=dev)
-    _call(_L.ds4moe_mx4_quantize, "mx4_quantize", dev, codes.data_ptr(), scales.data_ptr(), x.data_ptr(),
+    codes = _empty(rows, 16 * nb, dtype=torch.uint8, device=i)
+    scales = _empty(rows, nb, dtype=torch.uint8, device=i)
+    _call(_L.ds4moe_mx4_quantize, "mx4_quantize", i, codes.data_ptr(), scales.data_ptr(), x.data_ptr(),
           _DTYPES[x.dtype], rows, cols, ld)
     return codes, scales
 
@@ -175,9 +182,9 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int | None =
     cols = 32 * nb if cols is None else cols
     if (cols + 31) // 32 != nb:
         raise ValueError(f"{cols} columns are not {nb} blocks")
-    dev = codes.device
-    out = _empty(rows, cols, dtype=dtype, device=dev)
-    _call(_L.ds4moe_mx4_dequantize, "mx4_dequantize", dev, out.data_ptr(), _DTYPES[dtype], cols, codes.data_ptr(),
+    i = codes.get_device()
+    out = _empty(rows, cols, dtype=dtype, device=i)
+    _call(_L.ds4moe_mx4_dequantize, "mx4_dequantize", i, out.data_ptr(), _DTYPES[dtype], cols, codes.data_ptr(),
           scales.data_ptr(), rows, cols)
     return out
 
@@ -185,26 +192,27 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int | None =
 def mx4_matmul(a: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, a_scales: torch.Tensor | None = None,
                y_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """a [M,K] times w [N,K]^T: w in 4-bit form, a bf16, or in 4-bit form with a_scales."""
-    _untracked("a", a)
+    if a.requires_grad:
+        _tracked("a")
     _packed(w, w_scales, "w")
     if w.dim() != 2 or y_dtype not in _DTYPES:
         raise ValueError(f"w: a matrix is wanted, and an fp32 or bf16 result, not {y_dtype}")
-    N, K = w.shape
+    (N, K), i = w.shape, w.get_device()
     K *= 2
     if a_scales is None:
         lda, kind, sa = _rows(a, "a", _BF16), B.DS4MOE_BF16, None
         if a.shape[1] != K:
             raise ValueError(f"a: {a.shape[1]} columns, w has {K}")
-        if a.device != w.device:
-            raise ValueError(f"a: on {a.device}, w on {w.device}")
+        if a.get_device() != i:
+            _elsewhere(a, "a", i)
     else:
-        _packed(a, a_scales, "a", None, w.device)
+        _packed(a, a_scales, "a", None, i)
         if a.dim() != 2 or 2 * a.shape[1] != K:
             raise ValueError(f"a: shape {tuple(a.shape)}, w has {K} columns")
         lda, kind, sa = K, B.DS4MOE_MX4, a_scales.data_ptr()
-    M, dev = a.shape[0], a.device
-    y = _empty(M, N, dtype=y_dtype, device=dev)
-    _call(_L.ds4moe_mx4_matmul, "mx4_matmul", dev, y.data_ptr(), _DTYPES[y_dtype], N, a.data_ptr(), sa, kind, lda,
+    M = a.shape[0]
+    y = _empty(M, N, dtype=y_dtype, device=i)
+    _call(_L.ds4moe_mx4_matmul, "mx4_matmul", i, y.data_ptr(), _DTYPES[y_dtype], N, a.data_ptr(), sa, kind, lda,
           w.data_ptr(), w_scales.data_ptr(), M, N, K)
     return y
 
@@ -221,30 +229,32 @@ class Mx4Experts:
         _need(B.ds4moe_mx4_workspace_bytes(self.dims, 1) > 0, f"unsupported experts: H={H}, I={I}, E={E}, k={k}")
         self.gate = _packed(*gate, "gate", (E, I, H))
         self.device = self.gate[0].device
-        self.up = _packed(*up, "up", (E, I, H), self.device)
-        self.down = _packed(*down, "down", (E, H, I), self.device)
+        self.up = _packed(*up, "up", (E, I, H), self.device.index)
+        self.down = _packed(*down, "down", (E, H, I), self.device.index)
         self._dims = ctypes.byref(self.dims)
         self._weights = ctypes.byref(B.make_mx4_weights(*self.gate, *self.up, *self.down))
 
     def forward(self, x: torch.Tensor, routing: dict) -> torch.Tensor:
         """y [T,H] of bf16 x [T,H]; routing: the dict of Gate.forward or DeviceLayer.route."""
-        _untracked("x or topk_w", x, routing["topk_w"])
+        if x.requires_grad or routing["topk_w"].requires_grad:
+            _tracked("x or topk_w")
         ldx, dev = _rows(x, "x", _BF16), self.device
         T, H = x.shape
         if H != self.H:
             raise ValueError(f"x: {H} columns, hidden size {self.H}")
-        if x.device != dev:
-            raise ValueError(f"x: on {x.device}, the experts on {dev}")
+        i = dev.index
+        if x.get_device() != i:
+            _elsewhere(x, "x", i)
         i32, k, E = torch.int32, self.k, self.E
-        r = B.Routing(_flat(routing["topk_idx"], "topk_idx", i32, (T, k), dev).data_ptr(),
-                      _flat(routing["topk_w"], "topk_w", torch.float32, (T, k), dev).data_ptr(),
-                      _flat(routing["counts"], "counts", i32, (E,), dev).data_ptr(),
-                      _flat(routing["offsets"], "offsets", i32, (E + 1,), dev).data_ptr(),
-                      _flat(routing["perm"], "perm", i32, (T * k,), dev).data_ptr(), None)
+        r = B.Routing(_flat(routing["topk_idx"], "topk_idx", i32, (T, k), i).data_ptr(),
+                      _flat(routing["topk_w"], "topk_w", torch.float32, (T, k), i).data_ptr(),
+                      _flat(routing["counts"], "counts", i32, (E,), i).data_ptr(),
+                      _flat(routing["offsets"], "offsets", i32, (E + 1,), i).data_ptr(),
+                      _flat(routing["perm"], "perm", i32, (T * k,), i).data_ptr(), None)
         n = _L.ds4moe_mx4_workspace_bytes(self._dims, T)
         ws = _empty(n, dtype=torch.uint8, device=dev)
         y = _empty(T, H, dtype=self.y_dtype, device=dev)
-        _call(_L.ds4moe_mx4_experts, "mx4_experts", dev, self._dims, self._weights, x.data_ptr(), ldx, T,
+        _call(_L.ds4moe_mx4_experts, "mx4_experts", i, self._dims, self._weights, x.data_ptr(), ldx, T,
               ctypes.byref(r), y.data_ptr(), ws.data_ptr(), n)
         return y
 
@@ -254,7 +264,7 @@ class Mx4Layer:
     takes hidden sizes that are multiples of 256 and up to 256 experts; gate and experts go further on their own."""
 
     def __init__(self, router_w: torch.Tensor, gate: Gate, experts: Mx4Experts, bias: torch.Tensor | None = None):
-        _flat(router_w, "router_w", router_w.dtype, (experts.E, experts.H), experts.device)
+        _flat(router_w, "router_w", router_w.dtype, (experts.E, experts.H), experts.device.index)
         _need(router_w.dtype in _DTYPES, f"router_w: unsupported type {router_w.dtype}")
         _need((gate.E, gate.k) == (experts.E, experts.k), "gate and experts differ in their numbers of experts or choices")
         self.router_w, self.gate, self.experts, self.bias = router_w, gate, experts, bias
@@ -263,14 +273,15 @@ class Mx4Layer:
               f"unsupported router: hidden size {experts.H}, {experts.E} experts")
 
     def logits(self, x: torch.Tensor) -> torch.Tensor:
-        _untracked("x or router_w", x, self.router_w)
+        if x.requires_grad or self.router_w.requires_grad:
+            _tracked("x or router_w")
         T, dev = x.shape[0], self.experts.device
-        _flat(x, "x", torch.bfloat16, (T, self.experts.H), dev)
+        _flat(x, "x", torch.bfloat16, (T, self.experts.H), dev.index)
         out = torch.empty((T, self.experts.E), dtype=torch.float32, device=dev)
         n = B.ds4moe_workspace_bytes(self._dims, T, B.MODE_ROUTE)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
         w, r = B.make_weights(self.router_w, None, None, None), B.make_routing(logits=out)
-        _call(_L.ds4moe_route, "route", dev, ctypes.byref(self._dims), ctypes.byref(w), x.data_ptr(), T, ctypes.byref(r),
+        _call(_L.ds4moe_route, "route", dev.index, ctypes.byref(self._dims), ctypes.byref(w), x.data_ptr(), T, ctypes.byref(r),
               ws.data_ptr(), n)
         return out
 
