@@ -58,7 +58,13 @@ typedef enum {
   DS4MOE_ERR_HOSTMEM = 8      /* host expert weights are not pinned (device-visible) host memory */
 } ds4moe_status;
 
-typedef enum { DS4MOE_F32 = 0, DS4MOE_BF16 = 1, DS4MOE_MX4 = 2 /* 4-bit microscaled: ds4moe_mx4_matmul */ } ds4moe_dtype;
+typedef enum {
+  DS4MOE_F32 = 0,
+  DS4MOE_BF16 = 1,
+  DS4MOE_MX4 = 2, /* 4-bit microscaled: ds4moe_mx4_matmul */
+  DS4MOE_F16 = 3, /* products grouped by expert and 8-bit operators */
+  DS4MOE_I8 = 4   /* 8-bit integers with a scale per row: ds4moe_int8_matmul, ds4moe_grouped_matmul */
+} ds4moe_dtype;
 
 typedef enum { DS4MOE_MODE_ROUTE = 0, DS4MOE_MODE_DECODE = 1, DS4MOE_MODE_PREFILL = 2 } ds4moe_mode;
 
@@ -537,6 +543,110 @@ size_t ds4moe_mx4_workspace_bytes(const ds4moe_mx4_dims *dims, int32_t T);
  * token. */
 int ds4moe_mx4_experts(const ds4moe_mx4_dims *dims, const ds4moe_mx4_weights *w, const void *x, int64_t ldx, int32_t T,
                        const ds4moe_routing *routing, void *y, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * 8-BIT INTEGERS with one fp32 scale per row: a token of activations, or an
+ * output channel of weights.  A matrix [rows, cols] is codes [rows, K16] with
+ * K16 = cols rounded up to a multiple of 16 (filled with zeros), row by row
+ * without gaps, and scales [rows].
+ *
+ * Quantise: s = max|v| / 127 rounded to fp32 (2^-149 where that gives 0 for a
+ * row that is not all zeros, and no more than 8454659 * 2^98, of which 127 stay
+ * below infinity), each code the integer nearest to v / s, ties to
+ * even, held to +-127.  A row of zeros gets s = 0; a row with a NaN or an
+ * infinity gets s = NaN and codes 0.  src: rows of cols values of src_dtype
+ * (fp32, bf16 or fp16), ld elements apart (ld >= cols), aligned to their type;
+ * codes 16-byte aligned.  rows and cols >= 0 (0 = no-op), cols below 2^31. */
+int ds4moe_int8_quantize(int8_t *codes, float *scales, const void *src, int32_t src_dtype, int64_t rows, int64_t cols,
+                         int64_t ld, void *stream);
+
+/* code * scale in fp32, rounded once to fp32, bf16 or fp16. */
+int ds4moe_int8_dequantize(void *dst, int32_t dst_dtype, int64_t ld, const int8_t *codes, const float *scales,
+                           int64_t rows, int64_t cols, void *stream);
+
+/* Workspace bytes of ds4moe_int8_matmul (256 for a_dtype DS4MOE_I8, which
+ * needs none); never decreases with M.  0 for invalid arguments. */
+size_t ds4moe_int8_workspace_bytes(int64_t M, int64_t K, int32_t a_dtype);
+
+/* y[m,n] = a_scale[m] w_scale[n] sum_k a[m,k] w[n,k], the sum exact in 32-bit
+ * integers, then fp32 products and one rounding to y_dtype (fp32, bf16, fp16).
+ * w: codes [N, K16], w_scales [N].  a_dtype DS4MOE_I8: codes in rows of K
+ * bytes, lda bytes apart, both multiples of 16, and a_scales [M]; ws may be
+ * NULL.  a_dtype fp32, bf16 or fp16: rows of K values (any K, any lda >= K),
+ * a_scales NULL, quantised within the call as ds4moe_int8_quantize does.
+ * K: 1..131056; M, N: 0..2^24 (0 = no-op), M N up to 2^37.  y: rows of N
+ * values, ldy elements apart, aligned to 16 bytes with ldy free.  w, and codes
+ * a, 16-byte aligned.  y must not overlap the operands. */
+int ds4moe_int8_matmul(void *y, int32_t y_dtype, int64_t ldy, const void *a, const float *a_scales, int32_t a_dtype,
+                       int64_t lda, const int8_t *w, const float *w_scales, int64_t M, int64_t N, int64_t K, void *ws,
+                       size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * PRODUCTS GROUPED BY EXPERT, with ragged groups, and their gradients.
+ *
+ *   y[p]  = W_e x[row(p)]                  for offsets[e] <= p < offsets[e+1]
+ *   dx[t] = sum over p with row(p) = t of W_e^T dy[p]
+ *   dW_e  = sum over those p of dy[p] x[row(p)]^T
+ *
+ * with row(p) = perm[p] / top_k (rounded down), as ds4moe_gate's offsets and
+ * permutation have it, or row(p) = p where perm is NULL.  Sums are fp32 (of
+ * 8-bit integers exact in 32 bits) in an order that the sizes fix, with one
+ * rounding at the end; tokens' gradients are added up over the ranks in fp32
+ * and in their order.
+ *
+ * Sizes (host struct).
+ *   dtype      of x, w and dy: DS4MOE_BF16, DS4MOE_F16, or DS4MOE_I8 (no
+ *              gradients: DS4MOE_ERR_UNSUPPORTED)
+ *   y_dtype    of the call's output: DS4MOE_F32, DS4MOE_BF16 or DS4MOE_F16
+ *   n_experts  E: 1..512
+ *   top_k      1..16 (1 without a permutation)
+ *   rows       P, positions: 0..2^24
+ *   tokens     T, rows of x: 0..2^24
+ *   N, K       1..65536; K values make a multiple of 16 bytes; N is a multiple
+ *              of 8 in the gradients; no more than 2^37 values in P by N, P by
+ *              K or E by N by K
+ * w: [E, N, K] without gaps.  x and dy: rows a multiple of 16 bytes apart.
+ * Operands and outputs are 16-byte aligned; an output must not overlap an
+ * operand.
+ *
+ * offsets [E+1] ascend within 0..P.  Positions before the first or behind the
+ * last belong to no expert: their rows of y are zeros, and they add nothing to
+ * a gradient.  Offsets that do not ascend give unspecified values; nothing
+ * outside the arrays is read or written whatever they are.  A perm[p] outside
+ * 0..T*top_k-1 stands for a row of zeros, which gets no gradient. */
+typedef struct {
+  int32_t dtype;
+  int32_t y_dtype;
+  int32_t n_experts;
+  int32_t top_k;
+  int64_t rows;
+  int64_t tokens;
+  int64_t N;
+  int64_t K;
+} ds4moe_grouped_dims;
+
+/* y [P, N], ldy elements apart, every row of which is written.  x: [T, K], ldx
+ * elements apart.  dtype DS4MOE_I8: x_scales [T] and w_scales [E, N], y times
+ * both; NULL otherwise. */
+int ds4moe_grouped_matmul(const ds4moe_grouped_dims *dims, void *y, int64_t ldy, const void *x, int64_t ldx,
+                          const float *x_scales, const void *w, const float *w_scales, const int32_t *offsets,
+                          const int32_t *perm, void *stream);
+
+/* Workspace bytes of ds4moe_grouped_dx with a permutation.  0 for NULL or
+ * invalid arguments. */
+size_t ds4moe_grouped_workspace_bytes(const ds4moe_grouped_dims *dims);
+
+/* dx [T, K], lddx elements apart, every row of which is written.  dy: [P, N],
+ * lddy elements apart.  Without perm P = T and no workspace is needed.  With
+ * it an assignment (a value of perm) may be absent, and adds nothing; one that
+ * stands twice counts with its last position alone. */
+int ds4moe_grouped_dx(const ds4moe_grouped_dims *dims, void *dx, int64_t lddx, const void *dy, int64_t lddy, const void *w,
+                      const int32_t *offsets, const int32_t *perm, void *ws, size_t ws_bytes, void *stream);
+
+/* dW [E, N, K] without gaps, every matrix of which is written (zeros for an
+ * expert without rows).  No workspace. */
+int ds4moe_grouped_dw(const ds4moe_grouped_dims *dims, void *dw, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                      const int32_t *offsets, const int32_t *perm, void *stream);
 
 /* Static description of a status code (never NULL). */
 const char *ds4moe_status_str(int status);

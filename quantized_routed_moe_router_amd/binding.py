@@ -28,6 +28,8 @@ DS4MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 DS4MOE_F32 = 0
 DS4MOE_BF16 = 1
 DS4MOE_MX4 = 2
+DS4MOE_F16 = 3
+DS4MOE_I8 = 4
 SCORE_SQRT_SOFTPLUS, SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1, 2
 MODE_ROUTE, MODE_DECODE, MODE_PREFILL = 0, 1, 2
 
@@ -39,7 +41,9 @@ EXPORTED = ("ds4moe_packed_bytes", "ds4moe_packed_bytes_bits", "ds4moe_pack_q2k"
             "ds4moe_forward_decode_noalloc",
             "ds4moe_read_probe",
             "ds4moe_gate_workspace_bytes", "ds4moe_gate", "ds4moe_gate_backward", "ds4moe_mx4_quantize",
-            "ds4moe_mx4_dequantize", "ds4moe_mx4_matmul", "ds4moe_mx4_workspace_bytes", "ds4moe_mx4_experts")
+            "ds4moe_mx4_dequantize", "ds4moe_mx4_matmul", "ds4moe_mx4_workspace_bytes", "ds4moe_mx4_experts",
+            "ds4moe_int8_quantize", "ds4moe_int8_dequantize", "ds4moe_int8_workspace_bytes", "ds4moe_int8_matmul",
+            "ds4moe_grouped_matmul", "ds4moe_grouped_workspace_bytes", "ds4moe_grouped_dx", "ds4moe_grouped_dw")
 N_TIMED_KERNELS = 11
 KERNEL_SLOTS = ("router", "route", "permute", "gateup", "down", "shared_gateup", "shared_down", "combine",
                 "cache_plan", "cache_fill", "shared_convert")
@@ -74,6 +78,12 @@ class Mx4Dims(ctypes.Structure):
 class Mx4Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("gate", "gate_scales", "up", "up_scales", "down", "down_scales")]
+
+
+class GroupedDims(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("n_experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("rows", ctypes.c_int64), ("tokens", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64)]
 
 
 class Ds4MoeError(RuntimeError):
@@ -127,6 +137,16 @@ def lib() -> ctypes.CDLL:
         L.ds4moe_mx4_workspace_bytes.argtypes = [P, I32]
         L.ds4moe_mx4_workspace_bytes.restype = ctypes.c_size_t
         L.ds4moe_mx4_experts.argtypes = [P, P, P, I64, I32, P, P, P, ctypes.c_size_t, P]
+        L.ds4moe_int8_quantize.argtypes = [P, P, P, I32, I64, I64, I64, P]
+        L.ds4moe_int8_dequantize.argtypes = [P, I32, I64, P, P, I64, I64, P]
+        L.ds4moe_int8_workspace_bytes.argtypes = [I64, I64, I32]
+        L.ds4moe_int8_workspace_bytes.restype = ctypes.c_size_t
+        L.ds4moe_int8_matmul.argtypes = [P, I32, I64, P, P, I32, I64, P, P, I64, I64, I64, P, ctypes.c_size_t, P]
+        L.ds4moe_grouped_matmul.argtypes = [P, P, I64, P, I64, P, P, P, P, P, P]
+        L.ds4moe_grouped_workspace_bytes.argtypes = [P]
+        L.ds4moe_grouped_workspace_bytes.restype = ctypes.c_size_t
+        L.ds4moe_grouped_dx.argtypes = [P, P, I64, P, I64, P, P, P, P, ctypes.c_size_t, P]
+        L.ds4moe_grouped_dw.argtypes = [P, P, P, I64, P, I64, P, P, P]
         L.ds4moe_status_str.argtypes = [ctypes.c_int]
         L.ds4moe_status_str.restype = ctypes.c_char_p
         L.ds4moe_version.restype = ctypes.c_int
@@ -135,7 +155,9 @@ def lib() -> ctypes.CDLL:
                    "ds4moe_cache_stats",
                    "ds4moe_forward_decode", "ds4moe_forward_decode_noalloc", "ds4moe_read_probe",
                    "ds4moe_forward_prefill", "ds4moe_forward_timed", "ds4moe_gate", "ds4moe_gate_backward",
-                   "ds4moe_mx4_quantize", "ds4moe_mx4_dequantize", "ds4moe_mx4_matmul", "ds4moe_mx4_experts"):
+                   "ds4moe_mx4_quantize", "ds4moe_mx4_dequantize", "ds4moe_mx4_matmul", "ds4moe_mx4_experts",
+                   "ds4moe_int8_quantize", "ds4moe_int8_dequantize", "ds4moe_int8_matmul", "ds4moe_grouped_matmul",
+                   "ds4moe_grouped_dx", "ds4moe_grouped_dw"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -190,6 +212,10 @@ def make_mx4_dims(H, I, E, k, y_dtype=DS4MOE_BF16) -> Mx4Dims:
 
 def make_mx4_weights(gate, gate_scales, up, up_scales, down, down_scales) -> Mx4Weights:
     return Mx4Weights(*(_ptr(t) for t in (gate, gate_scales, up, up_scales, down, down_scales)))
+
+
+def make_grouped_dims(N, K, E, k, rows, tokens, dtype=DS4MOE_BF16, y_dtype=DS4MOE_BF16) -> GroupedDims:
+    return GroupedDims(dtype, y_dtype, E, k, rows, tokens, N, K)
 
 
 # ---------------------------------------------------------------- entry points
@@ -351,3 +377,44 @@ def ds4moe_mx4_experts(dims: Mx4Dims, weights: Mx4Weights, x, ldx: int, T: int, 
                        stream=None) -> None:
     _check(lib().ds4moe_mx4_experts(ctypes.byref(dims), ctypes.byref(weights), _ptr(x), ldx, T, ctypes.byref(routing),
                                     _ptr(y), _ptr(ws), ws_bytes, _stream(stream)), "mx4_experts")
+
+
+def ds4moe_int8_quantize(codes, scales, src, src_dtype: int, rows: int, cols: int, ld: int, stream=None) -> None:
+    _check(lib().ds4moe_int8_quantize(_ptr(codes), _ptr(scales), _ptr(src), src_dtype, rows, cols, ld,
+                                      _stream(stream)), "int8_quantize")
+
+
+def ds4moe_int8_dequantize(dst, dst_dtype: int, ld: int, codes, scales, rows: int, cols: int, stream=None) -> None:
+    _check(lib().ds4moe_int8_dequantize(_ptr(dst), dst_dtype, ld, _ptr(codes), _ptr(scales), rows, cols,
+                                        _stream(stream)), "int8_dequantize")
+
+
+def ds4moe_int8_workspace_bytes(M: int, K: int, a_dtype: int) -> int:
+    return int(lib().ds4moe_int8_workspace_bytes(M, K, a_dtype))
+
+
+def ds4moe_int8_matmul(y, y_dtype: int, ldy: int, a, a_scales, a_dtype: int, lda: int, w, w_scales, M: int, N: int,
+                       K: int, ws=None, ws_bytes: int = 0, stream=None) -> None:
+    _check(lib().ds4moe_int8_matmul(_ptr(y), y_dtype, ldy, _ptr(a), _ptr(a_scales), a_dtype, lda, _ptr(w),
+                                    _ptr(w_scales), M, N, K, _ptr(ws), ws_bytes, _stream(stream)), "int8_matmul")
+
+
+def ds4moe_grouped_matmul(dims: GroupedDims, y, ldy: int, x, ldx: int, x_scales, w, w_scales, offsets, perm,
+                          stream=None) -> None:
+    _check(lib().ds4moe_grouped_matmul(ctypes.byref(dims), _ptr(y), ldy, _ptr(x), ldx, _ptr(x_scales), _ptr(w),
+                                       _ptr(w_scales), _ptr(offsets), _ptr(perm), _stream(stream)), "grouped_matmul")
+
+
+def ds4moe_grouped_workspace_bytes(dims: GroupedDims) -> int:
+    return int(lib().ds4moe_grouped_workspace_bytes(ctypes.byref(dims)))
+
+
+def ds4moe_grouped_dx(dims: GroupedDims, dx, lddx: int, dy, lddy: int, w, offsets, perm, ws=None, ws_bytes: int = 0,
+                      stream=None) -> None:
+    _check(lib().ds4moe_grouped_dx(ctypes.byref(dims), _ptr(dx), lddx, _ptr(dy), lddy, _ptr(w), _ptr(offsets),
+                                   _ptr(perm), _ptr(ws), ws_bytes, _stream(stream)), "grouped_dx")
+
+
+def ds4moe_grouped_dw(dims: GroupedDims, dw, dy, lddy: int, x, ldx: int, offsets, perm, stream=None) -> None:
+    _check(lib().ds4moe_grouped_dw(ctypes.byref(dims), _ptr(dw), _ptr(dy), lddy, _ptr(x), ldx, _ptr(offsets),
+                                   _ptr(perm), _stream(stream)), "grouped_dw")

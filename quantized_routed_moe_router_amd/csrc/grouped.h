@@ -1,0 +1,60 @@
+// Launch wrappers of the products grouped by expert, their gradients and the
+// 8-bit integer operators (internal to the library).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ds4 {
+
+constexpr int GROUPED_EXPERTS = 512;  // the most experts (eight per lane of the wave that looks for a tile)
+
+// y[p] = W_e x[row(p)] for offsets[e] <= p < offsets[e+1]
+struct Grouped {
+  void *y;                    // [P, ldy]
+  int64_t ldy;                // elements
+  int32_t y_type;             // ds4moe_dtype: fp32, bf16 or fp16
+  int32_t type;               // of the operands: bf16, fp16 or 8-bit integers
+  const char *x;              // rows of Kb bytes
+  int64_t ldx;                // bytes
+  const char *w;              // [E][N] rows of Kb bytes
+  const float *xs, *ws;       // scales [T] and [E, N] of 8-bit operands
+  const int32_t *offsets;     // [E + 1], or null: one group of all rows
+  const int32_t *perm;        // [P]: row perm[p] / k, or null: row p
+  int32_t E, k, P, T;
+  uint32_t k_inv;             // ceil(2^32 / k), 0 for k = 1
+  int64_t N, Kb;
+};
+hipError_t launch_grouped(const Grouped &p, hipStream_t s);
+hipError_t launch_grouped_few(const Grouped &p, int rows, hipStream_t s);
+
+// dx[p] = W_e^T dy[p], or dW_e = sum_p dy[p] x[row(p)]^T
+struct GroupedGrad {
+  void *out;                  // dx [P, ldo] or dW [E, N, K]
+  int64_t ldo;                // elements
+  int32_t o_type, type;
+  const char *dy;             // [P] rows of N values
+  int64_t lddy;               // bytes
+  const char *x;              // rows of K values
+  int64_t ldx;                // bytes
+  const char *w;              // [E, N, K]
+  const int32_t *offsets, *perm;
+  int32_t E, k, P, T;
+  uint32_t k_inv;
+  int64_t N, K;
+};
+hipError_t launch_grouped_dx(const GroupedGrad &p, hipStream_t s);
+hipError_t launch_grouped_dw(const GroupedGrad &p, hipStream_t s);
+
+// dx[t] = sum over j of rows[inv[t k + j]], in the order of j; places[t k + j] of perm, -1 where none
+hipError_t launch_grouped_places(int32_t *places, const int32_t *perm, int32_t P, int32_t A, hipStream_t s);
+hipError_t launch_grouped_add_up(void *dx, int64_t ldo, int32_t o_type, const float *rows, const int32_t *places,
+                                 int32_t T, int32_t k, int64_t K, hipStream_t s);
+
+// ---------------------------------------------------------------- 8-bit integers
+hipError_t launch_int8_quantize(int8_t *codes, float *scales, const void *src, int32_t type, int64_t rows, int64_t cols,
+                                int64_t ld, hipStream_t s);
+hipError_t launch_int8_dequantize(void *dst, int32_t type, int64_t ld, const int8_t *codes, const float *scales,
+                                  int64_t rows, int64_t cols, hipStream_t s);
+
+}  // namespace ds4
