@@ -571,8 +571,8 @@ size_t ds4moe_int8_workspace_bytes(int64_t M, int64_t K, int32_t a_dtype);
 /* y[m,n] = a_scale[m] w_scale[n] sum_k a[m,k] w[n,k], the sum exact in 32-bit
  * integers, then fp32 products and one rounding to y_dtype (fp32, bf16, fp16).
  * w: codes [N, K16], w_scales [N].  a_dtype DS4MOE_I8: codes in rows of K
- * bytes, lda bytes apart, both multiples of 16, and a_scales [M]; ws may be
- * NULL.  a_dtype fp32, bf16 or fp16: rows of K values (any K, any lda >= K),
+ * bytes, lda (at most 2^22) bytes apart, both multiples of 16, and a_scales
+ * [M]; ws may be NULL.  a_dtype fp32, bf16 or fp16: rows of K values (any K, any lda >= K),
  * a_scales NULL, quantised within the call as ds4moe_int8_quantize does.
  * K: 1..131056; M, N: 0..2^24 (0 = no-op), M N up to 2^37.  y: rows of N
  * values, ldy elements apart, aligned to 16 bytes with ldy free.  w, and codes
@@ -605,7 +605,8 @@ int ds4moe_int8_matmul(void *y, int32_t y_dtype, int64_t ldy, const void *a, con
  *   N, K       1..65536; K values make a multiple of 16 bytes; N is a multiple
  *              of 8 in the gradients; no more than 2^37 values in P by N, P by
  *              K or E by N by K
- * w: [E, N, K] without gaps.  x and dy: rows a multiple of 16 bytes apart.
+ * w: [E, N, K] without gaps.  x and dy: rows a multiple of 16 bytes and at
+ * most 2^22 values apart.
  * Operands and outputs are 16-byte aligned; an output must not overlap an
  * operand.
  *

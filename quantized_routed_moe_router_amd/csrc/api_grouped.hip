@@ -14,6 +14,7 @@ constexpr int64_t kMaxRows = (int64_t)1 << 24;
 constexpr int64_t kMaxDim = 65536;
 constexpr int64_t kMaxOut = (int64_t)1 << 37;  // values of a matrix (more than memory holds; keeps grids within 2^32 threads)
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
+constexpr int64_t kMaxRow = (int64_t)1 << 22;  // values from row to row of an operand
 constexpr int64_t kMaxSum8 = 131056;  // columns of 8-bit products: their sums stay in 32 bits at 128 x 128 a product
 
 inline size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -42,8 +43,8 @@ int validate_grad(const ds4moe_grouped_dims *d) {
   if (!half_dtype(d->dtype)) return DS4MOE_ERR_UNSUPPORTED;
   return d->N % 8 ? DS4MOE_ERR_SHAPE : DS4MOE_OK;
 }
-// rows of `cols` values of operands, ld apart
-inline bool row_step(int64_t ld, int64_t cols, int32_t dtype) { return ld >= cols && ld <= kMaxLd && ld * elem(dtype) % 16 == 0; }
+// rows of `cols` values of operands, ld apart: 256 of them are within 32-bit offsets
+inline bool row_step(int64_t ld, int64_t cols, int32_t dtype) { return ld >= cols && ld <= kMaxRow && ld * elem(dtype) % 16 == 0; }
 
 struct DxLayout {
   size_t rows, places, total;
@@ -121,21 +122,23 @@ int ds4moe_grouped_dx(const ds4moe_grouped_dims *dims, void *dx, int64_t lddx, c
   const hipStream_t s = (hipStream_t)stream;
   float *const rows = reinterpret_cast<float *>((char *)ws + L.rows);
   int32_t *const places = reinterpret_cast<int32_t *>((char *)ws + L.places);
-  GroupedGrad p{};
-  p.out = perm ? rows : dx;
-  p.ldo = perm ? d.K : lddx;
-  p.o_type = perm ? DS4MOE_F32 : d.y_dtype;
+  Grouped p{};
+  p.y = perm ? rows : dx;
+  p.ldy = perm ? d.K : lddx;
+  p.y_type = perm ? DS4MOE_F32 : d.y_dtype;
   p.type = d.dtype;
-  p.dy = (const char *)dy;
-  p.lddy = lddy * elem(d.dtype);
+  p.x = (const char *)dy;
+  p.ldx = lddy * elem(d.dtype);
   p.w = (const char *)w;
+  p.turned = true;
   p.offsets = offsets;
   p.E = d.n_experts;
-  p.P = (int32_t)d.rows;
-  p.N = d.N;
-  p.K = d.K;
+  p.k = 1;
+  p.P = p.T = (int32_t)d.rows;
+  p.N = d.K;
+  p.Kb = d.N * elem(d.dtype);
   hipError_t e = hipSuccess;
-  if (d.rows) e = launch_grouped_dx(p, s);
+  if (d.rows) e = launch_grouped(p, s);
   if (e != hipSuccess || !perm) return hip_status(e);
   e = launch_grouped_places(places, perm, (int32_t)d.rows, (int32_t)(d.tokens * d.top_k), s);
   if (e != hipSuccess) return hip_status(e);
@@ -152,9 +155,9 @@ int ds4moe_grouped_dw(const ds4moe_grouped_dims *dims, void *dw, const void *dy,
   if (!dw || !offsets || (d.rows && (!dy || !x))) return DS4MOE_ERR_NULL;
   if (!aligned(dw, 16) || !aligned(dy, 16) || !aligned(x, 16) || !aligned(offsets, 4) || !aligned(perm, 4))
     return DS4MOE_ERR_ALIGN;
-  GroupedGrad p{};
-  p.out = dw;
-  p.o_type = d.y_dtype;
+  GroupedDw p{};
+  p.dw = dw;
+  p.dw_type = d.y_dtype;
   p.type = d.dtype;
   p.dy = (const char *)dy;
   p.lddy = lddy * elem(d.dtype);
@@ -206,7 +209,7 @@ int ds4moe_int8_matmul(void *y, int32_t y_dtype, int64_t ldy, const void *a, con
   const bool codes = a_dtype == DS4MOE_I8;
   if (!real_dtype(y_dtype) || (!codes && !real_dtype(a_dtype))) return DS4MOE_ERR_DTYPE;
   if (M < 0 || N < 0 || M > kMaxRows || N > kMaxRows || K < 1 || K > kMaxSum8) return DS4MOE_ERR_SHAPE;
-  if (M * N > kMaxOut || ldy < N || ldy > kMaxLd || lda < K || lda > kMaxLd) return DS4MOE_ERR_SHAPE;
+  if (M * N > kMaxOut || ldy < N || ldy > kMaxLd || lda < K || lda > (codes ? kMaxRow : kMaxLd)) return DS4MOE_ERR_SHAPE;
   if (codes && (K % 16 || lda % 16)) return DS4MOE_ERR_SHAPE;
   if (M == 0 || N == 0) return DS4MOE_OK;
   if (!y || !a || !w || !w_scales) return DS4MOE_ERR_NULL;

@@ -9,7 +9,8 @@ namespace ds4 {
 
 constexpr int GROUPED_EXPERTS = 512;  // the most experts (eight per lane of the wave that looks for a tile)
 
-// y[p] = W_e x[row(p)] for offsets[e] <= p < offsets[e+1]
+// y[p] = W_e x[row(p)] for offsets[e] <= p < offsets[e+1], or W_e^T x[row(p)]
+// (turned: the gradient of the rows)
 struct Grouped {
   void *y;                    // [P, ldy]
   int64_t ldy;                // elements
@@ -17,7 +18,8 @@ struct Grouped {
   int32_t type;               // of the operands: bf16, fp16 or 8-bit integers
   const char *x;              // rows of Kb bytes
   int64_t ldx;                // bytes
-  const char *w;              // [E][N] rows of Kb bytes
+  const char *w;              // [E][N] rows of Kb bytes; turned: [E][Kb / 2] rows of N values of 16 bits
+  bool turned;
   const float *xs, *ws;       // scales [T] and [E, N] of 8-bit operands
   const int32_t *offsets;     // [E + 1], or null: one group of all rows
   const int32_t *perm;        // [P]: row perm[p] / k, or null: row p
@@ -28,23 +30,20 @@ struct Grouped {
 hipError_t launch_grouped(const Grouped &p, hipStream_t s);
 hipError_t launch_grouped_few(const Grouped &p, int rows, hipStream_t s);
 
-// dx[p] = W_e^T dy[p], or dW_e = sum_p dy[p] x[row(p)]^T
-struct GroupedGrad {
-  void *out;                  // dx [P, ldo] or dW [E, N, K]
-  int64_t ldo;                // elements
-  int32_t o_type, type;
+// dW_e = sum over p of dy[p] x[row(p)]^T
+struct GroupedDw {
+  void *dw;                   // [E, N, K]
+  int32_t dw_type, type;
   const char *dy;             // [P] rows of N values
   int64_t lddy;               // bytes
   const char *x;              // rows of K values
   int64_t ldx;                // bytes
-  const char *w;              // [E, N, K]
   const int32_t *offsets, *perm;
   int32_t E, k, P, T;
   uint32_t k_inv;
   int64_t N, K;
 };
-hipError_t launch_grouped_dx(const GroupedGrad &p, hipStream_t s);
-hipError_t launch_grouped_dw(const GroupedGrad &p, hipStream_t s);
+hipError_t launch_grouped_dw(const GroupedDw &p, hipStream_t s);
 
 // dx[t] = sum over j of rows[inv[t k + j]], in the order of j; places[t k + j] of perm, -1 where none
 hipError_t launch_grouped_places(int32_t *places, const int32_t *perm, int32_t P, int32_t A, hipStream_t s);

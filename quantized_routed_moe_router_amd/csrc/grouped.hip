@@ -1,74 +1,70 @@
 // Products grouped by expert, y[p] = W_e x[row(p)], of bf16, fp16 or 8-bit
-// integer operands, and the dense product of 8-bit integers, which is one
-// group of all rows.
+// integer operands; the dense product of 8-bit integers, which is one group of
+// all rows; and the gradient of the rows, dx[p] = W_e^T dy[p], which is the
+// same product of weights that lie across.
 //
-// A workgroup has BM rows of one expert and BN of its weight rows.  Both are
-// staged in LDS, 128 bytes of a row (64 or 128 columns) at a time, by loads
-// that bypass the registers, NB buffers deep; WM x WN waves share the tile.
-// Weights are the matrix instructions' rows and activations their columns:
-// row 4 g + v of a wave's i-th group of 16 is weight row 4 NT g + 4 i + v of
-// it, so that a lane's results are 4 NT adjacent columns of one row of y.
+// A workgroup of WN waves has up to 256 rows of one expert and 32 WN columns
+// of y, 32 a wave.  Both operands are staged in LDS, 128 bytes of a row (64 or
+// 128 terms of the sums) at a time, by loads that bypass the registers.
+// Weights are the matrix instructions' rows and activations their columns: row
+// 4 g + v of a wave's i-th group of 16 is column 8 g + 4 i + v of it, so that a
+// lane's results are 8 adjacent columns of one row of y.
 #include "grouped_dev.h"
 
 namespace ds4 {
 
 namespace {
 
-template <class OP, int BM, int BN, int WM, int WN, int NB>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_grouped(Grouped p, int ntiles) {
-  constexpr int WAVES = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
-  constexpr int STAGE = (BM + BN) * 128, DA = BM / 8 / WAVES, DB = BN / 8 / WAVES;  // loads of 8 rows per wave
-  static_assert(DA * 8 * WAVES == BM && DB * 8 * WAVES == BN && BN / WN % 64 == 0, "whole loads, whole groups");
-  __shared__ __attribute__((aligned(16))) char lds[NB * STAGE];
+constexpr int LDS_PER_WAVE = 20 << 10;
+
+// One workgroup's tile: rows t (up to 16 MT), columns n0 .. of its expert, in
+// NB buffers of stages.  FAR: rows of x that 32-bit offsets do not reach.
+template <class OP, bool TURNED, int WN, int MT, int NB, bool FAR>
+__device__ __forceinline__ void multiply_tile(const Grouped &p, const Segment &t, int64_t n0, char *lds) {
+  constexpr int NT = 2, DA = (2 * MT + WN - 1) / WN, DB = 4;  // groups of 16 weight rows; loads of 8 rows per wave
+  constexpr int BOFF = DA * WN * 1024, STAGE = BOFF + DB * WN * 1024;
+  static_assert(NB * STAGE <= WN * LDS_PER_WAVE, "the buffers fit");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
-  const int wm = wave / WN, wn = wave % WN;
-  Finder<BM> f;
-  const int mtiles = f.count(p.offsets, p.E, p.P);
-  int mt, nt;
-  if (!place_tile<4>(blockIdx.x, mtiles, ntiles, mt, nt)) return;
-  const Segment t = f.find(mt);
-  const int64_t n0 = (int64_t)nt * BN;
-  if (t.e < 0) {
-    zero_rows(p.y, p.y_type, p.ldy, t.p0, t.n, n0, min(n0 + BN, p.N));
-    return;
-  }
-  const char *const zeros = (const char *)kZeros;
   const int last = (int)((p.Kb + 127) / 128) - 1, edge = (int)(p.Kb - (int64_t)last * 128) / 16;  // chunks of the last stage
 
-  // The lane's source of load q: row 8 (q WAVES + wave) + lane / 8, its chunk
-  // by the place that lane l's bytes get.  Rows past the end repeat the last
-  // one (their results are not stored).
-  const char *sa[DA], *sb[DB];
-  int step[DA], ca[DA], cb[DB];
+  // The lane's source of load q: row 8 (q WN + wave) + lane / 8, its chunk by
+  // the place that lane l's bytes get.  Rows past the end, and rows that the
+  // permutation does not name, are zeros.
+  const char *const we = p.w + (TURNED ? (int64_t)t.e * p.N * p.Kb + n0 * 2 : ((int64_t)t.e * p.N + n0) * p.Kb);
+  const int64_t wbytes = TURNED ? p.N * p.Kb - n0 * 2 : (p.N - n0) * p.Kb;  // to the matrix' end
+  const int64_t x0 = p.perm ? 0 : t.p0;  // the row that offsets count from
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x + x0 * p.ldx, range_of((p.T - x0 - 1) * p.ldx + p.Kb));
+  auto row = [&](int q) { return (q * WN + wave) * 8 + (lane >> 3); };
+  auto chunk_a = [&](int q) { return (lane & 7) ^ place8(row(q) & 15); };
+  auto chunk_b = [&](int q) { return (lane & 7) ^ place8((row(q) >> 3 & 3) << 2 | (row(q) & 3)); };
+  constexpr int CW = 4 * WN;  // chunks of a row of turned weights
+  auto turned_row = [&](int q) { return (q * WN + wave) * (64 / CW) + lane / CW; };
+  uint32_t sa[DA], sb[DB];
+  int at_x[DA];
 #pragma unroll
   for (int q = 0; q < DA; ++q) {
-    const int row = (q * WAVES + wave) * 8 + (lane >> 3);
-    const int at = row_of(p.perm, p.k_inv, p.T, p.k, t.p0 + min(row, t.n - 1));
-    ca[q] = (lane & 7) ^ place8(row & 15);
-    step[q] = at < 0 ? 0 : 128;
-    sa[q] = at < 0 ? zeros : p.x + at * p.ldx + ca[q] * 16;
+    at_x[q] = row(q) < t.n ? row_of(p.perm, p.k_inv, p.T, p.k, t.p0 + row(q)) : -1;
+    sa[q] = at_x[q] < 0 ? kNowhere : (uint32_t)((at_x[q] - x0) * p.ldx) + chunk_a(q) * 16;
   }
-  const char *const we = p.w + (int64_t)t.e * p.N * p.Kb;
 #pragma unroll
-  for (int q = 0; q < DB; ++q) {
-    const int row = (q * WAVES + wave) * 8 + (lane >> 3), in = row % (16 * NT);
-    cb[q] = (lane & 7) ^ place8((in / (4 * NT)) << 2 | (in & 3));
-    sb[q] = we + min(n0 + row, p.N - 1) * p.Kb + cb[q] * 16;
-  }
+  for (int q = 0; q < DB; ++q)
+    sb[q] = TURNED ? (uint32_t)(turned_row(q) * p.N * 2) + ((lane % CW) ^ across_place(turned_row(q))) * 16
+                   : (uint32_t)(row(q) * p.Kb) + chunk_b(q) * 16;
   auto load = [&](int st, char *to) {
-    const bool short_ = st == last && edge < 8;
+    const bool whole = st < last || edge == 8;
 #pragma unroll
     for (int q = 0; q < DA; ++q) {
-      const char *s = sa[q] + (int64_t)st * step[q];
-      if (short_ && ca[q] >= edge) s = zeros;
-      load_lds16(s, to + (q * WAVES + wave) * 1024);
+      char *const d = to + (q * WN + wave) * 1024;
+      const bool in = whole || chunk_a(q) < edge;
+      if (FAR) load_lds16(in && at_x[q] >= 0 ? p.x + at_x[q] * p.ldx + chunk_a(q) * 16 + (int64_t)st * 128 : (const char *)kZeros, d);
+      else load_stage16(rx, d, in ? sa[q] : kNowhere, st * 128);
     }
+    // turned, a stage is 64 rows, and the range ends with the matrix
+    const int64_t w0 = TURNED ? st * 128 * p.N : 0;
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(we + w0, range_of(wbytes - w0));
 #pragma unroll
-    for (int q = 0; q < DB; ++q) {
-      const char *s = sb[q] + (int64_t)st * 128;
-      if (short_ && cb[q] >= edge) s = zeros;
-      load_lds16(s, to + BM * 128 + (q * WAVES + wave) * 1024);
-    }
+    for (int q = 0; q < DB; ++q)
+      load_stage16(rw, to + BOFF + (q * WN + wave) * 1024, TURNED || whole || chunk_b(q) < edge ? sb[q] : kNowhere, TURNED ? 0 : st * 128);
     asm volatile("" ::: "memory");
   };
   typename OP::Acc acc[NT][MT];
@@ -77,81 +73,172 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_grouped(Grouped p, int ntil
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[i][m] = typename OP::Acc{0, 0, 0, 0};
 
-  const int fa = (wm * 16 * MT + r) * 128, fb = BM * 128 + (wn * 16 * NT + 4 * NT * (r >> 2) + (r & 3)) * 128;
-  const int f0 = (g ^ place8(r)) * 16;
+  // The products of 64 bytes of the rows go in steps of two groups of rows.  A
+  // step's fragments are read under the step before it, those of the next
+  // stage's first step under this one's last, behind a barrier that says that
+  // the next stage has landed and that this one has been read; the buffer that
+  // it frees is filled again at once.
+  constexpr int S = (MT + 1) / 2;
+  const int fa = r * 128, fb = BOFF + (wave * 32 + 8 * (r >> 2) + (r & 3)) * 128, f0 = (g ^ place8(r)) * 16;
+  u4 a[2][2], b[2][NT];
+  auto read_a = [&](const char *x, int u, int j) {
 #pragma unroll
-  for (int i = 0; i < NB - 1; ++i)
+    for (int m = 0; m < 2; ++m)
+      if (2 * j + m < MT) a[(u * S + j) & 1][m] = *reinterpret_cast<const u4 *>(x + fa + (2 * j + m) * 2048 + (f0 ^ 64 * u));
+  };
+  auto read_b = [&](const char *x, int u) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      b[u][i] = TURNED ? read_across(x + BOFF, 64 * WN, 4 * wave, i, u) : *reinterpret_cast<const u4 *>(x + fb + i * 512 + (f0 ^ 64 * u));
+  };
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
     if (i <= last) load(i, lds + i * STAGE);
-  if (last >= NB - 2) wait_vm<(NB - 2) * (DA + DB)>();
+  if (last >= NB - 1) wait_vm<(NB - 1) * (DA + DB)>();
   else wait_vm<0>();
   barrier_keep_loads();
-  const char *x = lds;
-  char *in = lds + (NB - 1) * STAGE;
+  char *x = lds;
+  read_b(x, 0);
+  read_a(x, 0, 0);
   for (int s = 0; s <= last; ++s) {
-    if (s + NB - 1 <= last) load(s + NB - 1, in);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u4 a[MT], b[NT];
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) b[i] = *reinterpret_cast<const u4 *>(x + fb + i * 512 + (f0 ^ 64 * h));
+      for (int j = 0; j < S; ++j) {
+        if (j + 1 < S) read_a(x, u, j + 1);
+        else if (u == 0) {
+          read_b(x, 1);
+          read_a(x, 1, 0);
+        } else if (s < last) {
+          if (s + NB - 1 <= last) wait_vm<(NB - 2) * (DA + DB)>();
+          else wait_vm<0>();
+          barrier_keep_loads();
+          if (s + NB <= last) load(s + NB, x);
+          x = x + STAGE == lds + NB * STAGE ? lds : x + STAGE;
+          read_b(x, 0);
+          read_a(x, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) a[m] = *reinterpret_cast<const u4 *>(x + fa + m * 2048 + (f0 ^ 64 * h));
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < NT; ++i) acc[i][m] = OP::mul(b[i], a[m], acc[i][m]);
-    }
-    if (s + NB - 1 <= last) wait_vm<(NB - 2) * (DA + DB)>();
-    else wait_vm<0>();
-    barrier_keep_loads();
-    x = x + STAGE == lds + NB * STAGE ? lds : x + STAGE;
-    in = in + STAGE == lds + NB * STAGE ? lds : in + STAGE;
+          for (int i = 0; i < NT; ++i)
+            if (2 * j + m < MT) acc[i][2 * j + m] = OP::mul(b[u][i], a[(u * S + j) & 1][m], acc[i][2 * j + m]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
   }
 
   const bool wide = wide_rows(p.y_type, p.ldy);
-  const int64_t n = n0 + wn * 16 * NT + 4 * NT * g;
-  float sw[4 * NT];
+  const int64_t n = n0 + wave * 32 + 8 * g;
+  if (n >= p.N) return;
+  float sw[8];
   if (OP::SCALED) {
 #pragma unroll
-    for (int i = 0; i < 4 * NT; ++i) sw[i] = p.ws[(int64_t)t.e * p.N + min(n + i, p.N - 1)];
+    for (int i = 0; i < 8; ++i) sw[i] = p.ws[(int64_t)t.e * p.N + min(n + i, p.N - 1)];
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int row = wm * 16 * MT + 16 * m + r;
-    if (row >= t.n || n >= p.N) continue;
-    float v[4 * NT];
+    const int at_row = 16 * m + r;
+    if (at_row >= t.n) continue;
     float sx = 1.0f;
     if (OP::SCALED) {
-      const int at = row_of(p.perm, p.k_inv, p.T, p.k, t.p0 + row);
+      const int at = row_of(p.perm, p.k_inv, p.T, p.k, t.p0 + at_row);
       sx = at < 0 ? 0.0f : p.xs[at];
     }
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 4 * NT; ++i) v[i] = OP::SCALED ? (float)acc[i / 4][m][i % 4] * sx * sw[i] : (float)acc[i / 4][m][i % 4];
-    store_values<4 * NT>(p.y, p.y_type, (int64_t)(t.p0 + row) * p.ldy + n, p.N - n, wide, v);
+    for (int i = 0; i < 8; ++i) v[i] = OP::SCALED ? (float)acc[i / 4][m][i % 4] * sx * sw[i] : (float)acc[i / 4][m][i % 4];
+    store_values<8>(p.y, p.y_type, (int64_t)(t.p0 + at_row) * p.ldy + n, p.N - n, wide, v);
   }
 }
 
-template <class OP, int BM, int BN, int WM, int WN, int NB>
-hipError_t tiled(const Grouped &p, hipStream_t s) {
-  const int64_t mt = grouped_max_tiles<BM>(p.offsets, p.E, p.P), nt = (p.N + BN - 1) / BN;
-  hipLaunchKernelGGL((k_grouped<OP, BM, BN, WM, WN, NB>), dim3((unsigned)((mt * nt + 7) / 8 * 8)), dim3(64 * WM * WN), 0, s, p, (int)nt);
+// Eight waves (256 columns) with the LDS of a CU, or four (128 columns) with
+// half of it.  A tile runs in the smallest instance that has its rows.
+template <class OP, bool TURNED, int WN>
+__global__ __launch_bounds__(64 * WN, 2) void k_grouped(Grouped p, int ntiles, int height) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  Finder f;
+  f.load(p.offsets, p.E, p.P);
+  if (height) f.set_height(height);
+  else if (WN == 8) f.choose_height({256, 224, 192, 176, 160, 144, 128}, ntiles, 256);
+  else f.choose_height({192, 160, 128, 64}, ntiles, 512);
+  const int mtiles = f.count();
+  int mt, nt;
+  if (!place_tile<4>(blockIdx.x, mtiles, ntiles, mt, nt)) return;
+  const Segment t = f.find(mt);
+  const int64_t n0 = (int64_t)nt * 32 * WN;
+  if (t.e < 0) zero_rows(p.y, p.y_type, p.ldy, t.p0, t.n, n0, min(n0 + 32 * WN, p.N));
+  else if (t.n <= 64) multiply_tile<OP, TURNED, WN, 4, WN == 8 ? 4 : 3, false>(p, t, n0, lds);
+  else if (t.n <= 128) multiply_tile<OP, TURNED, WN, 8, WN == 8 ? 3 : 2, false>(p, t, n0, lds);
+  else if (t.n <= 160) multiply_tile<OP, TURNED, WN, 10, 2, false>(p, t, n0, lds);
+  else if constexpr (WN == 4) multiply_tile<OP, TURNED, WN, 12, 2, false>(p, t, n0, lds);
+  else if (t.n <= 176) multiply_tile<OP, TURNED, WN, 11, 2, false>(p, t, n0, lds);
+  else if (t.n <= 192) multiply_tile<OP, TURNED, WN, 12, 2, false>(p, t, n0, lds);
+  else if (t.n <= 224) multiply_tile<OP, TURNED, WN, 14, 2, false>(p, t, n0, lds);
+  else multiply_tile<OP, TURNED, WN, 16, 2, false>(p, t, n0, lds);
+}
+template <class OP>
+__global__ __launch_bounds__(512, 2) void k_grouped_far(Grouped p, int ntiles) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  Finder f;
+  f.load(p.offsets, p.E, p.P);
+  f.set_height(128);
+  const int mtiles = f.count();
+  int mt, nt;
+  if (!place_tile<4>(blockIdx.x, mtiles, ntiles, mt, nt)) return;
+  const Segment t = f.find(mt);
+  const int64_t n0 = (int64_t)nt * 256;
+  if (t.e < 0) zero_rows(p.y, p.y_type, p.ldy, t.p0, t.n, n0, min(n0 + 256, p.N));
+  else multiply_tile<OP, false, 8, 8, 3, true>(p, t, n0, lds);
+}
+
+template <int WN>
+dim3 grid(const Grouped &p, int height, int64_t &nt) {
+  const int64_t mt = grouped_max_tiles(p.offsets, p.E, p.P, height);
+  nt = (p.N + 32 * WN - 1) / (32 * WN);
+  return dim3((unsigned)((mt * nt + 7) / 8 * 8));
+}
+template <class OP, bool TURNED, int WN>
+hipError_t tiled(const Grouped &p, int height, hipStream_t s) {
+  int64_t nt;
+  const dim3 g = grid<WN>(p, height ? height : WN == 8 ? 128 : 64, nt);
+  hipLaunchKernelGGL((k_grouped<OP, TURNED, WN>), g, dim3(64 * WN), WN * LDS_PER_WAVE, s, p, (int)nt, height);
+  return hipGetLastError();
+}
+template <class OP>
+hipError_t tiled_far(const Grouped &p, hipStream_t s) {
+  int64_t nt;
+  const dim3 g = grid<8>(p, 128, nt);
+  hipLaunchKernelGGL(k_grouped_far<OP>, g, dim3(512), 8 * LDS_PER_WAVE, s, p, (int)nt);
   return hipGetLastError();
 }
 
-template <class OP>
+// Rules, times in us on one MI355X with bf16 weights of 2048 x 4096 (h: height
+// of the tiles; choice: the height that the kernel finds):
+//   eight waves from P N = 2^25 on: 16384 rows of 8 experts 248 (four waves
+//   257), 16384 of 256 experts 782 (822); below, 8192 of 8 experts 158 (153),
+//   4096 of 256 experts 789 (759), 2048 of 8 experts 59 (54).
+//   Tiles as high as the rows of an expert, so that its weights are read once:
+//   eight waves, 64 rows each, h 128 782 and h 64 920; four waves, 64 rows
+//   each, h 64 28.4, h 128 42.5 and the choice 29.9; 128 rows each, h 64 44.7
+//   and the choice 45.2; 256 rows each, h 64 66 and the choice 55.
+template <class OP, bool TURNED>
 hipError_t choose(const Grouped &p, hipStream_t s) {
-  return tiled<OP, 128, 128, 2, 2, 2>(p, s);
+  const int64_t mean = p.offsets ? p.P / p.E : p.P;  // rows of an expert
+  if (p.P * p.N >= (1 << 25)) return tiled<OP, TURNED, 8>(p, mean <= 128 ? 128 : 0, s);
+  return tiled<OP, TURNED, 4>(p, mean <= 64 ? 64 : 0, s);
 }
 
 }  // namespace
 
 hipError_t launch_grouped(const Grouped &p, hipStream_t s) {
-  const int64_t mean = p.offsets ? p.P / p.E : p.P;  // rows of an expert
-  if (mean <= 16) return launch_grouped_few(p, (int)(mean <= 8 ? 16 : 32), s);
-  if (mean <= 64 && !p.offsets) return launch_grouped_few(p, (int)mean, s);
-  if (p.type == DS4MOE_BF16) return choose<OpBf16>(p, s);
-  if (p.type == DS4MOE_F16) return choose<OpF16>(p, s);
-  return choose<OpI8>(p, s);
+  if (p.turned) return p.type == DS4MOE_BF16 ? choose<OpBf16, true>(p, s) : choose<OpF16, true>(p, s);
+  if (p.offsets ? p.P <= 2 * p.E : p.P <= 64) return launch_grouped_few(p, p.offsets ? 16 : p.P, s);
+  if (p.perm && p.T * p.ldx > kRange)  // rows that 32-bit offsets do not reach
+    return p.type == DS4MOE_BF16 ? tiled_far<OpBf16>(p, s) : p.type == DS4MOE_F16 ? tiled_far<OpF16>(p, s) : tiled_far<OpI8>(p, s);
+  if (p.type == DS4MOE_BF16) return choose<OpBf16, false>(p, s);
+  if (p.type == DS4MOE_F16) return choose<OpF16, false>(p, s);
+  return choose<OpI8, false>(p, s);
 }
 
 }  // namespace ds4

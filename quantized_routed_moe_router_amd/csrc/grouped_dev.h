@@ -38,6 +38,18 @@ struct OpI8 {
 // 16 bytes of zeros in memory, which rows and columns that are not there read
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
+// Loads into LDS by buffer descriptors: a lane's offset at or beyond the range
+// reads zeros without touching memory, and the compiler counts LDS reads apart
+// from these loads (behind loads into LDS by plain addresses it waits for all
+// LDS reads at every one).
+constexpr int64_t kRange = 0xFFFF0000;
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;
+// the range of a descriptor over `bytes` bytes (none if there are less)
+__device__ __forceinline__ uint32_t range_of(int64_t bytes) { return bytes < 0 ? 0u : bytes > kRange ? (uint32_t)kRange : (uint32_t)bytes; }
+__device__ __forceinline__ void load_stage16(__amdgpu_buffer_rsrc_t r, void *lds, uint32_t off, int stage_off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, off, stage_off, 0, 0);
+}
+
 // the row of x of position p, or -1 where the permutation names none
 __device__ __forceinline__ int row_of(const int32_t *perm, uint32_t k_inv, int T, int k, int p) {
   if (!perm) return p < T ? p : -1;
@@ -51,80 +63,154 @@ struct Segment {
   int e, p0, n;
 };
 
-// The tiles of up to BM rows that the experts' segments make, and tile `mt` of
-// them once it is known.  Every wave looks for itself: a lane has up to eight
-// experts, whose loads go out together, and the lanes' sums are added up over
-// the wave; that is cheaper than a kernel that writes a list down first.
+// An operand whose rows are the terms of the sum lies across: it is staged as
+// it lies, 64 rows by the tile's columns, chunk c of 16 bytes of row j in the
+// place c ^ across_place(j), and turned on the way to the registers by the
+// LDS' transposing read, which gives lane i of 16 the column i of four rows.
+// Groups of 16 columns go in pairs: group m of a wave's has columns
+// 32 (m / 2) + 8 a + 4 (m % 2) + b in the place 4 a + b, so that a lane's
+// results of two groups are 8 adjacent columns.
+__device__ __forceinline__ int across_place(int row) { return (row & 3) << 2; }
+// Fragment of group m, half u of the 64 rows (`bytes` each), of columns from chunk c0 on.
+__device__ __forceinline__ u4 read_across(const char *x, int bytes, int c0, int m, int u) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, j = 32 * u + 8 * g + (r >> 2);  // the first of four rows
+  const char *at = x + j * bytes + ((c0 + 4 * (m >> 1) + (r & 3)) ^ across_place(r >> 2)) * 16 + 8 * (m & 1);
+  typedef __attribute__((address_space(3))) s4 lds_s4;
+  const u2 lo = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)at));
+  const u2 hi = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(at + 4 * bytes)));
+  return u4{lo[0], lo[1], hi[0], hi[1]};
+}
+
+// sum over this lane and the lanes before it, inside the vector unit
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int lanes_before(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v += lanes_before<0x111, 0xF>(v);  // 1, 2, 4, 8 lanes before, in a row of 16
+  v += lanes_before<0x112, 0xF>(v);
+  v += lanes_before<0x114, 0xF>(v);
+  v += lanes_before<0x118, 0xF>(v);
+  v += lanes_before<0x142, 0xA>(v);  // the last lane of the row before, in rows 1 and 3
+  return v + lanes_before<0x143, 0xC>(v);  // the last lane of the first half, in the second
+}
+
+// The tiles of up to `height` rows (a multiple of 16, up to 256) that the
+// experts' segments make, and tile `mt` of them once it is known.  Every wave
+// looks for itself: a lane has up to eight experts, whose loads go out
+// together, and the lanes' sums are added up over the wave; that is cheaper
+// than a kernel that writes a list down first.
 // Offsets are held to 0..P, so that whatever they are no row outside the
 // arrays is touched.  Rows before the first and behind the last expert's make
 // tiles of their own (e = -1).
-template <int BM>
 struct Finder {
   static constexpr int PER = GROUPED_EXPERTS / 64;
   int start[PER], rows[PER], lane_sum, incl, tiles, head, first, last;
-  int E, P, per;
+  int E, P, per, height;
+  uint32_t inv;  // ceil(2^32 / height): n / height for n < 2^24
   bool one;
 
   __device__ __forceinline__ int at(const int32_t *o, int e) const { return min(max(o[min(e, E)], 0), P); }
 
-  __device__ __forceinline__ int count(const int32_t *offsets, int E_, int P_) {
+  __device__ __forceinline__ void load(const int32_t *offsets, int E_, int P_) {
     E = E_;
     P = P_;
     one = offsets == nullptr;
-    if (one) return tiles = (P + BM - 1) / BM;
+    if (one) return;
     const int lane = threadIdx.x & 63;
     per = (E + 63) / 64;
     int o[PER + 1];
 #pragma unroll
     for (int i = 0; i <= PER; ++i) o[i] = i <= per ? at(offsets, lane * per + i) : 0;
     first = at(offsets, 0);
-    last = at(offsets, E);
-    lane_sum = 0;
+    last = max(first, at(offsets, E));
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       start[i] = o[i];
       rows[i] = i < per && lane * per + i < E ? max(o[i + 1] - o[i], 0) : 0;
-      lane_sum += (rows[i] + BM - 1) / BM;
     }
-    incl = lane_sum;
+  }
+  __device__ __forceinline__ void set_height(int h) {
+    height = h;
+    inv = (uint32_t)(((1ull << 32) + h - 1) / h);
+  }
+  __device__ __forceinline__ int up(int n) const { return n > 0 ? (int)__umulhi((uint32_t)(n - 1), inv) + 1 : 0; }
+  __device__ __forceinline__ int lane_tiles() const {
+    int n = up(rows[0]);
+    if (per > 1) {  // more than 64 experts
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(incl, d);
-      if (lane >= d) incl += v;
+      for (int i = 1; i < PER; ++i) n += up(rows[i]);
     }
+    return n;
+  }
+
+  // the number of tiles
+  __device__ __forceinline__ int count() {
+    if (one) return tiles = up(P);
+    lane_sum = lane_tiles();
+    incl = wave_scan(lane_sum);
     tiles = __builtin_amdgcn_readlane(incl, 63);
-    head = (first + BM - 1) / BM;
-    return tiles + head + (P - max(first, last) + BM - 1) / BM;
+    head = up(first);
+    return tiles + head + up(P - last);
+  }
+
+  // The height that suits the numbers: tiles run in rounds of as many as the
+  // card holds, and a round lasts about as long as for 64 rows more than its
+  // tiles have.
+  template <int N>
+  __device__ __forceinline__ void choose_height(const int (&heights)[N], int ntiles, int slots) {
+    int64_t best = INT64_MAX;
+    int of = heights[0], n[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      set_height(heights[i]);
+      n[i] = one ? up(P) : lane_tiles();
+    }
+    if (!one) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) n[i] = __builtin_amdgcn_readlane(wave_scan(n[i]), 63);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t rounds = ((int64_t)n[i] * ntiles + slots - 1) / slots, cost = rounds * (heights[i] + 64);
+      if (cost < best) {
+        best = cost;
+        of = heights[i];
+      }
+    }
+    set_height(__builtin_amdgcn_readfirstlane(of));
   }
 
   __device__ __forceinline__ Segment find(int mt) const {
-    if (one) return Segment{0, mt * BM, min(BM, P - mt * BM)};
+    if (one) return Segment{0, mt * height, min(height, P - mt * height)};
     if (mt >= tiles) {
       mt -= tiles;
-      if (mt < head) return Segment{-1, mt * BM, min(BM, first - mt * BM)};
-      const int p0 = max(first, last) + (mt - head) * BM;
-      return Segment{-1, p0, min(BM, P - p0)};
+      if (mt < head) return Segment{-1, mt * height, min(height, first - mt * height)};
+      const int p0 = last + (mt - head) * height;
+      return Segment{-1, p0, min(height, P - p0)};
     }
     const int lane = threadIdx.x & 63;
     const int from = __ffsll((unsigned long long)__ballot(incl > mt)) - 1;
-    int at = mt - (incl - lane_sum), e = 0, p0 = 0, n = 0;
+    int at = mt - (incl - lane_sum), e = lane * per, p0 = start[0] + at * height, n = min(height, rows[0] - at * height);
+    if (per > 1) {
+      at -= up(rows[0]);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int t = (rows[i] + BM - 1) / BM;
-      if (at >= 0 && at < t) {
-        e = lane * per + i;
-        p0 = start[i] + at * BM;
-        n = min(BM, rows[i] - at * BM);
+      for (int i = 1; i < PER; ++i) {
+        const int t = up(rows[i]);
+        if (at >= 0 && at < t) {
+          e = lane * per + i;
+          p0 = start[i] + at * height;
+          n = min(height, rows[i] - at * height);
+        }
+        at -= t;
       }
-      at -= t;
     }
     return Segment{__builtin_amdgcn_readlane(e, from), __builtin_amdgcn_readlane(p0, from), __builtin_amdgcn_readlane(n, from)};
   }
 };
-// what a grid has room for: the most tiles that E segments of P rows can make
-template <int BM>
-inline int64_t grouped_max_tiles(const int32_t *offsets, int64_t E, int64_t P) {
-  return offsets ? P / BM + (P < E + 2 ? P : E + 2) : (P + BM - 1) / BM;
+// what a grid has room for: the most tiles of `height` rows or more that E segments of P rows can make
+inline int64_t grouped_max_tiles(const int32_t *offsets, int64_t E, int64_t P, int64_t height) {
+  return offsets ? P / height + (P < E + 2 ? P : E + 2) : (P + height - 1) / height;
 }
 
 // The workgroup's row tile and column tile.  Consecutive workgroups go to

@@ -20,9 +20,10 @@ __global__ __launch_bounds__(64 * SW, 4) void k_grouped_few(Grouped p) {
   constexpr int U = MT == 1 ? 4 : 2;  // lines of a row on the way at a time
   __shared__ typename OP::Acc part[(SW - 1) * 64 * MT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-  Finder<16 * MT> f;
-  const int tiles = f.count(p.offsets, p.E, p.P);
-  if ((int)blockIdx.y >= tiles) return;
+  Finder f;
+  f.load(p.offsets, p.E, p.P);
+  f.set_height(16 * MT);
+  if ((int)blockIdx.y >= f.count()) return;
   const Segment t = f.find(blockIdx.y);
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   if (t.e < 0) {
@@ -88,7 +89,7 @@ __global__ __launch_bounds__(64 * SW, 4) void k_grouped_few(Grouped p) {
 
 template <class OP, int MT>
 hipError_t few(const Grouped &p, hipStream_t s) {
-  const dim3 g((unsigned)((p.N + 15) / 16), (unsigned)grouped_max_tiles<16 * MT>(p.offsets, p.E, p.P));
+  const dim3 g((unsigned)((p.N + 15) / 16), (unsigned)grouped_max_tiles(p.offsets, p.E, p.P, 16 * MT));
   hipLaunchKernelGGL((k_grouped_few<OP, MT>), g, dim3(64 * SW), 0, s, p);
   return hipGetLastError();
 }

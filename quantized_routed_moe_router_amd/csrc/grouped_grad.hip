@@ -1,126 +1,65 @@
-// Gradients of the products grouped by expert, in bf16 or fp16 operands:
-//   dx[p] = W_e^T dy[p]                 (the sum runs over W's rows)
-//   dW_e  = sum_p dy[p] x[row(p)]^T     (the sum runs over the expert's rows)
+// Gradients of the products grouped by expert: of the weights,
+//   dW_e = sum over p of dy[p] x[row(p)]^T,
+// in bf16 or fp16 operands, and the sum of the gradients of rows that several
+// experts share.  (The gradient of the rows is a product by turned weights.)
 //
-// The forward kernel's tiles and stages, 64 terms of the sum at a time.  An
-// operand whose rows are the terms lies across: W in dx, both in dW.  It is
-// staged as it lies, 64 rows by the tile's columns, and turned on the way to
-// the registers by the LDS' transposing read, which gives lane i of 16 the
-// column i of four rows.
+// A workgroup of WN waves has 16 MT rows and 32 WN columns of one dW_e, 64
+// terms of the sum at a time.  Both operands lie across.
 #include "grouped_dev.h"
 
 namespace ds4 {
 
 namespace {
 
-// four rows of a staged operand at `at` (lane i of 16 points at row i / 4,
-// columns 4 (i % 4) ..): lane i gets column i of them
-__device__ __forceinline__ u2 read_turned(const char *at) {
-  return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)at));
-}
-
-// Places of an operand that lies across: row j (term j) of 64, the tile's
-// columns.  Tile m of a wave's groups of 16 columns has columns 32 (m / 2) +
-// 8 a + 4 (m % 2) + b in the place 4 a + b, so that a lane's results of two
-// tiles are 8 adjacent ones.  Chunk c of 16 bytes of row j goes to c ^ 4 (j % 4).
-__device__ __forceinline__ int across_place(int row) { return (row & 3) << 2; }
-
-// DW: dW (both operands across), otherwise dx (W across)
-template <class OP, bool DW, int BM, int BN, int WM, int WN, int NB>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_grouped_grad(GroupedGrad p, int mtiles_dw, int ntiles) {
-  constexpr int WAVES = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
-  constexpr int STAGE = (BM + BN) * 128, DA = BM / 8 / WAVES, DB = BN / 8 / WAVES;
-  constexpr int CA = BM / 8, CB = BN / 8;  // chunks of a row of an operand that lies across
-  static_assert(BM >= 128 && BN >= 128 && MT % 2 == 0 && NT % 2 == 0, "places of chunks stay in the row");
-  __shared__ __attribute__((aligned(16))) char lds[NB * STAGE];
+// FAR: rows of x that 32-bit offsets do not reach
+template <class OP, int WN, int MT, bool FAR>
+__global__ __launch_bounds__(64 * WN, 2) void k_grouped_dw(GroupedDw p, int mtiles, int ntiles) {
+  constexpr int NT = 2, DA = 2 * MT / WN, DB = 4, CA = 2 * MT, CB = 4 * WN;  // loads per wave; chunks of a staged row
+  constexpr int BOFF = DA * WN * 1024, STAGE = BOFF + DB * WN * 1024;
+  static_assert(DA * WN == 2 * MT && MT % 2 == 0 && CA >= 16 && CB >= 16, "whole loads, places of chunks stay in the row");
+  __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
-  const int wm = wave / WN, wn = wave % WN;
-  Segment t;
-  int64_t m0 = 0;  // dW: the tile's first row
-  int nt;
-  if (DW) {
-    int mt;
-    if (!place_tile<4>(blockIdx.x, p.E * mtiles_dw, ntiles, mt, nt)) return;
-    t.e = mt / mtiles_dw;
-    m0 = (int64_t)(mt - t.e * mtiles_dw) * BM;
-    t.p0 = 0;
-    t.n = p.P;
-    if (p.offsets) {
-      t.p0 = min(max(p.offsets[t.e], 0), p.P);
-      t.n = max(min(max(p.offsets[t.e + 1], 0), p.P) - t.p0, 0);
-    }
-  } else {
-    Finder<BM> f;
-    const int mtiles = f.count(p.offsets, p.E, p.P);
-    int mt;
-    if (!place_tile<4>(blockIdx.x, mtiles, ntiles, mt, nt)) return;
-    t = f.find(mt);
+  int mt, nt;
+  if (!place_tile<4>(blockIdx.x, p.E * mtiles, ntiles, mt, nt)) return;
+  const int e = mt / mtiles;
+  const int64_t m0 = (int64_t)(mt - e * mtiles) * 16 * MT, n0 = (int64_t)nt * 32 * WN;
+  int p0 = 0, n = p.P;
+  if (p.offsets) {
+    p0 = min(max(p.offsets[e], 0), p.P);
+    n = max(min(max(p.offsets[e + 1], 0), p.P) - p0, 0);
   }
-  const int64_t n0 = (int64_t)nt * BN;
-  if (!DW && t.e < 0) {
-    zero_rows(p.out, p.o_type, p.ldo, t.p0, t.n, n0, min(n0 + BN, p.K));
-    return;
-  }
-  const char *const zeros = (const char *)kZeros;
-  const int64_t terms = DW ? t.n : p.N;
-  const int last = (int)((terms + 63) / 64) - 1, edge = (int)(terms - (int64_t)last * 64);  // terms of the last stage
+  const int last = (n + 63) / 64 - 1;
 
-  // this lane's row and column of load q of an operand that lies across
-  auto across_row = [&](int q, int chunks) { return (q * WAVES + wave) * (64 / chunks) + lane / chunks; };
-  auto across_col = [&](int q, int chunks) { return ((lane % chunks) ^ across_place(across_row(q, chunks))) * 8; };
-
-  const char *sa[DA], *sb[DB];
-  int ca[DA], at_x[DB];
-  if (!DW) {
-#pragma unroll
-    for (int q = 0; q < DA; ++q) {
-      const int row = (q * WAVES + wave) * 8 + (lane >> 3);
-      ca[q] = (lane & 7) ^ place8(row & 15);
-      sa[q] = p.dy + (int64_t)(t.p0 + min(row, t.n - 1)) * p.lddy + ca[q] * 16;
-    }
-#pragma unroll
-    for (int q = 0; q < DB; ++q) {
-      const int64_t c = n0 + across_col(q, CB);
-      sb[q] = c < p.K ? p.w + (((int64_t)t.e * p.N + across_row(q, CB)) * p.K + c) * 2 : nullptr;
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < DA; ++q) {
-      const int64_t c = m0 + across_col(q, CA);
-      sa[q] = c < p.N ? p.dy + (int64_t)(t.p0 + across_row(q, CA)) * p.lddy + c * 2 : nullptr;
-    }
-#pragma unroll
-    for (int q = 0; q < DB; ++q) {
-      const int64_t c = n0 + across_col(q, CB);
-      sb[q] = c < p.K ? p.x + c * 2 : nullptr;
-    }
-  }
-  // dW: the rows of x of stage st, asked for a stage ahead of their use
+  // load q of a stage: its rows from (q WN + wave) 64 / C on, chunk by place
+  auto at_row = [&](int q, int chunks) { return (q * WN + wave) * (64 / chunks) + lane / chunks; };
+  auto at_col = [&](int q, int chunks) { return ((lane % chunks) ^ across_place(at_row(q, chunks))) * 16; };
+  const char *const dy = p.dy + p0 * p.lddy + m0 * 2;
+  const int64_t x0 = p.perm ? 0 : p0;  // the row that offsets count from
+  const char *const xe = p.x + x0 * p.ldx + n0 * 2;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xe, range_of((p.T - x0 - 1) * p.ldx + (p.K - n0) * 2));
+  int at_x[DB];
+  // the rows of x of stage st, asked for a stage ahead
   auto find_rows = [&](int st) {
 #pragma unroll
     for (int q = 0; q < DB; ++q) {
-      const int row = st * 64 + across_row(q, CB);
-      at_x[q] = row < t.n ? row_of(p.perm, p.k_inv, p.T, p.k, t.p0 + row) : -1;
+      const int row = st * 64 + at_row(q, CB);
+      at_x[q] = row < n ? row_of(p.perm, p.k_inv, p.T, p.k, p0 + row) : -1;
     }
   };
   auto load = [&](int st, char *to) {
-    const bool short_ = st == last && edge < 64;
+    const int64_t d0 = (int64_t)st * 64 * p.lddy;  // the range ends with the expert's rows: past it are zeros
+    const __amdgpu_buffer_rsrc_t ry = make_rsrc(dy + d0, range_of((n - st * 64 - 1) * p.lddy + (p.N - m0) * 2));
 #pragma unroll
-    for (int q = 0; q < DA; ++q) {
-      const char *s;
-      if (DW) s = sa[q] && !(short_ && across_row(q, CA) >= edge) ? sa[q] + (int64_t)st * 64 * p.lddy : zeros;
-      else s = short_ && ca[q] * 8 >= edge ? zeros : sa[q] + (int64_t)st * 128;
-      load_lds16(s, to + (q * WAVES + wave) * 1024);
-    }
+    for (int q = 0; q < DA; ++q)
+      load_stage16(ry, to + (q * WN + wave) * 1024, (uint32_t)(at_row(q, CA) * p.lddy) + at_col(q, CA), 0);
 #pragma unroll
     for (int q = 0; q < DB; ++q) {
-      const char *s;
-      if (DW) s = sb[q] && at_x[q] >= 0 ? sb[q] + at_x[q] * p.ldx : zeros;
-      else s = sb[q] && !(short_ && across_row(q, CB) >= edge) ? sb[q] + (int64_t)st * 128 * p.K : zeros;
-      load_lds16(s, to + BM * 128 + (q * WAVES + wave) * 1024);
+      char *const d = to + BOFF + (q * WN + wave) * 1024;
+      if (FAR) load_lds16(at_x[q] >= 0 && n0 * 2 + at_col(q, CB) < p.K * 2 ? xe + at_x[q] * p.ldx + at_col(q, CB) : (const char *)kZeros, d);
+      else load_stage16(rx, d, at_x[q] >= 0 ? (uint32_t)((at_x[q] - x0) * p.ldx) + at_col(q, CB) : kNowhere, 0);
     }
     asm volatile("" ::: "memory");
-    if (DW) find_rows(st + 1);
+    find_rows(st + 1);
   };
   typename OP::Acc acc[NT][MT];
 #pragma unroll
@@ -128,80 +67,74 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_grouped_grad(GroupedGrad p,
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[i][m] = typename OP::Acc{0, 0, 0, 0};
 
-  // terms 32 h + 8 g .. + 7 of tile m of a wave whose columns begin at chunk c0
-  auto across = [&](const char *x, int chunks, int c0, int m, int h) {
-    const int j = 32 * h + 8 * g + (r >> 2);  // this lane's row of the first four
-    const char *at = x + (j * chunks + ((c0 + 4 * (m >> 1) + (r & 3)) ^ across_place(j))) * 16 + 8 * (m & 1);
-    const u2 lo = read_turned(at), hi = read_turned(at + 4 * chunks * 16);
-    return u4{lo[0], lo[1], hi[0], hi[1]};
-  };
-  const int fa = (wm * 16 * MT + r) * 128, f0 = (g ^ place8(r)) * 16;
-  if (DW) find_rows(0);
+  // the steps, and the order of reads, loads and barriers, of the forward product
+  constexpr int S = MT / 2;
+  u4 a[2][2], b[2][NT];
+  auto read_a = [&](const char *x, int u, int j) {
 #pragma unroll
-  for (int i = 0; i < NB - 1; ++i)
-    if (i <= last) load(i, lds + i * STAGE);
+    for (int m = 0; m < 2; ++m) a[(u * S + j) & 1][m] = read_across(x, CA * 16, 0, 2 * j + m, u);
+  };
+  auto read_b = [&](const char *x, int u) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) b[u][i] = read_across(x + BOFF, CB * 16, 4 * wave, i, u);
+  };
+  find_rows(0);
+  if (last >= 0) load(0, lds);
+  if (last >= 1) load(1, lds + STAGE);
   wait_vm<0>();
   barrier_keep_loads();
-  const char *x = lds;
-  char *in = lds + (NB - 1) * STAGE;
+  read_b(lds, 0);
+  read_a(lds, 0, 0);
   for (int s = 0; s <= last; ++s) {
-    if (s + NB - 1 <= last) load(s + NB - 1, in);
+    char *const x = lds + (s & 1) * STAGE, *const next = lds + (~s & 1) * STAGE;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u4 a[MT], b[NT];
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) b[i] = across(x + BM * 128, CB, wn * 2 * NT, i, h);
+      for (int j = 0; j < S; ++j) {
+        if (j + 1 < S) read_a(x, u, j + 1);
+        else if (u == 0) {
+          read_b(x, 1);
+          read_a(x, 1, 0);
+        } else if (s < last) {
+          wait_vm<0>();
+          barrier_keep_loads();
+          if (s + 2 <= last) load(s + 2, x);
+          read_b(next, 0);
+          read_a(next, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        a[m] = DW ? across(x, CA, wm * 2 * MT, m, h) : *reinterpret_cast<const u4 *>(x + fa + m * 2048 + (f0 ^ 64 * h));
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < NT; ++i) acc[i][m] = OP::mul(b[i], a[m], acc[i][m]);
-    }
-    wait_vm<0>();
-    barrier_keep_loads();
-    x = x + STAGE == lds + NB * STAGE ? lds : x + STAGE;
-    in = in + STAGE == lds + NB * STAGE ? lds : in + STAGE;
+          for (int i = 0; i < NT; ++i) acc[i][2 * j + m] = OP::mul(b[u][i], a[(u * S + j) & 1][m], acc[i][2 * j + m]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
   }
 
-  const int64_t ld = DW ? p.K : p.ldo, base = DW ? (int64_t)t.e * p.N * p.K : 0;
-  const bool wide = wide_rows(p.o_type, ld);
+  const bool wide = wide_rows(p.dw_type, p.K);
+  const int64_t c = n0 + wave * 32 + 8 * g;
+  if (c >= p.K) return;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    int64_t row;
-    if (DW) {
-      row = m0 + wm * 16 * MT + 32 * (m >> 1) + 8 * (r >> 2) + 4 * (m & 1) + (r & 3);
-      if (row >= p.N) continue;
-    } else {
-      const int at = wm * 16 * MT + 16 * m + r;
-      if (at >= t.n) continue;
-      row = t.p0 + at;
-    }
+    const int64_t row = m0 + 32 * (m >> 1) + 8 * (r >> 2) + 4 * (m & 1) + (r & 3);
+    if (row >= p.N) continue;
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < NT; i += 2) {
-      const int64_t n = n0 + wn * 16 * NT + 16 * i + 8 * g;
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = acc[i + j / 4][m][j % 4];
-      if (n < p.K) store_values<8>(p.out, p.o_type, base + row * ld + n, p.K - n, wide, v);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = acc[i / 4][m][i % 4];
+    store_values<8>(p.dw, p.dw_type, ((int64_t)e * p.N + row) * p.K + c, p.K - c, wide, v);
   }
 }
 
-template <class OP>
-hipError_t dx(const GroupedGrad &p, hipStream_t s) {
-  constexpr int BM = 128, BN = 128;
-  const int64_t mt = grouped_max_tiles<BM>(p.offsets, p.E, p.P), nt = (p.K + BN - 1) / BN;
-  hipLaunchKernelGGL((k_grouped_grad<OP, false, BM, BN, 2, 2, 2>), dim3((unsigned)((mt * nt + 7) / 8 * 8)), dim3(256), 0, s, p, 0, (int)nt);
+template <class OP, int WN, int MT, bool FAR>
+hipError_t dw(const GroupedDw &p, hipStream_t s) {
+  const int64_t mt = (p.N + 16 * MT - 1) / (16 * MT), nt = (p.K + 32 * WN - 1) / (32 * WN);
+  hipLaunchKernelGGL((k_grouped_dw<OP, WN, MT, FAR>), dim3((unsigned)((p.E * mt * nt + 7) / 8 * 8)), dim3(64 * WN), 0, s, p, (int)mt, (int)nt);
   return hipGetLastError();
 }
 template <class OP>
-hipError_t dw(const GroupedGrad &p, hipStream_t s) {
-  constexpr int BM = 128, BN = 128;
-  const int64_t mt = (p.N + BM - 1) / BM, nt = (p.K + BN - 1) / BN;
-  hipLaunchKernelGGL((k_grouped_grad<OP, true, BM, BN, 2, 2, 2>), dim3((unsigned)((p.E * mt * nt + 7) / 8 * 8)), dim3(256), 0, s, p, (int)mt, (int)nt);
-  return hipGetLastError();
+hipError_t choose_dw(const GroupedDw &p, hipStream_t s) {
+  if (p.perm && p.T * p.ldx > kRange) return dw<OP, 4, 8, true>(p, s);
+  return p.P / p.E > 256 && p.E * p.N * p.K >= (1 << 25) ? dw<OP, 8, 16, false>(p, s) : dw<OP, 4, 8, false>(p, s);
 }
 
 // ---------------------------------------------------------------- gradients of shared rows
@@ -240,8 +173,7 @@ __global__ __launch_bounds__(256) void k_grouped_add_up(void *dx, int64_t ldo, i
 
 }  // namespace
 
-hipError_t launch_grouped_dx(const GroupedGrad &p, hipStream_t s) { return p.type == DS4MOE_BF16 ? dx<OpBf16>(p, s) : dx<OpF16>(p, s); }
-hipError_t launch_grouped_dw(const GroupedGrad &p, hipStream_t s) { return p.type == DS4MOE_BF16 ? dw<OpBf16>(p, s) : dw<OpF16>(p, s); }
+hipError_t launch_grouped_dw(const GroupedDw &p, hipStream_t s) { return p.type == DS4MOE_BF16 ? choose_dw<OpBf16>(p, s) : choose_dw<OpF16>(p, s); }
 
 hipError_t launch_grouped_places(int32_t *places, const int32_t *perm, int32_t P, int32_t A, hipStream_t s) {
   hipLaunchKernelGGL(k_grouped_no_places, dim3((A + 255) / 256), dim3(256), 0, s, places, A);

@@ -10,7 +10,8 @@ namespace ds4 {
 
 namespace {
 
-constexpr int64_t kMaxGroups = 1 << 20;  // workgroups of a launch; what is beyond goes round
+// workgroups of a launch; what is beyond goes round
+unsigned groups(int64_t n) { return (unsigned)(n < (1 << 20) ? n : 1 << 20); }
 
 template <int TYPE>
 __device__ __forceinline__ float value_at(const void *src, int64_t i) {
@@ -165,7 +166,7 @@ hipError_t quantize(int8_t *codes, float *scales, const void *src, int64_t rows,
   const bool vec = ((uintptr_t)src % 16) == 0 && (ld * el) % 16 == 0;
   auto f = cols <= 256 ? k_int8_quantize<TYPE, 16> : cols <= 2048 ? k_int8_quantize<TYPE, 64> : k_int8_quantize<TYPE, 256>;
   const int64_t per = cols <= 256 ? 16 : cols <= 2048 ? 4 : 1;
-  hipLaunchKernelGGL(f, dim3((unsigned)min((rows + per - 1) / per, kMaxGroups)), dim3(256), 0, s, codes, scales, src, rows, cols, ld, vec);
+  hipLaunchKernelGGL(f, dim3(groups((rows + per - 1) / per)), dim3(256), 0, s, codes, scales, src, rows, cols, ld, vec);
   return hipGetLastError();
 }
 
@@ -182,7 +183,7 @@ hipError_t launch_int8_dequantize(void *dst, int32_t type, int64_t ld, const int
                                   int64_t cols, hipStream_t s) {
   const int64_t per = (cols + 15) / 16, total = rows * per, el = type == DS4MOE_F32 ? 4 : 2;
   const bool wide = ((uintptr_t)dst % 16) == 0 && (ld * el) % 16 == 0;
-  hipLaunchKernelGGL(k_int8_dequantize, dim3((unsigned)min((total + 255) / 256, kMaxGroups)), dim3(256), 0, s, dst, type, ld, codes, scales, cols,
+  hipLaunchKernelGGL(k_int8_dequantize, dim3(groups((total + 255) / 256)), dim3(256), 0, s, dst, type, ld, codes, scales, cols,
                      (uint32_t)per, total, wide);
   return hipGetLastError();
 }
