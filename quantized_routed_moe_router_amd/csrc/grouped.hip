@@ -43,12 +43,12 @@ __device__ __forceinline__ void multiply_tile(const Grouped &p, const Segment &t
   int at_x[DA];
 #pragma unroll
   for (int q = 0; q < DA; ++q) {
-    at_x[q] = row(q) < t.n ? row_of(p.perm, p.k_inv, p.T, p.k, t.p0 + row(q)) : -1;
+    at_x[q] = row(q) < t.n ? row_of(p.perm, p.k_inv, p.T, t.p0 + row(q)) : -1;
     sa[q] = at_x[q] < 0 ? kNowhere : (uint32_t)((at_x[q] - x0) * p.ldx) + chunk_a(q) * 16;
   }
 #pragma unroll
   for (int q = 0; q < DB; ++q)
-    sb[q] = TURNED ? (uint32_t)(turned_row(q) * p.N * 2) + ((lane % CW) ^ across_place(turned_row(q))) * 16
+    sb[q] = TURNED ? (uint32_t)(turned_row(q) * p.N * 2) + ((lane % CW) ^ across_place<true>(turned_row(q))) * 16
                    : (uint32_t)(row(q) * p.Kb) + chunk_b(q) * 16;
   auto load = [&](int st, char *to) {
     const bool whole = st < last || edge == 8;
@@ -89,7 +89,7 @@ __device__ __forceinline__ void multiply_tile(const Grouped &p, const Segment &t
   auto read_b = [&](const char *x, int u) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
-      b[u][i] = TURNED ? read_across(x + BOFF, 64 * WN, 4 * wave, i, u) : *reinterpret_cast<const u4 *>(x + fb + i * 512 + (f0 ^ 64 * u));
+      b[u][i] = TURNED ? read_across<true>(x + BOFF, 64 * WN, 4 * wave, i, u) : *reinterpret_cast<const u4 *>(x + fb + i * 512 + (f0 ^ 64 * u));
   };
 #pragma unroll
   for (int i = 0; i < NB; ++i)
@@ -142,7 +142,7 @@ __device__ __forceinline__ void multiply_tile(const Grouped &p, const Segment &t
     if (at_row >= t.n) continue;
     float sx = 1.0f;
     if (OP::SCALED) {
-      const int at = row_of(p.perm, p.k_inv, p.T, p.k, t.p0 + at_row);
+      const int at = row_of(p.perm, p.k_inv, p.T, t.p0 + at_row);
       sx = at < 0 ? 0.0f : p.xs[at];
     }
     float v[8];

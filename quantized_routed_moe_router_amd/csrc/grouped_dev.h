@@ -50,12 +50,14 @@ __device__ __forceinline__ void load_stage16(__amdgpu_buffer_rsrc_t r, void *lds
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, off, stage_off, 0, 0);
 }
 
-// the row of x of position p, or -1 where the permutation names none
-__device__ __forceinline__ int row_of(const int32_t *perm, uint32_t k_inv, int T, int k, int p) {
-  if (!perm) return p < T ? p : -1;
-  const int a = perm[p];
+// the row of x of an entry of the permutation, or -1 where it names none
+__device__ __forceinline__ int row_named(uint32_t k_inv, int T, int a) {
   const int t = k_inv ? (int)__umulhi((uint32_t)a, k_inv) : a;
   return a >= 0 && t < T ? t : -1;
+}
+// the row of x of position p
+__device__ __forceinline__ int row_of(const int32_t *perm, uint32_t k_inv, int T, int p) {
+  return perm ? row_named(k_inv, T, perm[p]) : p < T ? p : -1;
 }
 
 // rows p0 .. p0 + n - 1 of expert e (-1: of none)
@@ -67,17 +69,27 @@ struct Segment {
 // it lies, 64 rows by the tile's columns, chunk c of 16 bytes of row j in the
 // place c ^ across_place(j), and turned on the way to the registers by the
 // LDS' transposing read, which gives lane i of 16 the column i of four rows.
-// Groups of 16 columns go in pairs: group m of a wave's has columns
-// 32 (m / 2) + 8 a + 4 (m % 2) + b in the place 4 a + b, so that a lane's
-// results of two groups are 8 adjacent columns.
-__device__ __forceinline__ int across_place(int row) { return (row & 3) << 2; }
+// PAIRS: group m of a wave's groups of 16 columns has columns 32 (m / 2) + 8 a
+// + 4 (m % 2) + b in the place 4 a + b, so that a lane's results of two groups
+// are 8 adjacent columns; a read then uses half of every chunk that it touches,
+// and takes twice as long.  Otherwise group m has columns 16 m ..
+template <bool PAIRS>
+__device__ __forceinline__ int across_place(int row) {
+  return PAIRS ? (row & 3) << 2 : (row & 3) << 1 | (row & 8);
+}
+typedef __attribute__((address_space(3))) s4 lds_s4;
+// (__restrict__: without it the compiler lets this read wait for all loads into LDS, where it orders nothing: the
+// barrier behind the waits does)
+__device__ __forceinline__ u2 read_turned(lds_s4 *__restrict__ at) {
+  return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(at));
+}
 // Fragment of group m, half u of the 64 rows (`bytes` each), of columns from chunk c0 on.
+template <bool PAIRS>
 __device__ __forceinline__ u4 read_across(const char *x, int bytes, int c0, int m, int u) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, j = 32 * u + 8 * g + (r >> 2);  // the first of four rows
-  const char *at = x + j * bytes + ((c0 + 4 * (m >> 1) + (r & 3)) ^ across_place(r >> 2)) * 16 + 8 * (m & 1);
-  typedef __attribute__((address_space(3))) s4 lds_s4;
-  const u2 lo = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)at));
-  const u2 hi = __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(at + 4 * bytes)));
+  const int chunk = PAIRS ? c0 + 4 * (m >> 1) + (r & 3) : c0 + 2 * m + (r >> 1 & 1), half = PAIRS ? m & 1 : r & 1;
+  const char *at = x + j * bytes + (chunk ^ across_place<PAIRS>(8 * g + (r >> 2))) * 16 + 8 * half;
+  const u2 lo = read_turned((lds_s4 *)at), hi = read_turned((lds_s4 *)(at + 4 * bytes));
   return u4{lo[0], lo[1], hi[0], hi[1]};
 }
 

@@ -36,7 +36,7 @@ __global__ __launch_bounds__(64 * SW, 4) void k_grouped_few(Grouped p) {
   int at[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    at[m] = 16 * m + r < t.n ? row_of(p.perm, p.k_inv, p.T, p.k, t.p0 + 16 * m + r) : -1;
+    at[m] = 16 * m + r < t.n ? row_of(p.perm, p.k_inv, p.T, t.p0 + 16 * m + r) : -1;
     in[m] = at[m] >= 0;
     x[m] = p.x + (in[m] ? at[m] : 0) * p.ldx;
   }

@@ -32,34 +32,39 @@ __global__ __launch_bounds__(64 * WN, 2) void k_grouped_dw(GroupedDw p, int mtil
 
   // load q of a stage: its rows from (q WN + wave) 64 / C on, chunk by place
   auto at_row = [&](int q, int chunks) { return (q * WN + wave) * (64 / chunks) + lane / chunks; };
-  auto at_col = [&](int q, int chunks) { return ((lane % chunks) ^ across_place(at_row(q, chunks))) * 16; };
+  auto col_a = [&](int q) { return ((lane % CA) ^ across_place<false>(at_row(q, CA))) * 16; };
+  auto col_b = [&](int q) { return ((lane % CB) ^ across_place<true>(at_row(q, CB))) * 16; };
   const char *const dy = p.dy + p0 * p.lddy + m0 * 2;
   const int64_t x0 = p.perm ? 0 : p0;  // the row that offsets count from
   const char *const xe = p.x + x0 * p.ldx + n0 * 2;
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(xe, range_of((p.T - x0 - 1) * p.ldx + (p.K - n0) * 2));
-  int at_x[DB];
-  // the rows of x of stage st, asked for a stage ahead
+  // the entries of the permutation of stage st, asked for a stage ahead and not touched before
+  int named[DB];
   auto find_rows = [&](int st) {
 #pragma unroll
     for (int q = 0; q < DB; ++q) {
       const int row = st * 64 + at_row(q, CB);
-      at_x[q] = row < n ? row_of(p.perm, p.k_inv, p.T, p.k, p0 + row) : -1;
+      named[q] = row >= n ? -1 : p.perm ? p.perm[p0 + row] : p0 + row;
     }
   };
   auto load = [&](int st, char *to) {
+    int at_x[DB];
+#pragma unroll
+    for (int q = 0; q < DB; ++q) at_x[q] = row_named(p.k_inv, p.T, named[q]);
+    find_rows(st + 1);
+    asm volatile("" ::: "memory");
     const int64_t d0 = (int64_t)st * 64 * p.lddy;  // the range ends with the expert's rows: past it are zeros
     const __amdgpu_buffer_rsrc_t ry = make_rsrc(dy + d0, range_of((n - st * 64 - 1) * p.lddy + (p.N - m0) * 2));
 #pragma unroll
     for (int q = 0; q < DA; ++q)
-      load_stage16(ry, to + (q * WN + wave) * 1024, (uint32_t)(at_row(q, CA) * p.lddy) + at_col(q, CA), 0);
+      load_stage16(ry, to + (q * WN + wave) * 1024, (uint32_t)(at_row(q, CA) * p.lddy) + col_a(q), 0);
 #pragma unroll
     for (int q = 0; q < DB; ++q) {
       char *const d = to + BOFF + (q * WN + wave) * 1024;
-      if (FAR) load_lds16(at_x[q] >= 0 && n0 * 2 + at_col(q, CB) < p.K * 2 ? xe + at_x[q] * p.ldx + at_col(q, CB) : (const char *)kZeros, d);
-      else load_stage16(rx, d, at_x[q] >= 0 ? (uint32_t)((at_x[q] - x0) * p.ldx) + at_col(q, CB) : kNowhere, 0);
+      if (FAR) load_lds16(at_x[q] >= 0 && n0 * 2 + col_b(q) < p.K * 2 ? xe + at_x[q] * p.ldx + col_b(q) : (const char *)kZeros, d);
+      else load_stage16(rx, d, at_x[q] >= 0 ? (uint32_t)((at_x[q] - x0) * p.ldx) + col_b(q) : kNowhere, 0);
     }
     asm volatile("" ::: "memory");
-    find_rows(st + 1);
   };
   typename OP::Acc acc[NT][MT];
 #pragma unroll
@@ -72,11 +77,11 @@ __global__ __launch_bounds__(64 * WN, 2) void k_grouped_dw(GroupedDw p, int mtil
   u4 a[2][2], b[2][NT];
   auto read_a = [&](const char *x, int u, int j) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m) a[(u * S + j) & 1][m] = read_across(x, CA * 16, 0, 2 * j + m, u);
+    for (int m = 0; m < 2; ++m) a[(u * S + j) & 1][m] = read_across<false>(x, CA * 16, 0, 2 * j + m, u);
   };
   auto read_b = [&](const char *x, int u) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) b[u][i] = read_across(x + BOFF, CB * 16, 4 * wave, i, u);
+    for (int i = 0; i < NT; ++i) b[u][i] = read_across<true>(x + BOFF, CB * 16, 4 * wave, i, u);
   };
   find_rows(0);
   if (last >= 0) load(0, lds);
@@ -116,7 +121,7 @@ __global__ __launch_bounds__(64 * WN, 2) void k_grouped_dw(GroupedDw p, int mtil
   if (c >= p.K) return;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int64_t row = m0 + 32 * (m >> 1) + 8 * (r >> 2) + 4 * (m & 1) + (r & 3);
+    const int64_t row = m0 + 16 * m + r;
     if (row >= p.N) continue;
     float v[8];
 #pragma unroll
