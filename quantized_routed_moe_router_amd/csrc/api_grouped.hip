@@ -10,7 +10,8 @@ using namespace ds4;
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t)1 << 24;
+constexpr int64_t kMaxRows = (int64_t)1 << 24;    // of a dense product
+constexpr int64_t kMaxGrouped = (int64_t)1 << 23;  // positions and tokens: entries of a permutation stay below 2^27
 constexpr int64_t kMaxDim = 65536;
 constexpr int64_t kMaxOut = (int64_t)1 << 37;  // values of a matrix (more than memory holds; keeps grids within 2^32 threads)
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
@@ -23,7 +24,7 @@ int hip_status(hipError_t e) { return e == hipSuccess ? DS4MOE_OK : DS4MOE_ERR_H
 inline bool real_dtype(int32_t d) { return d == DS4MOE_F32 || d == DS4MOE_BF16 || d == DS4MOE_F16; }
 inline bool half_dtype(int32_t d) { return d == DS4MOE_BF16 || d == DS4MOE_F16; }
 inline int64_t elem(int32_t d) { return d == DS4MOE_F32 ? 4 : d == DS4MOE_I8 ? 1 : 2; }
-inline uint32_t inverse(int32_t k) { return k == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + k - 1) / k); }
+inline uint32_t inverse(int32_t k) { return (uint32_t)((((uint64_t)1 << 31) + k - 1) / k); }
 
 int validate_grouped(const ds4moe_grouped_dims *d) {
   if (!d) return DS4MOE_ERR_NULL;
@@ -31,7 +32,7 @@ int validate_grouped(const ds4moe_grouped_dims *d) {
   if (!real_dtype(d->y_dtype)) return DS4MOE_ERR_DTYPE;
   if (d->n_experts < 1 || d->n_experts > GROUPED_EXPERTS) return DS4MOE_ERR_SHAPE;
   if (d->top_k < 1 || d->top_k > 16) return DS4MOE_ERR_SHAPE;
-  if (d->rows < 0 || d->rows > kMaxRows || d->tokens < 0 || d->tokens > kMaxRows) return DS4MOE_ERR_SHAPE;
+  if (d->rows < 0 || d->rows > kMaxGrouped || d->tokens < 0 || d->tokens > kMaxGrouped) return DS4MOE_ERR_SHAPE;
   if (d->N < 1 || d->N > kMaxDim || d->K < 1 || d->K > kMaxDim) return DS4MOE_ERR_SHAPE;
   if (d->K * elem(d->dtype) % 16) return DS4MOE_ERR_SHAPE;
   if (d->rows * d->N > kMaxOut || d->rows * d->K > kMaxOut || d->n_experts * d->N * d->K > kMaxOut) return DS4MOE_ERR_SHAPE;
@@ -137,10 +138,12 @@ int ds4moe_grouped_dx(const ds4moe_grouped_dims *dims, void *dx, int64_t lddx, c
   p.P = p.T = (int32_t)d.rows;
   p.N = d.K;
   p.Kb = d.N * elem(d.dtype);
+  p.places = places;
+  p.n_places = perm ? (int32_t)(d.tokens * d.top_k) : 0;
   hipError_t e = hipSuccess;
   if (d.rows) e = launch_grouped(p, s);
   if (e != hipSuccess || !perm) return hip_status(e);
-  e = launch_grouped_places(places, perm, (int32_t)d.rows, (int32_t)(d.tokens * d.top_k), s);
+  e = launch_grouped_places(places, perm, (int32_t)d.rows, (int32_t)(d.tokens * d.top_k), d.rows == 0, s);
   if (e != hipSuccess) return hip_status(e);
   return hip_status(launch_grouped_add_up(dx, lddx, d.y_dtype, rows, places, (int32_t)d.tokens, d.top_k, d.K, s));
 }
@@ -236,6 +239,7 @@ int ds4moe_int8_matmul(void *y, int32_t y_dtype, int64_t ldy, const void *a, con
     if (!ws) return DS4MOE_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return DS4MOE_ERR_ALIGN;
     if (ws_bytes < ds4moe_int8_workspace_bytes(M, K, a_dtype)) return DS4MOE_ERR_WORKSPACE;
+    if (int8_few_fits(M, K)) return hip_status(launch_int8_few(p, a, a_dtype, lda, K, s));
     int8_t *const c = (int8_t *)ws;
     float *const sc = reinterpret_cast<float *>((char *)ws + align256((size_t)(M * K16)));
     const hipError_t e = launch_int8_quantize(c, sc, a, a_dtype, M, K, lda, s);

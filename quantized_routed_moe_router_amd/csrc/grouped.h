@@ -24,8 +24,10 @@ struct Grouped {
   const int32_t *offsets;     // [E + 1], or null: one group of all rows
   const int32_t *perm;        // [P]: row perm[p] / k, or null: row p
   int32_t E, k, P, T;
-  uint32_t k_inv;             // ceil(2^32 / k), 0 for k = 1
+  uint32_t k_inv;             // ceil(2^31 / k)
   int64_t N, Kb;
+  int32_t *places;            // turned: this many of them are set to -1 on the way
+  int32_t n_places;
 };
 hipError_t launch_grouped(const Grouped &p, hipStream_t s);
 hipError_t launch_grouped_few(const Grouped &p, int rows, hipStream_t s);
@@ -45,8 +47,9 @@ struct GroupedDw {
 };
 hipError_t launch_grouped_dw(const GroupedDw &p, hipStream_t s);
 
-// dx[t] = sum over j of rows[inv[t k + j]], in the order of j; places[t k + j] of perm, -1 where none
-hipError_t launch_grouped_places(int32_t *places, const int32_t *perm, int32_t P, int32_t A, hipStream_t s);
+// dx[t] = sum over j of rows[places[t k + j]], in the order of j, where that is not -1; places[perm[p]] = p, to be -1
+// before (`clear`: they are made so here)
+hipError_t launch_grouped_places(int32_t *places, const int32_t *perm, int32_t P, int32_t A, bool clear, hipStream_t s);
 hipError_t launch_grouped_add_up(void *dx, int64_t ldo, int32_t o_type, const float *rows, const int32_t *places,
                                  int32_t T, int32_t k, int64_t K, hipStream_t s);
 
@@ -55,5 +58,9 @@ hipError_t launch_int8_quantize(int8_t *codes, float *scales, const void *src, i
                                 int64_t ld, hipStream_t s);
 hipError_t launch_int8_dequantize(void *dst, int32_t type, int64_t ld, const int8_t *codes, const float *scales,
                                   int64_t rows, int64_t cols, hipStream_t s);
+
+// the dense product g of M rows (g.P) that are quantised on the way: a, rows lda values apart; g.x and g.xs are not read
+bool int8_few_fits(int64_t M, int64_t K);
+hipError_t launch_int8_few(const Grouped &g, const void *a, int32_t a_type, int64_t lda, int64_t K, hipStream_t s);
 
 }  // namespace ds4

@@ -80,6 +80,7 @@ __device__ __forceinline__ void multiply_tile(const Grouped &p, const Segment &t
   // it frees is filled again at once.
   constexpr int S = (MT + 1) / 2;
   const int fa = r * 128, fb = BOFF + (wave * 32 + 8 * (r >> 2) + (r & 3)) * 128, f0 = (g ^ place8(r)) * 16;
+  const uint32_t tb = BOFF + across_at<true>(64 * WN, 4 * wave, 0);
   u4 a[2][2], b[2][NT];
   auto read_a = [&](const char *x, int u, int j) {
 #pragma unroll
@@ -89,7 +90,7 @@ __device__ __forceinline__ void multiply_tile(const Grouped &p, const Segment &t
   auto read_b = [&](const char *x, int u) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
-      b[u][i] = TURNED ? read_across<true>(x + BOFF, 64 * WN, 4 * wave, i, u) : *reinterpret_cast<const u4 *>(x + fb + i * 512 + (f0 ^ 64 * u));
+      b[u][i] = TURNED ? read_across((lds_at)x + tb + (32 * 64 * WN * u + 8 * i), 64 * WN) : *reinterpret_cast<const u4 *>(x + fb + i * 512 + (f0 ^ 64 * u));
   };
 #pragma unroll
   for (int i = 0; i < NB; ++i)
@@ -129,26 +130,42 @@ __device__ __forceinline__ void multiply_tile(const Grouped &p, const Segment &t
   }
 
   const bool wide = wide_rows(p.y_type, p.ldy);
-  const int64_t n = n0 + wave * 32 + 8 * g;
-  if (n >= p.N) return;
+  const int64_t n_wave = n0 + wave * 32, n = n_wave + 8 * g;
+  if (!wide) barrier_keep_loads();  // the buffers have been read
+  if (n_wave >= p.N) return;
   float sw[8];
   if (OP::SCALED) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) sw[i] = p.ws[(int64_t)t.e * p.N + min(n + i, p.N - 1)];
   }
+  float *const own = reinterpret_cast<float *>(lds + wave * 16 * 36 * 4);  // 16 rows of 32 values, 4 apart
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int at_row = 16 * m + r;
-    if (at_row >= t.n) continue;
     float sx = 1.0f;
     if (OP::SCALED) {
-      const int at = row_of(p.perm, p.k_inv, p.T, t.p0 + at_row);
+      const int at = at_row < t.n ? row_of(p.perm, p.k_inv, p.T, t.p0 + at_row) : -1;
       sx = at < 0 ? 0.0f : p.xs[at];
     }
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = OP::SCALED ? (float)acc[i / 4][m][i % 4] * sx * sw[i] : (float)acc[i / 4][m][i % 4];
-    store_values<8>(p.y, p.y_type, (int64_t)(t.p0 + at_row) * p.ldy + n, p.N - n, wide, v);
+    if (wide) {
+      if (at_row < t.n && n < p.N) store_values<8>(p.y, p.y_type, (int64_t)(t.p0 + at_row) * p.ldy + n, p.N - n, true, v);
+      continue;
+    }
+    // Rows that begin anywhere: eight values of 16 rows each would go out one
+    // by one from 64 places.  Through LDS two whole rows of 32 go at a time.
+    *reinterpret_cast<f4 *>(own + r * 36 + 8 * g) = f4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f4 *>(own + r * 36 + 8 * g + 4) = f4{v[4], v[5], v[6], v[7]};
+    lds_order();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = 2 * i + (lane >> 5), c = lane & 31;
+      const float u[1] = {own[row * 36 + c]};
+      if (16 * m + row < t.n && n_wave + c < p.N) store_values<1>(p.y, p.y_type, (int64_t)(t.p0 + 16 * m + row) * p.ldy + n_wave + c, 1, false, u);
+    }
+    lds_order();
   }
 }
 
@@ -157,6 +174,8 @@ __device__ __forceinline__ void multiply_tile(const Grouped &p, const Segment &t
 template <class OP, bool TURNED, int WN>
 __global__ __launch_bounds__(64 * WN, 2) void k_grouped(Grouped p, int ntiles, int height) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
+  if (TURNED)
+    for (int i = blockIdx.x * 64 * WN + threadIdx.x; i < p.n_places; i += gridDim.x * 64 * WN) p.places[i] = -1;
   Finder f;
   f.load(p.offsets, p.E, p.P);
   if (height) f.set_height(height);

@@ -50,10 +50,12 @@ __device__ __forceinline__ void load_stage16(__amdgpu_buffer_rsrc_t r, void *lds
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16, off, stage_off, 0, 0);
 }
 
-// the row of x of an entry of the permutation, or -1 where it names none
-__device__ __forceinline__ int row_named(uint32_t k_inv, int T, int a) {
-  const int t = k_inv ? (int)__umulhi((uint32_t)a, k_inv) : a;
-  return a >= 0 && t < T ? t : -1;
+// the row of x of an entry of the permutation, or -1 where it names none;
+// k_inv: ceil(2^31 / k), which gives entry / k exactly for entries below 2^27,
+// and no less than it for others
+__device__ __forceinline__ int row_named(uint32_t k_inv, int T, int entry) {
+  const int t = (int)__umulhi(2u * (uint32_t)entry, k_inv);
+  return ((entry >= 0) & (t < T)) ? t : -1;
 }
 // the row of x of position p
 __device__ __forceinline__ int row_of(const int32_t *perm, uint32_t k_inv, int T, int p) {
@@ -83,13 +85,18 @@ typedef __attribute__((address_space(3))) s4 lds_s4;
 __device__ __forceinline__ u2 read_turned(lds_s4 *__restrict__ at) {
   return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(at));
 }
-// Fragment of group m, half u of the 64 rows (`bytes` each), of columns from chunk c0 on.
+typedef __attribute__((address_space(3))) const char *lds_at;
+// Where this lane reads group m of columns from chunk c0 on, of rows of `bytes` each.  The place of a chunk makes it
+// another number for every group (of PAIRS, every pair), so it is worked out once and kept.
 template <bool PAIRS>
-__device__ __forceinline__ u4 read_across(const char *x, int bytes, int c0, int m, int u) {
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, j = 32 * u + 8 * g + (r >> 2);  // the first of four rows
+__device__ __forceinline__ uint32_t across_at(int bytes, int c0, int m) {
+  const int lane = threadIdx.x & 63, r = lane & 15, j = 8 * (lane >> 4) + (r >> 2);  // the first of four rows
   const int chunk = PAIRS ? c0 + 4 * (m >> 1) + (r & 3) : c0 + 2 * m + (r >> 1 & 1), half = PAIRS ? m & 1 : r & 1;
-  const char *at = x + j * bytes + (chunk ^ across_place<PAIRS>(8 * g + (r >> 2))) * 16 + 8 * half;
-  const u2 lo = read_turned((lds_s4 *)at), hi = read_turned((lds_s4 *)(at + 4 * bytes));
+  return j * bytes + (chunk ^ across_place<PAIRS>(j)) * 16 + 8 * half;
+}
+// a fragment: rows j .. j + 3 and j + 4 .. j + 7
+__device__ __forceinline__ u4 read_across(lds_at x, int bytes) {
+  const u2 lo = read_turned((lds_s4 *)x), hi = read_turned((lds_s4 *)(x + 4 * bytes));
   return u4{lo[0], lo[1], hi[0], hi[1]};
 }
 
@@ -243,7 +250,7 @@ __device__ __forceinline__ bool place_tile(int id, int mtiles, int ntiles, int &
 // pieces of 16 bytes (or of NV values, if that is less)
 template <int NV>
 __device__ __forceinline__ void store_values(void *base, int type, int64_t at, int64_t n, bool wide, const float (&v)[NV]) {
-  if (wide && n >= NV) {
+  if constexpr (NV >= 4) if (wide && n >= NV) {
     if (type == DS4MOE_F32) {
       float *y = (float *)base + at;
 #pragma unroll

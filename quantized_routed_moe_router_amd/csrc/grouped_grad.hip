@@ -3,7 +3,7 @@
 // in bf16 or fp16 operands, and the sum of the gradients of rows that several
 // experts share.  (The gradient of the rows is a product by turned weights.)
 //
-// A workgroup of WN waves has 16 MT rows and 32 WN columns of one dW_e, 64
+// A workgroup of 2 WN waves has 32 MT rows and 64 WN columns of one dW_e, 32
 // terms of the sum at a time.  Both operands lie across.
 #include "grouped_dev.h"
 
@@ -11,58 +11,78 @@ namespace ds4 {
 
 namespace {
 
-// FAR: rows of x that 32-bit offsets do not reach
-template <class OP, int WN, int MT, bool FAR>
-__global__ __launch_bounds__(64 * WN, 2) void k_grouped_dw(GroupedDw p, int mtiles, int ntiles) {
-  constexpr int NT = 2, DA = 2 * MT / WN, DB = 4, CA = 2 * MT, CB = 4 * WN;  // loads per wave; chunks of a staged row
-  constexpr int BOFF = DA * WN * 1024, STAGE = BOFF + DB * WN * 1024;
-  static_assert(DA * WN == 2 * MT && MT % 2 == 0 && CA >= 16 && CB >= 16, "whole loads, places of chunks stay in the row");
-  __shared__ __attribute__((aligned(16))) char lds[2 * STAGE];
+// PERM: rows by a permutation.  FAR: rows that 32-bit offsets do not reach.
+template <class OP, int WN, int MT, int NB, bool PERM, bool FAR>
+__global__ __launch_bounds__(128 * WN, 2) void k_grouped_dw(GroupedDw p, int mtiles, int ntiles) {
+  constexpr int WAVES = 2 * WN, NT = 4, BM = 32 * MT, BN = 64 * WN;
+  constexpr int CA = BM / 8, CB = BN / 8;                        // chunks of a staged row
+  constexpr int DA = CA / 2 / WAVES, DB = CB / 2 / WAVES, D = DA + DB;  // loads per wave
+  constexpr int BOFF = BM * 64, STAGE = BOFF + BN * 64;
+  static_assert(DA * WAVES * 2 == CA && DB * WAVES * 2 == CB && MT % 4 == 0 && CA >= 16 && CB >= 16 && NB % 2 == 0,
+                "whole loads, places of chunks stay in the row");
+  __shared__ __attribute__((aligned(16))) char lds[NB * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+  const int wm = wave / WN, wn = wave % WN;
   int mt, nt;
   if (!place_tile<4>(blockIdx.x, p.E * mtiles, ntiles, mt, nt)) return;
   const int e = mt / mtiles;
-  const int64_t m0 = (int64_t)(mt - e * mtiles) * 16 * MT, n0 = (int64_t)nt * 32 * WN;
+  const int64_t m0 = (int64_t)(mt - e * mtiles) * BM, n0 = (int64_t)nt * BN;
   int p0 = 0, n = p.P;
   if (p.offsets) {
     p0 = min(max(p.offsets[e], 0), p.P);
     n = max(min(max(p.offsets[e + 1], 0), p.P) - p0, 0);
   }
-  const int last = (n + 63) / 64 - 1;
+  const int last = (n + 31) / 32 - 1;
 
-  // load q of a stage: its rows from (q WN + wave) 64 / C on, chunk by place
-  auto at_row = [&](int q, int chunks) { return (q * WN + wave) * (64 / chunks) + lane / chunks; };
-  auto col_a = [&](int q) { return ((lane % CA) ^ across_place<false>(at_row(q, CA))) * 16; };
-  auto col_b = [&](int q) { return ((lane % CB) ^ across_place<true>(at_row(q, CB))) * 16; };
+  // Load q of a stage: its rows from (q WAVES + wave) 64 / C on, chunk by place.
+  // The ranges of dy, and of x in order, end with the expert's rows: past them
+  // are zeros.
+  auto row_a = [&](int q) { return (q * WAVES + wave) * (64 / CA) + lane / CA; };
+  auto row_b = [&](int q) { return (q * WAVES + wave) * (64 / CB) + lane / CB; };
+  auto col_a = [&](int q) { return ((lane % CA) ^ across_place<false>(row_a(q))) * 16; };
+  auto col_b = [&](int q) { return ((lane % CB) ^ across_place<true>(row_b(q))) * 16; };
+  const uint32_t lddy = (uint32_t)p.lddy, ldx = (uint32_t)p.ldx;
   const char *const dy = p.dy + p0 * p.lddy + m0 * 2;
-  const int64_t x0 = p.perm ? 0 : p0;  // the row that offsets count from
-  const char *const xe = p.x + x0 * p.ldx + n0 * 2;
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xe, range_of((p.T - x0 - 1) * p.ldx + (p.K - n0) * 2));
-  // the entries of the permutation of stage st, asked for a stage ahead and not touched before
-  int named[DB];
-  auto find_rows = [&](int st) {
+  const char *const xe = p.x + (PERM ? 0 : p0 * p.ldx) + n0 * 2;
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(dy, range_of((int64_t)(n - 1) * p.lddy + (p.N - m0) * 2));
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(xe, range_of((int64_t)((PERM ? p.T : min(n, p.T - p0)) - 1) * p.ldx + (p.K - n0) * 2));
+  uint32_t sa[DA], sb[DB];
+#pragma unroll
+  for (int q = 0; q < DA; ++q) sa[q] = row_a(q) * lddy + col_a(q);
+#pragma unroll
+  for (int q = 0; q < DB; ++q) sb[q] = PERM ? 0 : row_b(q) * ldx + col_b(q);
+  // The permutation's entries of a stage are asked for two stages before they
+  // are turned into offsets, and that is done in the middle of the stage whose
+  // end issues the loads: behind the barrier, where all waves are at the same
+  // place, nothing is left to work out.
+  int named[2][DB];
+  auto ask = [&](int st, int (&to)[DB]) {
+#pragma unroll
+    for (int q = 0; q < DB; ++q) to[q] = p.perm[p0 + min(st * 32 + row_b(q), n - 1)];
+  };
+  int at_x[DB];
+  auto prepare = [&](int st, const int (&from)[DB]) {
 #pragma unroll
     for (int q = 0; q < DB; ++q) {
-      const int row = st * 64 + at_row(q, CB);
-      named[q] = row >= n ? -1 : p.perm ? p.perm[p0 + row] : p0 + row;
+      const int at = row_named(p.k_inv, p.T, from[q]);
+      at_x[q] = st * 32 + row_b(q) < n ? at : -1;
+      sb[q] = at_x[q] >= 0 ? at * ldx + col_b(q) : kNowhere;
     }
   };
   auto load = [&](int st, char *to) {
-    int at_x[DB];
 #pragma unroll
-    for (int q = 0; q < DB; ++q) at_x[q] = row_named(p.k_inv, p.T, named[q]);
-    find_rows(st + 1);
-    asm volatile("" ::: "memory");
-    const int64_t d0 = (int64_t)st * 64 * p.lddy;  // the range ends with the expert's rows: past it are zeros
-    const __amdgpu_buffer_rsrc_t ry = make_rsrc(dy + d0, range_of((n - st * 64 - 1) * p.lddy + (p.N - m0) * 2));
-#pragma unroll
-    for (int q = 0; q < DA; ++q)
-      load_stage16(ry, to + (q * WN + wave) * 1024, (uint32_t)(at_row(q, CA) * p.lddy) + col_a(q), 0);
+    for (int q = 0; q < DA; ++q) {
+      char *const d = to + (q * WAVES + wave) * 1024;
+      if (FAR) load_lds16(st * 32 + row_a(q) < n && m0 * 2 + col_a(q) < p.N * 2 ? dy + (int64_t)(st * 32 + row_a(q)) * p.lddy + col_a(q) : (const char *)kZeros, d);
+      else load_stage16(ry, d, sa[q], st * 32 * lddy);
+    }
 #pragma unroll
     for (int q = 0; q < DB; ++q) {
-      char *const d = to + BOFF + (q * WN + wave) * 1024;
-      if (FAR) load_lds16(at_x[q] >= 0 && n0 * 2 + col_b(q) < p.K * 2 ? xe + at_x[q] * p.ldx + col_b(q) : (const char *)kZeros, d);
-      else load_stage16(rx, d, at_x[q] >= 0 ? (uint32_t)((at_x[q] - x0) * p.ldx) + col_b(q) : kNowhere, 0);
+      char *const d = to + BOFF + (q * WAVES + wave) * 1024;
+      if (FAR) {
+        const int64_t at = PERM ? at_x[q] : st * 32 + row_b(q) < min(n, p.T - p0) ? st * 32 + row_b(q) : -1;
+        load_lds16(at >= 0 && n0 * 2 + col_b(q) < p.K * 2 ? xe + at * p.ldx + col_b(q) : (const char *)kZeros, d);
+      } else load_stage16(rx, d, sb[q], PERM ? 0 : st * 32 * ldx);
     }
     asm volatile("" ::: "memory");
   };
@@ -74,39 +94,70 @@ __global__ __launch_bounds__(64 * WN, 2) void k_grouped_dw(GroupedDw p, int mtil
 
   // the steps, and the order of reads, loads and barriers, of the forward product
   constexpr int S = MT / 2;
+  uint32_t la[MT], lb[NT / 2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) la[m] = across_at<false>(CA * 16, 2 * MT * wm, m);
+#pragma unroll
+  for (int i = 0; i < NT / 2; ++i) lb[i] = BOFF + across_at<true>(CB * 16, 8 * wn, 2 * i);
   u4 a[2][2], b[2][NT];
   auto read_a = [&](const char *x, int u, int j) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m) a[(u * S + j) & 1][m] = read_across<false>(x, CA * 16, 0, 2 * j + m, u);
+    for (int m = 0; m < 2; ++m) a[(u * S + j) & 1][m] = read_across((lds_at)x + la[2 * j + m], CA * 16);
   };
   auto read_b = [&](const char *x, int u) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) b[u][i] = read_across<true>(x + BOFF, CB * 16, 4 * wave, i, u);
+    for (int i = 0; i < NT; ++i) b[u][i] = read_across((lds_at)x + lb[i / 2] + 8 * (i & 1), CB * 16);
   };
-  find_rows(0);
-  if (last >= 0) load(0, lds);
-  if (last >= 1) load(1, lds + STAGE);
-  wait_vm<0>();
-  barrier_keep_loads();
-  read_b(lds, 0);
-  read_a(lds, 0, 0);
-  for (int s = 0; s <= last; ++s) {
-    char *const x = lds + (s & 1) * STAGE, *const next = lds + (~s & 1) * STAGE;
+  if (last >= 0) {
+    if (PERM) {
+      int first[NB][DB];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+      for (int i = 0; i < NB; ++i) ask(i, first[i]);
+      ask(NB, named[0]);
+      ask(NB + 1, named[1]);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        prepare(i, first[i]);
+        if (i <= last) load(i, lds + i * STAGE);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        if (i <= last) load(i, lds + i * STAGE);
+    }
+  }
+  if (last >= NB - 1) wait_vm<(NB - 1) * D>();
+  else wait_vm<0>();
+  barrier_keep_loads();
+  char *x = lds;
+  read_b(x, 0);
+  read_a(x, 0, 0);
+  int s = 0;
+  bool more = last >= 0;
+  while (more) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (!more) break;
 #pragma unroll
       for (int j = 0; j < S; ++j) {
-        if (j + 1 < S) read_a(x, u, j + 1);
-        else if (u == 0) {
-          read_b(x, 1);
-          read_a(x, 1, 0);
-        } else if (s < last) {
-          wait_vm<0>();
-          barrier_keep_loads();
-          if (s + 2 <= last) load(s + 2, x);
-          read_b(next, 0);
-          read_a(next, 0, 0);
+        if (PERM && j == S / 2 && s + NB <= last) {
+          prepare(s + NB, named[u]);
+          ask(s + NB + 2, named[u]);
+          asm volatile("" ::: "memory");
         }
+        if (j + 1 < S) read_a(x, u, j + 1);
+        else if (s < last) {
+          // younger than the next stage's loads: those of NB - 2 stages and the entries asked for in NB - 1
+          if (s + NB <= last) wait_vm<(NB - 2) * D + (PERM ? (NB - 1) * DB : 0)>();
+          else if (s + NB - 1 <= last) wait_vm<(NB - 2) * D>();
+          else wait_vm<0>();
+          barrier_keep_loads();
+          if (s + NB <= last) load(s + NB, x);
+          x = x + STAGE == lds + NB * STAGE ? lds : x + STAGE;
+          read_b(x, u ^ 1);
+          read_a(x, u ^ 1, 0);
+          ++s;
+        } else more = false;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -114,32 +165,40 @@ __global__ __launch_bounds__(64 * WN, 2) void k_grouped_dw(GroupedDw p, int mtil
           for (int i = 0; i < NT; ++i) acc[i][2 * j + m] = OP::mul(b[u][i], a[(u * S + j) & 1][m], acc[i][2 * j + m]);
         __builtin_amdgcn_sched_barrier(0);
       }
+    }
   }
 
   const bool wide = wide_rows(p.dw_type, p.K);
-  const int64_t c = n0 + wave * 32 + 8 * g;
-  if (c >= p.K) return;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int64_t row = m0 + 16 * m + r;
+    const int64_t row = m0 + wm * 16 * MT + 16 * m + r;
     if (row >= p.N) continue;
-    float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = acc[i / 4][m][i % 4];
-    store_values<8>(p.dw, p.dw_type, ((int64_t)e * p.N + row) * p.K + c, p.K - c, wide, v);
+    for (int i = 0; i < NT; i += 2) {
+      const int64_t c = n0 + wn * 64 + 16 * i + 8 * g;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = acc[i + j / 4][m][j % 4];
+      if (c < p.K) store_values<8>(p.dw, p.dw_type, ((int64_t)e * p.N + row) * p.K + c, p.K - c, wide, v);
+    }
   }
 }
 
-template <class OP, int WN, int MT, bool FAR>
+template <class OP, int WN, int MT, int NB, bool FAR>
 hipError_t dw(const GroupedDw &p, hipStream_t s) {
-  const int64_t mt = (p.N + 16 * MT - 1) / (16 * MT), nt = (p.K + 32 * WN - 1) / (32 * WN);
-  hipLaunchKernelGGL((k_grouped_dw<OP, WN, MT, FAR>), dim3((unsigned)((p.E * mt * nt + 7) / 8 * 8)), dim3(64 * WN), 0, s, p, (int)mt, (int)nt);
+  const int64_t mt = (p.N + 32 * MT - 1) / (32 * MT), nt = (p.K + 64 * WN - 1) / (64 * WN);
+  const dim3 g((unsigned)((p.E * mt * nt + 7) / 8 * 8)), b(128 * WN);
+  if (p.perm) hipLaunchKernelGGL((k_grouped_dw<OP, WN, MT, NB, true, FAR>), g, b, 0, s, p, (int)mt, (int)nt);
+  else hipLaunchKernelGGL((k_grouped_dw<OP, WN, MT, NB, false, FAR>), g, b, 0, s, p, (int)mt, (int)nt);
   return hipGetLastError();
 }
 template <class OP>
 hipError_t choose_dw(const GroupedDw &p, hipStream_t s) {
-  if (p.perm && p.T * p.ldx > kRange) return dw<OP, 4, 8, true>(p, s);
-  return p.P / p.E > 256 && p.E * p.N * p.K >= (1 << 25) ? dw<OP, 8, 16, false>(p, s) : dw<OP, 4, 8, false>(p, s);
+  // offsets of an expert's rows, and of those that the permutation names
+  if (p.P * p.lddy > kRange || (p.perm ? p.T : p.P) * p.ldx > kRange) return dw<OP, 2, 4, 4, true>(p, s);
+  // Tiles of 256 x 256 (one workgroup on a CU) as long as all CUs have one, else 128 x 128 (two): 1024 of the large
+  // tiles 160 us and 199, 480 of them 46 and 52, 128 of them 120 and 95, 4 of them 53 and 25.
+  return p.E * ((p.N + 255) / 256) * ((p.K + 255) / 256) >= 256 ? dw<OP, 4, 8, 4, false>(p, s) : dw<OP, 2, 4, 4, false>(p, s);
 }
 
 // ---------------------------------------------------------------- gradients of shared rows
@@ -180,8 +239,8 @@ __global__ __launch_bounds__(256) void k_grouped_add_up(void *dx, int64_t ldo, i
 
 hipError_t launch_grouped_dw(const GroupedDw &p, hipStream_t s) { return p.type == DS4MOE_BF16 ? choose_dw<OpBf16>(p, s) : choose_dw<OpF16>(p, s); }
 
-hipError_t launch_grouped_places(int32_t *places, const int32_t *perm, int32_t P, int32_t A, hipStream_t s) {
-  hipLaunchKernelGGL(k_grouped_no_places, dim3((A + 255) / 256), dim3(256), 0, s, places, A);
+hipError_t launch_grouped_places(int32_t *places, const int32_t *perm, int32_t P, int32_t A, bool clear, hipStream_t s) {
+  if (clear) hipLaunchKernelGGL(k_grouped_no_places, dim3((A + 255) / 256), dim3(256), 0, s, places, A);
   if (P) hipLaunchKernelGGL(k_grouped_places, dim3((P + 255) / 256), dim3(256), 0, s, places, perm, P, A);
   return hipGetLastError();
 }
