@@ -151,8 +151,8 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, perm
         y_dtype = x.dtype if y_dtype is None else y_dtype
     kind = _real(y_dtype, "y_dtype")
     y = _empty(P, N, dtype=y_dtype, device=i)
-    if P == 0:
-        return y
+    if P == 0 or T == 0:
+        return y.zero_()
     dims = B.GroupedDims(_TYPES[x.dtype], kind, E, k, P, T, N, K)
     _call(_L.ds4moe_grouped_matmul, "grouped_matmul", i, _byref(dims), y.data_ptr(), N, x.data_ptr(), ldx, sx, w.data_ptr(),
           sw, offsets.data_ptr(), at)
@@ -181,7 +181,7 @@ def grouped_matmul_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, 
     dx = dw = None
     if need_dx:
         dx = _empty(T, K, dtype=x.dtype, device=i)
-        if P == 0:
+        if P == 0 or T == 0:
             dx.zero_()
         else:
             dims = B.GroupedDims(half, half, E, k, P, T, N, K)
@@ -193,7 +193,10 @@ def grouped_matmul_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, 
                   offsets.data_ptr(), at, None if ws is None else ws.data_ptr(), n)
     if need_dw:
         dw = _empty(E, N, K, dtype=dw_dtype, device=i)
-        dims = B.GroupedDims(half, kind, E, k, P, T, N, K)
-        _call(_L.ds4moe_grouped_dw, "grouped_dw", i, _byref(dims), dw.data_ptr(), dy.data_ptr(), ldy, x.data_ptr(), ldx,
-              offsets.data_ptr(), at)
+        if P == 0 or T == 0:
+            dw.zero_()
+        else:
+            dims = B.GroupedDims(half, kind, E, k, P, T, N, K)
+            _call(_L.ds4moe_grouped_dw, "grouped_dw", i, _byref(dims), dw.data_ptr(), dy.data_ptr(), ldy, x.data_ptr(), ldx,
+                  offsets.data_ptr(), at)
     return dx, dw
