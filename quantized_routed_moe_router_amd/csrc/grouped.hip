@@ -170,31 +170,39 @@ __device__ __forceinline__ void multiply_tile(const Grouped &p, const Segment &t
 }
 
 // Eight waves (256 columns) with the LDS of a CU, or four (128 columns) with
-// half of it.  A tile runs in the smallest instance that has its rows.
-template <class OP, bool TURNED, int WN>
-__global__ __launch_bounds__(64 * WN, 2) void k_grouped(Grouped p, int ntiles, int height) {
+// half of it.  HEIGHT: of the tiles, 0 for one that suits the numbers of rows;
+// a tile runs in the smallest instance that has its rows.
+template <class OP, bool TURNED, int WN, int HEIGHT>
+__global__ __launch_bounds__(64 * WN, 2) void k_grouped(Grouped p, int ntiles) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   if (TURNED)
     for (int i = blockIdx.x * 64 * WN + threadIdx.x; i < p.n_places; i += gridDim.x * 64 * WN) p.places[i] = -1;
   Finder f;
   f.load(p.offsets, p.E, p.P);
-  if (height) f.set_height(height);
-  else if (WN == 8) f.choose_height({256, 224, 192, 176, 160, 144, 128}, ntiles, 256);
-  else f.choose_height({192, 160, 128, 64}, ntiles, 512);
+  if (HEIGHT) f.set_height(HEIGHT);
+  else if (WN == 8) f.choose_height<8>({256, 224, 192, 160, 128}, ntiles);
+  else f.choose_height<9>({192, 160, 128, 64}, ntiles);
   const int mtiles = f.count();
   int mt, nt;
   if (!place_tile<4>(blockIdx.x, mtiles, ntiles, mt, nt)) return;
   const Segment t = f.find(mt);
   const int64_t n0 = (int64_t)nt * 32 * WN;
-  if (t.e < 0) zero_rows(p.y, p.y_type, p.ldy, t.p0, t.n, n0, min(n0 + 32 * WN, p.N));
-  else if (t.n <= 64) multiply_tile<OP, TURNED, WN, 4, WN == 8 ? 4 : 3, false>(p, t, n0, lds);
-  else if (t.n <= 128) multiply_tile<OP, TURNED, WN, 8, WN == 8 ? 3 : 2, false>(p, t, n0, lds);
-  else if (t.n <= 160) multiply_tile<OP, TURNED, WN, 10, 2, false>(p, t, n0, lds);
-  else if constexpr (WN == 4) multiply_tile<OP, TURNED, WN, 12, 2, false>(p, t, n0, lds);
-  else if (t.n <= 176) multiply_tile<OP, TURNED, WN, 11, 2, false>(p, t, n0, lds);
-  else if (t.n <= 192) multiply_tile<OP, TURNED, WN, 12, 2, false>(p, t, n0, lds);
-  else if (t.n <= 224) multiply_tile<OP, TURNED, WN, 14, 2, false>(p, t, n0, lds);
-  else multiply_tile<OP, TURNED, WN, 16, 2, false>(p, t, n0, lds);
+  if (t.e < 0) {
+    zero_rows(p.y, p.y_type, p.ldy, t.p0, t.n, n0, min(n0 + 32 * WN, p.N));
+    return;
+  }
+  if (HEIGHT == 64 || t.n <= 64) return multiply_tile<OP, TURNED, WN, 4, WN == 8 ? 4 : 3, false>(p, t, n0, lds);
+  if constexpr (HEIGHT != 64) {
+    if (HEIGHT == 128 || t.n <= 128) return multiply_tile<OP, TURNED, WN, 8, WN == 8 ? 3 : 2, false>(p, t, n0, lds);
+  }
+  if constexpr (HEIGHT == 0) {
+    if (t.n <= 160) return multiply_tile<OP, TURNED, WN, 10, 2, false>(p, t, n0, lds);
+    if (WN == 4 || t.n <= 192) return multiply_tile<OP, TURNED, WN, 12, 2, false>(p, t, n0, lds);
+    if constexpr (WN == 8) {
+      if (t.n <= 224) return multiply_tile<OP, TURNED, WN, 14, 2, false>(p, t, n0, lds);
+      multiply_tile<OP, TURNED, WN, 16, 2, false>(p, t, n0, lds);
+    }
+  }
 }
 template <class OP>
 __global__ __launch_bounds__(512, 2) void k_grouped_far(Grouped p, int ntiles) {
@@ -217,11 +225,11 @@ dim3 grid(const Grouped &p, int height, int64_t &nt) {
   nt = (p.N + 32 * WN - 1) / (32 * WN);
   return dim3((unsigned)((mt * nt + 7) / 8 * 8));
 }
-template <class OP, bool TURNED, int WN>
-hipError_t tiled(const Grouped &p, int height, hipStream_t s) {
+template <class OP, bool TURNED, int WN, int HEIGHT>
+hipError_t tiled(const Grouped &p, hipStream_t s) {
   int64_t nt;
-  const dim3 g = grid<WN>(p, height ? height : WN == 8 ? 128 : 64, nt);
-  hipLaunchKernelGGL((k_grouped<OP, TURNED, WN>), g, dim3(64 * WN), WN * LDS_PER_WAVE, s, p, (int)nt, height);
+  const dim3 g = grid<WN>(p, HEIGHT ? HEIGHT : WN == 8 ? 128 : 64, nt);
+  hipLaunchKernelGGL((k_grouped<OP, TURNED, WN, HEIGHT>), g, dim3(64 * WN), WN * LDS_PER_WAVE, s, p, (int)nt);
   return hipGetLastError();
 }
 template <class OP>
@@ -232,32 +240,40 @@ hipError_t tiled_far(const Grouped &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rules, times in us on one MI355X with bf16 weights of 2048 x 4096 (h: height
-// of the tiles; choice: the height that the kernel finds):
-//   eight waves from P N = 2^25 on: 16384 rows of 8 experts 248 (four waves
-//   257), 16384 of 256 experts 782 (822); below, 8192 of 8 experts 158 (153),
-//   4096 of 256 experts 789 (759), 2048 of 8 experts 59 (54).
-//   Tiles as high as the rows of an expert, so that its weights are read once:
-//   eight waves, 64 rows each, h 128 782 and h 64 920; four waves, 64 rows
-//   each, h 64 28.4, h 128 42.5 and the choice 29.9; 128 rows each, h 64 44.7
-//   and the choice 45.2; 256 rows each, h 64 66 and the choice 55.
-template <class OP, bool TURNED>
+// Rules, with times in us on one MI355X of bf16 matrices of 2048 x 4096.
+// Few rows an expert: tiles as high as those, so that its weights are read
+// once.  64 rows each: of 256 experts eight waves 782 at a height of 128 and
+// 920 at 64 (four waves 822), of 8 experts four waves 28 at 64, 43 at 128, 30
+// with the choice (eight 39); 128 rows each of 8 experts 45 at 64, 48 at 128.
+// Many rows: 2048 each of 8 experts 248 by eight waves with the choice and 256
+// by four, 1024 each 154 and 152, 256 each 60 and 56.
+template <class OP>
 hipError_t choose(const Grouped &p, hipStream_t s) {
   const int64_t mean = p.offsets ? p.P / p.E : p.P;  // rows of an expert
-  if (p.P * p.N >= (1 << 25)) return tiled<OP, TURNED, 8>(p, mean <= 128 ? 128 : 0, s);
-  return tiled<OP, TURNED, 4>(p, mean <= 64 ? 64 : 0, s);
+  if (p.P * p.N >= (1 << 25)) return mean <= 128 ? tiled<OP, false, 8, 128>(p, s) : tiled<OP, false, 8, 0>(p, s);
+  return mean <= 64 ? tiled<OP, false, 4, 64>(p, s) : tiled<OP, false, 4, 0>(p, s);
+}
+// Turned weights, fp32 results: of 256 experts 64 rows each eight waves 857 and
+// four 943, 16 rows each 774 and 830, of 60 experts (488 x 1000) 62 rows each
+// 21.7 and 19.7; of 8 experts 1024 rows each eight waves with the choice 149 to
+// 165 and four 149, 2048 rows each 290 and 271.
+template <class OP>
+hipError_t choose_turned(const Grouped &p, hipStream_t s) {
+  const int64_t mean = p.P / p.E;
+  if (mean <= 128 && p.E * ((p.N + 255) / 256) >= 1024) return tiled<OP, true, 8, 128>(p, s);
+  return mean <= 64 ? tiled<OP, true, 4, 64>(p, s) : tiled<OP, true, 4, 0>(p, s);
 }
 
 }  // namespace
 
 hipError_t launch_grouped(const Grouped &p, hipStream_t s) {
-  if (p.turned) return p.type == DS4MOE_BF16 ? choose<OpBf16, true>(p, s) : choose<OpF16, true>(p, s);
+  if (p.turned) return p.type == DS4MOE_BF16 ? choose_turned<OpBf16>(p, s) : choose_turned<OpF16>(p, s);
   if (p.offsets ? p.P <= 2 * p.E : p.P <= 64) return launch_grouped_few(p, p.offsets ? 16 : p.P, s);
   if (p.perm && p.T * p.ldx > kRange)  // rows that 32-bit offsets do not reach
     return p.type == DS4MOE_BF16 ? tiled_far<OpBf16>(p, s) : p.type == DS4MOE_F16 ? tiled_far<OpF16>(p, s) : tiled_far<OpI8>(p, s);
-  if (p.type == DS4MOE_BF16) return choose<OpBf16, false>(p, s);
-  if (p.type == DS4MOE_F16) return choose<OpF16, false>(p, s);
-  return choose<OpI8, false>(p, s);
+  if (p.type == DS4MOE_BF16) return choose<OpBf16>(p, s);
+  if (p.type == DS4MOE_F16) return choose<OpF16>(p, s);
+  return choose<OpI8>(p, s);
 }
 
 }  // namespace ds4
