@@ -13,42 +13,60 @@ namespace ds4 {
 namespace {
 
 // workgroups of a launch; what is beyond goes round
-unsigned groups(int64_t n) { return (unsigned)(n < (1 << 20) ? n : 1 << 20); }
+unsigned groups(int64_t n, int64_t most = 1 << 20) { return (unsigned)(n < most ? n : most); }
 
+// 8 adjacent values as they lie in memory: adjacent lanes read adjacent 16
+// bytes of 16-bit values, and a row of 4096 of them takes a lane 32 registers
 template <int TYPE>
-__device__ __forceinline__ float value_at(const void *src, int64_t i) {
-  if (TYPE == DS4MOE_F32) return ((const float *)src)[i];
-  if (TYPE == DS4MOE_BF16) return bf16_bits_to_float(((const uint16_t *)src)[i]);
-  return (float)((const half_t *)src)[i];
-}
+struct Eight {
+  static constexpr bool WIDE = TYPE == DS4MOE_F32;
+  u4 u[WIDE ? 2 : 1];
 
-// 16 adjacent values from column c on, zeros past the end of `cols`
-template <int TYPE>
-__device__ __forceinline__ void load_values16(const void *src, int64_t row, int64_t c, int64_t cols, bool vec, float (&v)[16]) {
-  if (vec && c + 16 <= cols) {
-    if (TYPE == DS4MOE_F32) {
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const f4 u = *reinterpret_cast<const f4 *>((const float *)src + row + c + i);
-#pragma unroll
-        for (int l = 0; l < 4; ++l) v[i + l] = u[l];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; i += 8) {
-        const u4 u = load16((const uint16_t *)src + row + c + i);
-#pragma unroll
-        for (int l = 0; l < 8; ++l) {
-          const uint16_t b = (uint16_t)(u[l / 2] >> (16 * (l & 1)));
-          v[i + l] = TYPE == DS4MOE_BF16 ? bf16_bits_to_float(b) : half_bits_to_float(b);
-        }
-      }
+  // from column c on, zeros past the end of `cols`; vec: aligned to 16 bytes
+  __device__ __forceinline__ void load(const void *src, int64_t row, int64_t c, int64_t cols, bool vec) {
+    if (vec && c + 8 <= cols) {
+      u[0] = load16((const char *)src + (row + c) * (WIDE ? 4 : 2));
+      if (WIDE) u[WIDE] = load16((const char *)src + (row + c) * 4 + 16);
+      return;
     }
-    return;
-  }
+    uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = c + i < cols ? value_at<TYPE>(src, row + c + i) : 0.0f;
-}
+    for (int i = 0; i < 8; ++i)
+      w[i] = c + i >= cols ? 0u : WIDE ? ((const uint32_t *)src)[row + c + i] : (uint32_t)((const uint16_t *)src)[row + c + i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (WIDE) {
+        u[0][i] = w[i];
+        u[WIDE][i] = w[4 + i];
+      } else u[0][i] = w[2 * i] | w[2 * i + 1] << 16;
+    }
+  }
+  __device__ __forceinline__ float value(int i) const {
+    if (WIDE) return __uint_as_float(u[WIDE ? i >> 2 : 0][i & 3]);
+    const uint32_t d = u[0][i >> 1];
+    if (TYPE == DS4MOE_BF16) return __uint_as_float(i & 1 ? d & 0xFFFF0000u : d << 16);
+    return half_bits_to_float((uint16_t)(i & 1 ? d >> 16 : d & 0xFFFFu));
+  }
+  // the largest magnitude so far as bits of the type, two halves side by side
+  __device__ __forceinline__ uint32_t largest(uint32_t m) const {
+    typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (WIDE) {
+        m = max(m, u[0][i] & 0x7FFFFFFFu);
+        m = max(m, u[WIDE][i] & 0x7FFFFFFFu);
+      } else
+        m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, m), __builtin_bit_cast(us2, u[0][i] & 0x7FFF7FFFu)));
+    }
+    return m;
+  }
+  // and as bits of an fp32 number (NaN and infinity come out on top)
+  static __device__ __forceinline__ uint32_t as_float(uint32_t m) {
+    if (WIDE) return m;
+    m = max(m & 0xFFFFu, m >> 16);
+    return TYPE == DS4MOE_BF16 ? m << 16 : __float_as_uint(half_bits_to_float((uint16_t)m)) & 0x7FFFFFFFu;
+  }
+};
 
 struct RowScale {
   float scale, unit, up, inv;  // codes are of up x in units of `unit` = up scale
@@ -77,68 +95,60 @@ __device__ __forceinline__ int exact_code(float x, const RowScale &s) {
   return min(max((int)q, -127), 127);
 }
 
-// the largest magnitude of some values, as bits
-__device__ __forceinline__ uint32_t largest(uint32_t m, const float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-    m = m > b ? m : b;
-  }
-  return m;
-}
-
-// codes of 16 values
-__device__ __forceinline__ u4 codes_of(const float (&v)[16], const RowScale &s) {
+// codes of 8 values
+template <int TYPE>
+__device__ __forceinline__ u2 codes_of(const Eight<TYPE> &v, const RowScale &s) {
   constexpr float kShift = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer, which the low bits then are
   float off = s.up == 1.0f ? 0.0f : 1.0f;
-  uint32_t q[16];
+  uint32_t q[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float u = fmaf(v[i], s.inv, kShift);
+  for (int i = 0; i < 8; ++i) {
+    const float x = v.value(i), u = fmaf(x, s.inv, kShift);
     q[i] = __float_as_uint(u);
-    off = fmaxf(off, fabsf(fmaf(v[i], s.inv, kShift - u)));
+    off = fmaxf(off, fabsf(fmaf(x, s.inv, kShift - u)));
   }
   if (off > 0.4999f) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = (uint32_t)exact_code(v[i], s);
+    for (int i = 0; i < 8; ++i) q[i] = (uint32_t)exact_code(v.value(i), s);
   }
-  u4 o;
+  u2 o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = __builtin_amdgcn_perm(q[4 * i + 1], q[4 * i], 0x0C0C0400), hi = __builtin_amdgcn_perm(q[4 * i + 3], q[4 * i + 2], 0x04000C0C);
-    o[i] = lo | hi;
-  }
+  for (int i = 0; i < 2; ++i)
+    o[i] = __builtin_amdgcn_perm(q[4 * i + 1], q[4 * i], 0x0C0C0400) | __builtin_amdgcn_perm(q[4 * i + 3], q[4 * i + 2], 0x04000C0C);
   return o;
 }
 
-// L lanes to a row, 16 values a lane at a time; up to KEEP steps stay in
-// registers between the maximum and the codes, more are read again.  Up to 4096
-// columns a row is one wave's, which needs no barrier.
+// L lanes to a row, 8 values a lane at a time; up to 8 steps stay in registers
+// between the maximum and the codes, more are read again.  Up to 4096 columns a
+// row is one wave's, which needs no barrier.  Bound by the memory: of the bytes
+// that go in and out, 8192 x 4096 bf16 take 29.4 us (3.4 TB/s; a copy reaches
+// 4.9), 65536 x 4096 232 us (3.5).
 template <int TYPE, int L>
 __global__ __launch_bounds__(256) void k_int8_quantize(int8_t *codes, float *scales, const void *src, int64_t rows, int64_t cols,
                                                        int64_t ld, bool vec) {
-  constexpr int KEEP = 4;
+  constexpr int KEEP = L == 16 ? 2 : 8;
   __shared__ uint32_t tops[4];
   const int l = threadIdx.x % L;
   const int64_t to = (cols + 15) / 16 * 16;
   for (int64_t row0 = (int64_t)blockIdx.x * (256 / L); row0 < rows; row0 += (int64_t)gridDim.x * (256 / L)) {
     const int64_t row = row0 + threadIdx.x / L, at = row * ld;
     const bool in = row < rows;
-    float v[KEEP][16];
+    Eight<TYPE> v[KEEP];
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < KEEP; ++j) {
-      const int64_t c = (int64_t)(j * L + l) * 16;
-      if (in && c < cols) load_values16<TYPE>(src, at, c, cols, vec, v[j]);
+      const int64_t c = (int64_t)(j * L + l) * 8;
+      if (in && c < to) v[j].load(src, at, c, cols, vec);
     }
 #pragma unroll
     for (int j = 0; j < KEEP; ++j)
-      if (in && (int64_t)(j * L + l) * 16 < cols) m = largest(m, v[j]);
-    for (int64_t c = (int64_t)(KEEP * L + l) * 16; in && c < cols; c += L * 16) {
-      float u[16];
-      load_values16<TYPE>(src, at, c, cols, vec, u);
-      m = largest(m, u);
+      if (in && (int64_t)(j * L + l) * 8 < to) m = v[j].largest(m);
+    for (int64_t c = (int64_t)(KEEP * L + l) * 8; in && c < to; c += L * 8) {
+      Eight<TYPE> u;
+      u.load(src, at, c, cols, vec);
+      m = u.largest(m);
     }
+    m = Eight<TYPE>::as_float(m);
 #pragma unroll
     for (int d = 1; d < (L < 64 ? L : 64); d *= 2) {
       const uint32_t o = (uint32_t)__shfl_xor((int)m, d);
@@ -155,19 +165,21 @@ __global__ __launch_bounds__(256) void k_int8_quantize(int8_t *codes, float *sca
     const RowScale s = row_scale(m);
 #pragma unroll
     for (int j = 0; j < KEEP; ++j) {
-      const int64_t c = (int64_t)(j * L + l) * 16;
-      if (c < cols) *reinterpret_cast<u4 *>(codes + row * to + c) = codes_of(v[j], s);
+      const int64_t c = (int64_t)(j * L + l) * 8;
+      if (c < to) *reinterpret_cast<u2 *>(codes + row * to + c) = codes_of(v[j], s);
     }
-    for (int64_t c = (int64_t)(KEEP * L + l) * 16; c < cols; c += L * 16) {
-      float u[16];
-      load_values16<TYPE>(src, at, c, cols, vec, u);
-      *reinterpret_cast<u4 *>(codes + row * to + c) = codes_of(u, s);
+    for (int64_t c = (int64_t)(KEEP * L + l) * 8; c < to; c += L * 8) {
+      Eight<TYPE> u;
+      u.load(src, at, c, cols, vec);
+      *reinterpret_cast<u2 *>(codes + row * to + c) = codes_of(u, s);
     }
     if (l == 0) scales[row] = s.scale;
   }
 }
 
-// 16 values a lane
+// 16 values a lane.  Bound by the memory: 8192 x 4096 to bf16 17.2 us (5.9 TB/s
+// of codes and values, some of which stay in the cache), 65536 x 4096 138 us
+// (5.8 TB/s).
 __global__ __launch_bounds__(256) void k_int8_dequantize(void *dst, int type, int64_t ld, const int8_t *codes, const float *scales,
                                                          int64_t cols, uint32_t per, int64_t total, bool wide) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
@@ -187,7 +199,11 @@ hipError_t quantize(int8_t *codes, float *scales, const void *src, int64_t rows,
   const bool vec = ((uintptr_t)src % 16) == 0 && (ld * el) % 16 == 0;
   auto f = cols <= 256 ? k_int8_quantize<TYPE, 16> : cols <= 4096 ? k_int8_quantize<TYPE, 64> : k_int8_quantize<TYPE, 256>;
   const int64_t per = cols <= 256 ? 16 : cols <= 4096 ? 4 : 1;
-  hipLaunchKernelGGL(f, dim3(groups((rows + per - 1) / per)), dim3(256), 0, s, codes, scales, src, rows, cols, ld, vec);
+  // Four workgroups a CU, which go round, against one for every row's place:
+  // 8192 x 4096 29.4 us (32.2), 8192 x 1024 8.5 (9.9), 4096 x 16384 37.2
+  // (41.2), 65536 x 4096 232 (237).  Short rows take sixteen: 100000 x 256 17.3
+  // us (all 18.2, four 20.2).
+  hipLaunchKernelGGL(f, dim3(groups((rows + per - 1) / per, cols <= 256 ? 4096 : 1024)), dim3(256), 0, s, codes, scales, src, rows, cols, ld, vec);
   return hipGetLastError();
 }
 
@@ -240,19 +256,23 @@ __global__ __launch_bounds__(64 * QW, 4) void k_int8_few(QuantProduct p) {
   __syncthreads();
   const int row = tid / p.per, l = tid % p.per;
   const bool in = row < p.M;
+  constexpr int KEEP = 2;
+  Eight<TYPE> v[KEEP];
   uint32_t m = 0;
-  float first[16];
   if (in) {
-    for (int64_t c = (int64_t)l * 16; c < p.K; c += p.per * 16) {
-      float v[16];
-      load_values16<TYPE>(p.a, row * p.lda, c, p.K, p.vec, v);
-      m = largest(m, v);
-      if (c == (int64_t)l * 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) first[i] = v[i];
-      }
+    for (int j = 0; j < KEEP; ++j)
+      if ((j * p.per + l) * 8 < K16) v[j].load(p.a, row * p.lda, (j * p.per + l) * 8, p.K, p.vec);
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j)
+      if ((j * p.per + l) * 8 < K16) m = v[j].largest(m);
+    for (int c = (KEEP * p.per + l) * 8; c < K16; c += p.per * 8) {
+      Eight<TYPE> u;
+      u.load(p.a, row * p.lda, c, p.K, p.vec);
+      m = u.largest(m);
     }
   }
+  m = Eight<TYPE>::as_float(m);
   for (int d = 1; d < min(p.per, 64); d *= 2) {
     const uint32_t o = (uint32_t)__shfl_xor((int)m, d);
     m = m > o ? m : o;
@@ -262,10 +282,14 @@ __global__ __launch_bounds__(64 * QW, 4) void k_int8_few(QuantProduct p) {
   if (in) {
     const RowScale s = row_scale(tops[row]);
     if (l == 0) scales[row] = s.scale;
-    for (int64_t c = (int64_t)l * 16; c < p.K; c += p.per * 16) {
-      float v[16];
-      if (c != (int64_t)l * 16) load_values16<TYPE>(p.a, row * p.lda, c, p.K, p.vec, v);
-      *reinterpret_cast<u4 *>(codes + row * step + c) = c == (int64_t)l * 16 ? codes_of(first, s) : codes_of(v, s);
+    char *const to = codes + row * step;
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j)
+      if ((j * p.per + l) * 8 < K16) *reinterpret_cast<u2 *>(to + (j * p.per + l) * 8) = codes_of(v[j], s);
+    for (int c = (KEEP * p.per + l) * 8; c < K16; c += p.per * 8) {
+      Eight<TYPE> u;
+      u.load(p.a, row * p.lda, c, p.K, p.vec);
+      *reinterpret_cast<u2 *>(to + c) = codes_of(u, s);
     }
   }
   __syncthreads();
@@ -287,10 +311,10 @@ __global__ __launch_bounds__(64 * QW, 4) void k_int8_few(QuantProduct p) {
   if (wave || r >= p.M || n >= p.N) return;
 #pragma unroll
   for (int i = 0; i < QW - 1; ++i) acc += part[i * 64 + lane];
-  float v[4];
+  float y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = (float)acc[i] * scales[r] * p.ws[min(n + i, p.N - 1)];
-  store_values<4>(p.y, p.y_type, r * p.ldy + n, p.N - n, p.ldy % 4 == 0, v);
+  for (int i = 0; i < 4; ++i) y[i] = (float)acc[i] * scales[r] * p.ws[min(n + i, p.N - 1)];
+  store_values<4>(p.y, p.y_type, r * p.ldy + n, p.N - n, p.ldy % 4 == 0, y);
 }
 
 }  // namespace
@@ -319,7 +343,11 @@ hipError_t launch_int8_dequantize(void *dst, int32_t type, int64_t ld, const int
                                   int64_t cols, hipStream_t s) {
   const int64_t per = (cols + 15) / 16, total = rows * per, el = type == DS4MOE_F32 ? 4 : 2;
   const bool wide = ((uintptr_t)dst % 16) == 0 && (ld * el) % 16 == 0;
-  hipLaunchKernelGGL(k_int8_dequantize, dim3(groups((total + 255) / 256)), dim3(256), 0, s, dst, type, ld, codes, scales, cols,
+  // sixteen workgroups a CU, which go round, as long as there are few rounds
+  // (8192 x 4096 17.2 us, one for every place 19.7; 100000 x 256 13.7, 16.2),
+  // and one for every place beyond (65536 x 4096 138 us, going round 179)
+  const int64_t all = (total + 255) / 256;
+  hipLaunchKernelGGL(k_int8_dequantize, dim3(groups(all, all <= 16384 ? 4096 : 1 << 20)), dim3(256), 0, s, dst, type, ld, codes, scales, cols,
                      (uint32_t)per, total, wide);
   return hipGetLastError();
 }

@@ -202,3 +202,26 @@ def test_routed_experts_of_8_bits_run_together():
             want[t] += v
             mag[t] += np.abs(v)
     assert (np.abs(out.cpu().double().numpy() - want) <= 2.0**-20 * mag).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(9001, 40), (65549, 250), (4103, 300), (9000, 264), (2050, 4097), (70000, 272)])
+def test_more_rows_than_workgroups_go_round(rows, cols):
+    q = _q()
+    x = (np.random.default_rng(rows).standard_normal((rows, cols)) * 3).astype(np.float32)
+    codes, scales = q.int8_quantize(dev(x))
+    rc, rs = R.quantize(x)
+    assert same(scales.cpu().numpy(), rs) and same(codes.cpu().numpy(), rc)
+    got = q.int8_dequantize(codes, scales, cols)
+    assert np.array_equal(got.cpu().numpy(), (rc.astype(np.float32) * rs[:, None])[:, :cols])
+
+
+@pytest.mark.parametrize("M,K", [(1, 65520), (1, 65521), (2, 32752), (15, 4336), (16, 4080), (16, 4081), (9, 7200)])
+def test_rows_up_to_the_size_of_a_workgroups_memory(M, K):
+    """The longest rows that are quantised in the product's own launch, and the shortest that are not: the same bits as of
+    two calls."""
+    q = _q()
+    rng = np.random.default_rng(K)
+    a = dev(rng.standard_normal((M, K)).astype(np.float32))
+    w, sw = q.int8_quantize(dev(rng.standard_normal((33, K)).astype(np.float32)))
+    codes, sa = q.int8_quantize(a)
+    assert torch.equal(q.int8_matmul(a, w, sw, y_dtype=torch.float32), q.int8_matmul(codes, w, sw, sa, y_dtype=torch.float32))
