@@ -600,8 +600,8 @@ int ds4moe_int8_matmul(void *y, int32_t y_dtype, int64_t ldy, const void *a, con
  *   y_dtype    of the call's output: DS4MOE_F32, DS4MOE_BF16 or DS4MOE_F16
  *   n_experts  E: 1..512
  *   top_k      1..16 (1 without a permutation)
- *   rows       P, positions: 0..2^24
- *   tokens     T, rows of x: 0..2^24
+ *   rows       P, positions: 0..2^23
+ *   tokens     T, rows of x: 0..2^23
  *   N, K       1..65536; K values make a multiple of 16 bytes; N is a multiple
  *              of 8 in the gradients; no more than 2^37 values in P by N, P by
  *              K or E by N by K

@@ -194,8 +194,9 @@ hipError_t dw(const GroupedDw &p, hipStream_t s) {
 }
 template <class OP>
 hipError_t choose_dw(const GroupedDw &p, hipStream_t s) {
-  // offsets of an expert's rows, and of those that the permutation names
-  if (p.P * p.lddy > kRange || (p.perm ? p.T : p.P) * p.ldx > kRange) return dw<OP, 2, 4, 2, true>(p, s);
+  // offsets of an expert's rows, up to 31 past the last in the last stage, and of those that the permutation names
+  const int64_t end = (int64_t)p.P + 31;
+  if (end * p.lddy > kRange || (p.perm ? p.T : end) * p.ldx > kRange) return dw<OP, 2, 4, 2, true>(p, s);
   // Tiles of 256 x 256 (one workgroup on a CU) or 128 x 128 (three): 32768 of the large ones, 64 terms each, 1177 us and
   // 1279; 1024, 1024 terms each, 158 and 174; 480, 62 terms each, 46 and 40; 128, 4096 terms each, 121 and 93.
   return p.E * ((p.N + 255) / 256) * ((p.K + 255) / 256) >= 1024 ? dw<OP, 4, 8, 4, false>(p, s) : dw<OP, 2, 4, 2, false>(p, s);

@@ -265,3 +265,20 @@ def test_a_training_step_of_routed_experts():
         dls = 2 * (A[3].repeat_interleave(k, 0) * zs).sum(1).view(T, k).sum(1, keepdim=True)
     for got, want, mag in ((y, Y.detach(), (zs.view(T, k, H) * s[:, :, None]).sum(1)), (dx, gX, dxs), (dwd, gD, dws), (dwu, gU, dus), (dl, gL, dls)):
         assert (np.abs(host(got) - want.detach().numpy()) <= 2.0**-8 * mag.detach().numpy() + 1e-6).all()
+
+
+def test_gradients_of_rows_whose_last_stage_ends_beyond_32_bit_offsets():
+    """513 rows within 2^32 bytes, 544 of which (whole stages of 32) are not: what lies at the buffer's start, where their
+    offsets would come out again, adds nothing."""
+    q = _q()
+    P, step, N, K = 513, 8372128 // 2, 72, 64
+    rng = np.random.default_rng(0)
+    xs, ds = (torch.full((P * step,), 3.0, dtype=torch.bfloat16, device="cuda").view(P, step) for _ in range(2))
+    xv, dv = rng.integers(-8, 9, (P, K)) / 4.0, rng.integers(-8, 9, (P, N)) / 4.0
+    xs[:, :K], ds[:, :N] = torch.from_numpy(xv).to(torch.bfloat16).cuda(), torch.from_numpy(dv).to(torch.bfloat16).cuda()
+    w = torch.zeros(1, N, K, dtype=torch.bfloat16, device="cuda")
+    offsets = torch.tensor([0, P], dtype=torch.int32, device="cuda")
+    rows = rng.permutation(P).astype(np.int32)
+    for perm, order in ((None, np.arange(P)), (dev(rows), rows)):
+        _, dw = q.grouped_matmul_backward(ds[:, :N], xs[:, :K], w, offsets, perm, need_dx=False, dw_dtype=torch.float32)
+        assert np.array_equal(host(dw)[0], dv.T @ xv[order])  # sixteenths below 2^24 of them
