@@ -108,64 +108,82 @@ __global__ __launch_bounds__(128 * WN, 2) void k_grouped_dw(GroupedDw p, int mti
 #pragma unroll
     for (int i = 0; i < NT; ++i) b[u][i] = read_across((lds_at)x + lb[i / 2] + 8 * (i & 1), CB * 16);
   };
-  if (last >= 0) {
-    if (PERM) {
-      int first[NB][DB];
-#pragma unroll
-      for (int i = 0; i < NB; ++i) ask(i, first[i]);
-      ask(NB, named[0]);
-      ask(NB + 1, named[1]);
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        prepare(i, first[i]);
-        if (i <= last) load(i, lds + i * STAGE);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-        if (i <= last) load(i, lds + i * STAGE);
-    }
-  }
-  if (last >= NB - 1) wait_vm<(NB - 1) * D>();
-  else wait_vm<0>();
-  barrier_keep_loads();
   char *x = lds;
-  read_b(x, 0);
-  read_a(x, 0, 0);
   int s = 0;
   bool more = last >= 0;
-  while (more) {
+  // `all`: the sum has stages for all that is asked for here
+  auto begin = [&](bool all) __attribute__((always_inline)) {
+    int first[NB][DB];
+    if (PERM) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (!more) break;
-#pragma unroll
-      for (int j = 0; j < S; ++j) {
-        if (PERM && j == S / 2 && s + NB <= last) {
-          prepare(s + NB, named[u]);
-          ask(s + NB + 2, named[u]);
-          asm volatile("" ::: "memory");
-        }
-        if (j + 1 < S) read_a(x, u, j + 1);
-        else if (s < last) {
-          // younger than the next stage's loads: those of NB - 2 stages and the entries asked for in NB - 1
-          if (s + NB <= last) wait_vm<(NB - 2) * D + (PERM ? (NB - 1) * DB : 0)>();
-          else if (s + NB - 1 <= last) wait_vm<(NB - 2) * D>();
-          else wait_vm<0>();
-          barrier_keep_loads();
-          if (s + NB <= last) load(s + NB, x);
-          x = x + STAGE == lds + NB * STAGE ? lds : x + STAGE;
-          read_b(x, u ^ 1);
-          read_a(x, u ^ 1, 0);
-          ++s;
-        } else more = false;
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int i = 0; i < NT; ++i) acc[i][2 * j + m] = OP::mul(b[u][i], a[(u * S + j) & 1][m], acc[i][2 * j + m]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      for (int i = 0; i < NB; ++i) ask(i, first[i]);
     }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      if (PERM) {
+        if (i >= NB - 2) ask(i + 2, named[i - (NB - 2)]);  // in the order of the loop, whose waits count them
+        prepare(i, first[i]);
+      }
+      if (all || i <= last) load(i, lds + i * STAGE);
+    }
+  };
+  auto start = [&](bool all) __attribute__((always_inline)) {
+    // younger than the first stage's loads: those of NB - 1 stages, and of the entries that are asked for behind it
+    // (not counted where nobody may need them: they might not be asked for)
+    if (all) wait_vm<(NB - 1) * D + (PERM ? (NB > 2 ? 2 : 1) * DB : 0)>();
+    else if (last >= NB - 1) wait_vm<(NB - 1) * D>();
+    else wait_vm<0>();
+    barrier_keep_loads();
+    read_b(x, 0);
+    read_a(x, 0, 0);
+  };
+  // `all`: NB more stages follow this one
+  auto stage = [&](bool all, int u) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      if (PERM && j == S / 2 && (all || s + NB <= last)) {
+        prepare(s + NB, named[u]);
+        ask(s + NB + 2, named[u]);
+        asm volatile("" ::: "memory");
+      }
+      if (j + 1 < S) read_a(x, u, j + 1);
+      else if (all || s < last) {
+        // younger than the next stage's loads: those of NB - 2 stages and the entries asked for in NB - 1 (counted as above)
+        if (all) wait_vm<(NB - 2) * D + (PERM ? (NB - 1) * DB : 0)>();
+        else if (s + NB - 1 <= last) wait_vm<(NB - 2) * D>();
+        else wait_vm<0>();
+        barrier_keep_loads();
+        if (all || s + NB <= last) load(s + NB, x);
+        x = x + STAGE == lds + NB * STAGE ? lds : x + STAGE;
+        read_b(x, u ^ 1);
+        read_a(x, u ^ 1, 0);
+        ++s;
+      } else more = false;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i][2 * j + m] = OP::mul(b[u][i], a[(u * S + j) & 1][m], acc[i][2 * j + m]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Stages whose loads depend on nothing have a loop of their own: there the
+  // compiler knows how many loads are younger than an entry that it waits for.
+  // Behind a condition it waits for all of them.
+  if (last > NB) {
+    begin(true);
+    start(true);
+    while (s + NB < last) {
+      stage(true, 0);
+      stage(true, 1);
+    }
+  } else {
+    if (more) begin(false);
+    start(false);
+  }
+  while (more) {
+    stage(false, 0);
+    if (more) stage(false, 1);
   }
 
   const bool wide = wide_rows(p.dw_type, p.K);

@@ -282,3 +282,25 @@ def test_gradients_of_rows_whose_last_stage_ends_beyond_32_bit_offsets():
     for perm, order in ((None, np.arange(P)), (dev(rows), rows)):
         _, dw = q.grouped_matmul_backward(ds[:, :N], xs[:, :K], w, offsets, perm, need_dx=False, dw_dtype=torch.float32)
         assert np.array_equal(host(dw)[0], dv.T @ xv[order])  # sixteenths below 2^24 of them
+
+
+def test_weights_gradients_of_many_experts_with_middling_rows():
+    """Large tiles of experts whose sums are a few stages long, from one to a dozen: each of them ends in another part of
+    the loop."""
+    q = _q()
+    E, N, K = 512, 264, 264
+    rng = np.random.default_rng(5)
+    rows = np.arange(E) % 400
+    offsets = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    P = int(offsets[-1])
+    perm = rng.permutation(P).astype(np.int32)
+    x, xv = half(rng.integers(-8, 9, (P, K)) / 4.0, "bf16")
+    dy, dv = half(rng.integers(-8, 9, (P, N)) / 4.0, "bf16")
+    w = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda")
+    for at, order in ((dev(perm), perm), (None, np.arange(P))):
+        for _ in range(2):
+            _, dw = q.grouped_matmul_backward(dy, x, w, dev(offsets), at, need_dx=False, dw_dtype=torch.float32)
+            got = dw.cpu().numpy()
+            for e in range(E):
+                p = slice(offsets[e], offsets[e + 1])
+                assert np.array_equal(got[e], dv[p].T @ xv[order[p]]), (e, rows[e])  # sixteenths below 2^24 of them
