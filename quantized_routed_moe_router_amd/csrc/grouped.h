@@ -30,7 +30,7 @@ struct Grouped {
   int32_t n_places;
 };
 hipError_t launch_grouped(const Grouped &p, hipStream_t s);
-hipError_t launch_grouped_few(const Grouped &p, int rows, hipStream_t s);
+hipError_t launch_grouped_few(const Grouped &p, hipStream_t s);
 
 // dW_e = sum over p of dy[p] x[row(p)]^T
 struct GroupedDw {

@@ -268,7 +268,7 @@ hipError_t choose_turned(const Grouped &p, hipStream_t s) {
 
 hipError_t launch_grouped(const Grouped &p, hipStream_t s) {
   if (p.turned) return p.type == DS4MOE_BF16 ? choose_turned<OpBf16>(p, s) : choose_turned<OpF16>(p, s);
-  if (p.offsets ? p.P <= 2 * p.E : p.P <= 64) return launch_grouped_few(p, p.offsets ? 16 : p.P, s);
+  if (p.offsets ? p.P <= 2 * p.E : p.P <= 64) return launch_grouped_few(p, s);
   if (p.perm && p.T * p.ldx > kRange)  // rows that 32-bit offsets do not reach
     return p.type == DS4MOE_BF16 ? tiled_far<OpBf16>(p, s) : p.type == DS4MOE_F16 ? tiled_far<OpF16>(p, s) : tiled_far<OpI8>(p, s);
   if (p.type == DS4MOE_BF16) return choose<OpBf16>(p, s);

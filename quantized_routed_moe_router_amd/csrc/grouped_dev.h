@@ -8,7 +8,6 @@ namespace ds4 {
 
 typedef int i4 __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
-typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 
 // Matrix instructions of 16 x 16 whose operands are 16 bytes a lane: row
 // l % 16, bytes 16 (l / 16) .. of 64.  That is 32 columns of 16 bits or 64 of

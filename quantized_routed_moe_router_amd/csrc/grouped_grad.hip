@@ -5,6 +5,14 @@
 //
 // A workgroup of 2 WN waves has 32 MT rows and 64 WN columns of one dW_e, 32
 // terms of the sum at a time.  Both operands lie across.
+//
+// With many rows an expert it is the matrix units that bound it (a workgroup's
+// first loads and its results are not under another's products): 8 experts of
+// 1024 rows, 2048 x 4096, 155 us (0.89 PFLOP/s; the library's product of these
+// sizes reaches 1.5).  With few rows it is writing dW: 256 experts of 64 rows,
+// 1170 us for 4.4 GB (3.7 TB/s).  Left out, of 8192 rows: tiles of 128 x 256
+// 151 us and 1315 with 64 rows an expert; 256 x 256 in two buffers 148 and
+// 1237; one workgroup a CU that goes round 157 and 1298.
 #include "grouped_dev.h"
 
 namespace ds4 {
@@ -215,8 +223,8 @@ hipError_t choose_dw(const GroupedDw &p, hipStream_t s) {
   // offsets of an expert's rows, up to 31 past the last in the last stage, and of those that the permutation names
   const int64_t end = (int64_t)p.P + 31;
   if (end * p.lddy > kRange || (p.perm ? p.T : end) * p.ldx > kRange) return dw<OP, 2, 4, 2, true>(p, s);
-  // Tiles of 256 x 256 (one workgroup on a CU) or 128 x 128 (three): 32768 of the large ones, 64 terms each, 1177 us and
-  // 1279; 1024, 1024 terms each, 158 and 174; 480, 62 terms each, 46 and 40; 128, 4096 terms each, 121 and 93.
+  // Tiles of 256 x 256 (one workgroup on a CU) or 128 x 128 (three): 32768 of the large ones, 64 terms each, 1170 us and
+  // 1288; 1024, 1024 terms each, 155 and 158; 480, 62 terms each, 44 and 38; 128, 4096 terms each, 115 and 73.
   return p.E * ((p.N + 255) / 256) * ((p.K + 255) / 256) >= 1024 ? dw<OP, 4, 8, 4, false>(p, s) : dw<OP, 2, 4, 2, false>(p, s);
 }
 
@@ -233,7 +241,8 @@ __global__ __launch_bounds__(256) void k_grouped_places(int32_t *places, const i
   if (a >= 0 && a < A) atomicMax(places + a, i);
 }
 
-// dx[t] = sum over j of the rows of its assignments, in the order of j, in fp32 with one rounding
+// dx[t] = sum over j of the rows of its assignments, in the order of j, in fp32 with one rounding.  The rows are fp32 so
+// that there is one.  Bound by the memory: two rows each of 4096 tokens, 4096 wide, 29 us (134 MB in, 34 out, 5.8 TB/s).
 template <int NV>
 __global__ __launch_bounds__(256) void k_grouped_add_up(void *dx, int64_t ldo, int o_type, const float *rows, const int32_t *places, int T, int k, int64_t K) {
   const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * NV;

@@ -211,7 +211,10 @@ hipError_t quantize(int8_t *codes, float *scales, const void *src, int64_t rows,
 // A workgroup of eight waves has 16 weight rows and all of the M <= 16 rows of
 // a, which it quantises for itself: they come from L2, and a launch of their
 // own takes longer.  The weights' first lines are asked for before that.  Then
-// as the product of a few rows: the waves share the columns.
+// as the product of a few rows: the waves share the columns.  Bound by the
+// launch and the latency of what follows another (a row, its maximum, the
+// weights): one token, 2048 x 4096, 9.1 to 9.6 us a call (12.4 in two launches),
+// 1.7 of them for the weights' 8.4 MB.
 constexpr int QW = 8;                    // waves
 constexpr int QUANT_LDS = 64 << 10;      // bytes of codes
 
