@@ -13,7 +13,7 @@ namespace {
 constexpr int64_t kMaxRows = (int64_t)1 << 24;    // of a dense product
 constexpr int64_t kMaxGrouped = (int64_t)1 << 23;  // positions and tokens: entries of a permutation stay below 2^27
 constexpr int64_t kMaxDim = 65536;
-constexpr int64_t kMaxOut = (int64_t)1 << 37;  // values of a matrix (more than memory holds; keeps grids within 2^32 threads)
+constexpr int64_t kMaxOut = (int64_t)1 << 37;  // values of a matrix: launches have less than 2^32 threads
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
 constexpr int64_t kMaxRow = (int64_t)1 << 22;  // values from row to row of an operand
 constexpr int64_t kMaxSum8 = 131056;  // columns of 8-bit products: their sums stay in 32 bits at 128 x 128 a product
@@ -138,7 +138,7 @@ int ds4moe_grouped_dx(const ds4moe_grouped_dims *dims, void *dx, int64_t lddx, c
   p.P = p.T = (int32_t)d.rows;
   p.N = d.K;
   p.Kb = d.N * elem(d.dtype);
-  p.places = places;
+  p.places = perm ? places : nullptr;
   p.n_places = perm ? (int32_t)(d.tokens * d.top_k) : 0;
   hipError_t e = hipSuccess;
   if (d.rows) e = launch_grouped(p, s);

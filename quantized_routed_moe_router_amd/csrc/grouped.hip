@@ -189,7 +189,7 @@ template <class OP, bool TURNED, int WN, int HEIGHT>
 __global__ __launch_bounds__(64 * WN, 2) void k_grouped(Grouped p, int ntiles) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   if (TURNED)
-    for (int i = blockIdx.x * 64 * WN + threadIdx.x; i < p.n_places; i += gridDim.x * 64 * WN) p.places[i] = -1;
+    for (int64_t i = (int64_t)blockIdx.x * (64 * WN) + threadIdx.x; i < p.n_places; i += (int64_t)gridDim.x * (64 * WN)) p.places[i] = -1;
   Finder f;
   f.load(p.offsets, p.E, p.P);
   if (HEIGHT) f.set_height(HEIGHT);
@@ -232,56 +232,39 @@ __global__ __launch_bounds__(512, 2) void k_grouped_far(Grouped p, int ntiles) {
   else multiply_tile<OP, false, 8, 8, 3, true>(p, t, n0, lds);
 }
 
-template <int WN>
-dim3 grid(const Grouped &p, int height, int64_t &nt) {
-  const int64_t mt = grouped_max_tiles(p.offsets, p.E, p.P, height);
-  nt = (p.N + 32 * WN - 1) / (32 * WN);
-  return dim3((unsigned)((mt * nt + 7) / 8 * 8));
-}
 template <class OP, bool TURNED, int WN, int HEIGHT>
 hipError_t tiled(const Grouped &p, hipStream_t s) {
-  int64_t nt;
-  const dim3 g = grid<WN>(p, HEIGHT ? HEIGHT : WN == 8 ? 128 : 64, nt);
-  hipLaunchKernelGGL((k_grouped<OP, TURNED, WN, HEIGHT>), g, dim3(64 * WN), WN * LDS_PER_WAVE, s, p, (int)nt);
+  constexpr GroupedForm f{WN, HEIGHT};
+  const dim3 g((unsigned)grouped_workgroups(f, p.offsets, p.E, p.P, p.N));
+  hipLaunchKernelGGL((k_grouped<OP, TURNED, WN, HEIGHT>), g, dim3(64 * WN), WN * LDS_PER_WAVE, s, p, (int)grouped_col_tiles(f, p.N));
   return hipGetLastError();
 }
 template <class OP>
 hipError_t tiled_far(const Grouped &p, hipStream_t s) {
-  int64_t nt;
-  const dim3 g = grid<8>(p, 128, nt);
-  hipLaunchKernelGGL(k_grouped_far<OP>, g, dim3(512), 8 * LDS_PER_WAVE, s, p, (int)nt);
+  constexpr GroupedForm f{8, 128};
+  const dim3 g((unsigned)grouped_workgroups(f, p.offsets, p.E, p.P, p.N));
+  hipLaunchKernelGGL(k_grouped_far<OP>, g, dim3(512), 8 * LDS_PER_WAVE, s, p, (int)grouped_col_tiles(f, p.N));
   return hipGetLastError();
 }
 
-// Rules, with times in us on one MI355X of bf16 matrices of 2048 x 4096.
-// Few rows an expert: tiles as high as those, so that its weights are read
-// once.  64 rows each: of 256 experts eight waves 782 at a height of 128 and
-// 920 at 64 (four waves 822), of 8 experts four waves 28 at 64, 43 at 128, 30
-// with the choice (eight 39); 128 rows each of 8 experts 45 at 64, 48 at 128.
-// Many rows: 2048 each of 8 experts 248 by eight waves with the choice and 256
-// by four, 1024 each 154 and 152, 256 each 60 and 56.
 template <class OP>
 hipError_t choose(const Grouped &p, hipStream_t s) {
-  const int64_t mean = p.offsets ? p.P / p.E : p.P;  // rows of an expert
-  if (p.P * p.N >= (1 << 25)) return mean <= 128 ? tiled<OP, false, 8, 128>(p, s) : tiled<OP, false, 8, 0>(p, s);
-  return mean <= 64 ? tiled<OP, false, 4, 64>(p, s) : tiled<OP, false, 4, 0>(p, s);
+  const GroupedForm f = grouped_form(p.offsets, p.E, p.P, p.N);
+  if (f.waves == 8) return f.height ? tiled<OP, false, 8, 128>(p, s) : tiled<OP, false, 8, 0>(p, s);
+  return f.height ? tiled<OP, false, 4, 64>(p, s) : tiled<OP, false, 4, 0>(p, s);
 }
-// Turned weights, fp32 results: of 256 experts 64 rows each eight waves 857 and
-// four 943, 16 rows each 774 and 830, of 60 experts (488 x 1000) 62 rows each
-// 21.7 and 19.7; of 8 experts 1024 rows each eight waves with the choice 149 to
-// 165 and four 149, 2048 rows each 290 and 271.
 template <class OP>
 hipError_t choose_turned(const Grouped &p, hipStream_t s) {
-  const int64_t mean = p.P / p.E;
-  if (mean <= 128 && p.E * ((p.N + 255) / 256) >= 1024) return tiled<OP, true, 8, 128>(p, s);
-  return mean <= 64 ? tiled<OP, true, 4, 64>(p, s) : tiled<OP, true, 4, 0>(p, s);
+  const GroupedForm f = grouped_turned_form(p.E, p.P, p.N);
+  if (f.waves == 8) return tiled<OP, true, 8, 128>(p, s);
+  return f.height ? tiled<OP, true, 4, 64>(p, s) : tiled<OP, true, 4, 0>(p, s);
 }
 
 }  // namespace
 
 hipError_t launch_grouped(const Grouped &p, hipStream_t s) {
   if (p.turned) return p.type == DS4MOE_BF16 ? choose_turned<OpBf16>(p, s) : choose_turned<OpF16>(p, s);
-  if (p.offsets ? p.P <= 2 * p.E : p.P <= 64) return launch_grouped_few(p, s);
+  if (grouped_is_few(p.offsets, p.E, p.P)) return launch_grouped_few(p, s);
   if (p.perm && p.T * p.ldx > kRange)  // rows that 32-bit offsets do not reach
     return p.type == DS4MOE_BF16 ? tiled_far<OpBf16>(p, s) : p.type == DS4MOE_F16 ? tiled_far<OpF16>(p, s) : tiled_far<OpI8>(p, s);
   if (p.type == DS4MOE_BF16) return choose<OpBf16>(p, s);

@@ -2,6 +2,7 @@
 #pragma once
 #include "../../include/ds4moe.h"
 #include "grouped.h"
+#include "grouped_plan.h"
 #include "mx4_dev.h"
 
 namespace ds4 {
@@ -190,7 +191,8 @@ struct Finder {
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int cost = ((n[i] * ntiles + (1 << LOG) - 1) >> LOG) * (heights[i] + 80);  // less than 2^31: at most 2^22 tiles
+      // within 32 bits: 2^22 tiles or a few more, 2^8 times as many of offsets that do not ascend
+      const int cost = ((n[i] * ntiles + (1 << LOG) - 1) >> LOG) * (heights[i] + 80);
       if (cost < best) {
         best = cost;
         of = heights[i];
@@ -226,10 +228,6 @@ struct Finder {
     return Segment{__builtin_amdgcn_readlane(e, from), __builtin_amdgcn_readlane(p0, from), __builtin_amdgcn_readlane(n, from)};
   }
 };
-// what a grid has room for: the most tiles of `height` rows or more that E segments of P rows can make
-inline int64_t grouped_max_tiles(const int32_t *offsets, int64_t E, int64_t P, int64_t height) {
-  return offsets ? P / height + (P < E + 2 ? P : E + 2) : (P + height - 1) / height;
-}
 
 // The workgroup's row tile and column tile.  Consecutive workgroups go to
 // different XCDs, each of which takes a contiguous part of the work; GM row

@@ -92,7 +92,7 @@ __global__ __launch_bounds__(64 * SW, 4) void k_grouped_few(Grouped p) {
 
 template <class OP, int MT>
 hipError_t few(const Grouped &p, hipStream_t s) {
-  const dim3 g((unsigned)((p.N + 15) / 16), (unsigned)grouped_max_tiles(p.offsets, p.E, p.P, 16 * MT));
+  const dim3 g((unsigned)((p.N + 15) / 16), (unsigned)grouped_max_tiles(p.offsets != nullptr, p.E, p.P, 16 * MT));
   hipLaunchKernelGGL((k_grouped_few<OP, MT>), g, dim3(64 * SW), 0, s, p);
   return hipGetLastError();
 }

@@ -212,8 +212,9 @@ __global__ __launch_bounds__(128 * WN, 2) void k_grouped_dw(GroupedDw p, int mti
 
 template <class OP, int WN, int MT, int NB, bool FAR>
 hipError_t dw(const GroupedDw &p, hipStream_t s) {
+  static_assert(32 * MT == 64 * WN, "square tiles");
   const int64_t mt = (p.N + 32 * MT - 1) / (32 * MT), nt = (p.K + 64 * WN - 1) / (64 * WN);
-  const dim3 g((unsigned)((p.E * mt * nt + 7) / 8 * 8)), b(128 * WN);
+  const dim3 g((unsigned)grouped_dw_workgroups(WN == 4, p.E, p.N, p.K)), b(128 * WN);
   if (p.perm) hipLaunchKernelGGL((k_grouped_dw<OP, WN, MT, NB, true, FAR>), g, b, 0, s, p, (int)mt, (int)nt);
   else hipLaunchKernelGGL((k_grouped_dw<OP, WN, MT, NB, false, FAR>), g, b, 0, s, p, (int)mt, (int)nt);
   return hipGetLastError();
@@ -223,9 +224,7 @@ hipError_t choose_dw(const GroupedDw &p, hipStream_t s) {
   // offsets of an expert's rows, up to 31 past the last in the last stage, and of those that the permutation names
   const int64_t end = (int64_t)p.P + 31;
   if (end * p.lddy > kRange || (p.perm ? p.T : end) * p.ldx > kRange) return dw<OP, 2, 4, 2, true>(p, s);
-  // Tiles of 256 x 256 (one workgroup on a CU) or 128 x 128 (three): 32768 of the large ones, 64 terms each, 1170 us and
-  // 1288; 1024, 1024 terms each, 155 and 158; 480, 62 terms each, 44 and 38; 128, 4096 terms each, 115 and 73.
-  return p.E * ((p.N + 255) / 256) * ((p.K + 255) / 256) >= 1024 ? dw<OP, 4, 8, 4, false>(p, s) : dw<OP, 2, 4, 2, false>(p, s);
+  return grouped_dw_large(p.E, p.N, p.K) ? dw<OP, 4, 8, 4, false>(p, s) : dw<OP, 2, 4, 2, false>(p, s);
 }
 
 // ---------------------------------------------------------------- gradients of shared rows
