@@ -48,13 +48,14 @@ int validate_grad(const ds4moe_grouped_dims *d) {
 inline bool row_step(int64_t ld, int64_t cols, int32_t dtype) { return ld >= cols && ld <= kMaxRow && ld * elem(dtype) % 16 == 0; }
 
 struct DxLayout {
-  size_t rows, places, total;
+  size_t rows, next, places, total;
 };
 DxLayout dx_layout(const ds4moe_grouped_dims &d) {
   DxLayout L{};
   L.rows = 0;
-  L.places = align256(4 * (size_t)d.rows * (size_t)d.K);
-  L.total = L.places + align256(4 * (size_t)d.tokens * (size_t)d.top_k);
+  L.next = align256(4 * (size_t)d.rows * (size_t)d.K);
+  L.places = L.next + align256(4 * (size_t)d.rows);
+  L.total = L.places + align256(4 * ((size_t)d.tokens * (size_t)d.top_k + 2));
   return L;
 }
 
@@ -122,7 +123,8 @@ int ds4moe_grouped_dx(const ds4moe_grouped_dims *dims, void *dx, int64_t lddx, c
   }
   const hipStream_t s = (hipStream_t)stream;
   float *const rows = reinterpret_cast<float *>((char *)ws + L.rows);
-  int32_t *const places = reinterpret_cast<int32_t *>((char *)ws + L.places);
+  const GroupedPlaces places{reinterpret_cast<int32_t *>((char *)ws + L.places), reinterpret_cast<int32_t *>((char *)ws + L.next),
+                             (int32_t)(d.tokens * d.top_k)};
   Grouped p{};
   p.y = perm ? rows : dx;
   p.ldy = perm ? d.K : lddx;
@@ -138,12 +140,12 @@ int ds4moe_grouped_dx(const ds4moe_grouped_dims *dims, void *dx, int64_t lddx, c
   p.P = p.T = (int32_t)d.rows;
   p.N = d.K;
   p.Kb = d.N * elem(d.dtype);
-  p.places = perm ? places : nullptr;
-  p.n_places = perm ? (int32_t)(d.tokens * d.top_k) : 0;
+  p.places = perm ? places.first : nullptr;
+  p.n_places = perm ? places.A + 2 : 0;
   hipError_t e = hipSuccess;
   if (d.rows) e = launch_grouped(p, s);
   if (e != hipSuccess || !perm) return hip_status(e);
-  e = launch_grouped_places(places, perm, (int32_t)d.rows, (int32_t)(d.tokens * d.top_k), d.rows == 0, s);
+  e = launch_grouped_places(places, offsets, d.n_experts, perm, (int32_t)d.rows, s);
   if (e != hipSuccess) return hip_status(e);
   return hip_status(launch_grouped_add_up(dx, lddx, d.y_dtype, rows, places, (int32_t)d.tokens, d.top_k, d.K, s));
 }

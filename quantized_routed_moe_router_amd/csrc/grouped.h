@@ -47,10 +47,16 @@ struct GroupedDw {
 };
 hipError_t launch_grouped_dw(const GroupedDw &p, hipStream_t s);
 
-// dx[t] = sum over j of rows[places[t k + j]], in the order of j, where that is not -1; places[perm[p]] = p, to be -1
-// before (`clear`: they are made so here)
-hipError_t launch_grouped_places(int32_t *places, const int32_t *perm, int32_t P, int32_t A, bool clear, hipStream_t s);
-hipError_t launch_grouped_add_up(void *dx, int64_t ldo, int32_t o_type, const float *rows, const int32_t *places,
+// Where the assignments of tokens stand: the first position of each, and what follows it where it stands again
+struct GroupedPlaces {
+  int32_t *first;  // [A + 2], of which the last two are the kernel's own; -1 before
+  int32_t *next;   // [P]
+  int32_t A;
+};
+// the places of the positions that have an expert (P = 0: of none, and nothing has to be -1 before)
+hipError_t launch_grouped_places(const GroupedPlaces &p, const int32_t *offsets, int32_t E, const int32_t *perm, int32_t P, hipStream_t s);
+// dx[t] = sum over j of the rows of assignment t k + j: the first of each in the order of j, then of each what follows
+hipError_t launch_grouped_add_up(void *dx, int64_t ldo, int32_t o_type, const float *rows, const GroupedPlaces &p,
                                  int32_t T, int32_t k, int64_t K, hipStream_t s);
 
 // ---------------------------------------------------------------- 8-bit integers

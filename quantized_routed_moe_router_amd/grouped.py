@@ -164,7 +164,7 @@ def grouped_matmul_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, 
                             dw_dtype: torch.dtype | None = None) -> tuple:
     """(dx [T,K] in x's type, dw [E,N,K] in w's or dw_dtype) from dy [P,N], the gradient of grouped_matmul(x, w, offsets,
     perm, k); None in the place of one that is not asked for.  x, w and dy in bf16 or fp16, N a multiple of 8.  A value
-    of perm that stands twice counts with its last position in dx."""
+    of perm may stand several times (tokens' numbers with k = 1, say): every position of an expert adds to dx."""
     ldy, ldx = _rows(dy, "dy", _HALF), _rows(x, "x", _HALF)
     T = x.shape[0]
     E, N, K, P, i, at = _groups(w, offsets, perm, k, T, (x.dtype,))

@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_grouped import _q, dev, host
+import grouped_ref as R
+from test_gpu_grouped import _q, case, check, dev, half, host
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,101 @@ def test_rows_gradients_of_2_to_the_36_values():
         assert torch.equal(part, dy.float() @ wt[0, :, c:c + 128].float().sum(1))
     del dx
     torch.cuda.empty_cache()
+
+
+def routed(T, E, P, k, style, rng):
+    """Entries of a permutation that stand several times, and offsets."""
+    if style == "tokens":  # the numbers of tokens, each with several experts: k = 1
+        flat = rng.integers(0, E, P)
+        offsets = np.concatenate([[0], np.cumsum(np.bincount(flat, minlength=E))])
+        perm = np.sort(rng.integers(0, T, P))[np.argsort(flat, kind="stable")]
+    elif style == "one":  # all positions of one assignment
+        offsets = np.sort(np.concatenate([[0, P], rng.integers(0, P + 1, E - 1)]))
+        perm = np.full(P, T * k // 2)
+    elif style == "some":  # distinct ones but for a few, and some that name nothing
+        offsets = np.sort(np.concatenate([[0, P], rng.integers(0, P + 1, E - 1)]))
+        perm = rng.permutation(T * k)[:P]
+        perm[rng.integers(0, P, 3)] = perm[rng.integers(0, P, 3)]
+        perm[rng.integers(0, P, 2)] = [-1, T * k]
+    else:  # "padded": positions of no expert at both ends, all of which name assignment 0
+        a, b = P // 7, P - P // 5
+        offsets = np.sort(np.concatenate([[a, b], rng.integers(a, b + 1, E - 1)]))
+        perm = np.concatenate([np.zeros(a, int), rng.permutation(T * k)[:b - a], np.zeros(P - b, int)])
+        perm[a + (b - a) // 2] = 0
+    return offsets.astype(np.int32), perm.astype(np.int32)
+
+
+@pytest.mark.parametrize("T,E,P,k,style", [
+    (5, 3, 9, 1, "tokens"), (300, 8, 600, 1, "tokens"), (4000, 8, 8000, 1, "tokens"), (1000, 60, 3711, 1, "tokens"), (64, 4, 1023, 1, "tokens"),
+    (64, 4, 1024, 1, "tokens"), (64, 4, 1025, 2, "tokens"), (3, 4, 2049, 1, "one"), (7, 2, 5000, 3, "one"), (1, 6, 6, 1, "one"), (700, 5, 1300, 2, "some"),
+    (3000, 5, 9000, 3, "some"), (20, 2, 30, 2, "padded"), (900, 6, 1800, 2, "padded"), (5000, 6, 9001, 2, "padded")])
+def test_rows_gradient_of_assignments_that_stand_several_times(T, E, P, k, style):
+    """Every position of an expert adds to its token's gradient, in an order that is the same every time; those of no expert
+    add nothing and take nothing away."""
+    q = _q()
+    N, K = 24, 40
+    x, xv, w, wv, _, _ = case(T, E, 1, N, K, "f16")
+    rng = np.random.default_rng(P + T)
+    offsets, perm = routed(T, E, P, k, style, rng)
+    inside = np.zeros(P, dtype=bool)
+    inside[offsets[0]:offsets[-1]] = True
+    rows = np.where(inside, R.rows_of(perm, k, T, P), -1)
+    assert np.unique(perm[rows >= 0]).size < (rows >= 0).sum() or style == "padded"
+    dy, dyv = half(0.1 * rng.standard_normal((P, N)), "f16")
+    wx, ww, mx, mw = R.backward(dyv, xv, wv, offsets, rows)
+    most = int(np.bincount(rows[rows >= 0], minlength=T).max())
+    o, p = dev(offsets), dev(perm)
+    dx, dw = q.grouped_matmul_backward(dy, x, w, o, p, k)
+    check(dx, wx, mx, N + most, "f16")
+    check(dw, ww, mw, P, "f16")
+    for _ in range(3):
+        assert torch.equal(q.grouped_matmul_backward(dy, x, w, o, p, k, need_dw=False)[0], dx)
+
+
+def test_rows_gradient_by_tokens_numbers_is_that_of_the_gates_permutation():
+    """Top-2 routing by the gate's permutation with k = 2, and by tokens' numbers with k = 1: sums of two, which have no order."""
+    q = _q()
+    T, E, k, N, K = 500, 8, 2, 64, 136
+    x, _, w, _, offsets, perm = case(T, E, k, N, K, "bf16")
+    dy = half(np.random.default_rng(1).standard_normal((T * k, N)), "bf16")[0]
+    a = q.grouped_matmul_backward(dy, x, w, dev(offsets), dev(perm), k)
+    b = q.grouped_matmul_backward(dy, x, w, dev(offsets), dev(perm // k), 1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_rows_gradient_in_a_graph_whose_assignments_change():
+    """One captured call, replayed on permutations whose assignments are distinct and on others, in turn."""
+    q = _q()
+    T, E, k, N, K = 400, 4, 2, 40, 72
+    x, _, w, _, offsets, perm = case(T, E, k, N, K, "bf16")
+    dy = half(np.random.default_rng(1).standard_normal((T * k, N)), "bf16")[0]
+    o, p = dev(offsets), dev(perm)
+    q.grouped_matmul_backward(dy, x, w, o, p, k, need_dw=False)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dx, _ = q.grouped_matmul_backward(dy, x, w, o, p, k, need_dw=False)
+    for i in range(6):
+        rng = np.random.default_rng(i)
+        p.copy_(dev(perm if i % 2 else rng.integers(-2, T * k + 2, T * k).astype(np.int32)))
+        g.replay()
+        torch.cuda.synchronize()
+        got = dx.clone()
+        assert torch.equal(got, q.grouped_matmul_backward(dy, x, w, o, p, k, need_dw=False)[0]), i
+
+
+def test_rows_gradient_of_repeated_assignments_is_the_difference():
+    """Central differences of sum(dy * y) along random directions of x, an assignment standing three times."""
+    q = _q()
+    T, N, K = 4, 16, 32
+    x, xv, w, wv, _, _ = case(T, 2, 1, N, K, "f16")
+    perm, offsets = np.array([1, 1, 3, 1], dtype=np.int32), np.array([0, 2, 4], dtype=np.int32)
+    rows = R.rows_of(perm, 1, T, 4)
+    dy, dyv = half(np.random.default_rng(1).standard_normal((4, N)), "f16")
+    dx, _ = q.grouped_matmul_backward(dy, x, w, dev(offsets), dev(perm), need_dw=False)
+    _, _, mx, _ = R.backward(dyv, xv, wv, offsets, rows)
+    rng, h = np.random.default_rng(2), 2.0**-10
+    for _ in range(4):
+        u = rng.standard_normal(xv.shape)
+        up, down = (R.matmul(xv + s * h * u, wv, offsets, rows)[0] for s in (1, -1))
+        want = ((up - down) * dyv).sum() / (2 * h)  # linear in x: exact but for 64-bit roundings
+        assert abs((host(dx) * u).sum() - want) <= (np.abs(u) * (mx * (2.0**-23 * (N + 5) + 2.0**-11) + R.TINY["f16"])).sum()
