@@ -614,7 +614,8 @@ int ds4moe_int8_matmul(void *y, int32_t y_dtype, int64_t ldy, const void *a, con
  * last belong to no expert: their rows of y are zeros, and they add nothing to
  * a gradient.  Offsets that do not ascend give unspecified values; nothing
  * outside the arrays is read or written whatever they are.  A perm[p] outside
- * 0..T*top_k-1 stands for a row of zeros, which gets no gradient. */
+ * 0..T*top_k-1 stands for a row of zeros, which gets no gradient, and its dy[p],
+ * whatever it holds, adds nothing to dW. */
 typedef struct {
   int32_t dtype;
   int32_t y_dtype;

@@ -26,8 +26,8 @@ __global__ __launch_bounds__(128 * WN, 2) void k_grouped_dw(GroupedDw p, int mti
   constexpr int CA = BM / 8, CB = BN / 8;                        // chunks of a staged row
   constexpr int DA = CA / 2 / WAVES, DB = CB / 2 / WAVES, D = DA + DB;  // loads per wave
   constexpr int BOFF = BM * 64, STAGE = BOFF + BN * 64;
-  static_assert(DA * WAVES * 2 == CA && DB * WAVES * 2 == CB && MT % 4 == 0 && CA >= 16 && CB >= 16 && NB % 2 == 0,
-                "whole loads, places of chunks stay in the row");
+  static_assert(DA * WAVES * 2 == CA && CA == CB && MT % 4 == 0 && CA >= 16 && NB % 2 == 0,
+                "whole loads, places of chunks stay in the row, load q has the same rows of both operands");
   __shared__ __attribute__((aligned(16))) char lds[NB * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
   const int wm = wave / WN, wn = wave % WN;
@@ -68,21 +68,25 @@ __global__ __launch_bounds__(128 * WN, 2) void k_grouped_dw(GroupedDw p, int mti
 #pragma unroll
     for (int q = 0; q < DB; ++q) to[q] = p.perm[p0 + min(st * 32 + row_b(q), n - 1)];
   };
+  // A position that names no row has zeros of dy too: what stands there, a NaN
+  // or an infinity, adds nothing.
   int at_x[DB];
+  uint32_t named_a[DA];
   auto prepare = [&](int st, const int (&from)[DB]) {
 #pragma unroll
     for (int q = 0; q < DB; ++q) {
       const int at = row_named(p.k_inv, p.T, from[q]);
       at_x[q] = st * 32 + row_b(q) < n ? at : -1;
       sb[q] = at_x[q] >= 0 ? at * ldx + col_b(q) : kNowhere;
+      named_a[q] = at_x[q] >= 0 ? sa[q] : kNowhere;
     }
   };
   auto load = [&](int st, char *to) {
 #pragma unroll
     for (int q = 0; q < DA; ++q) {
       char *const d = to + (q * WAVES + wave) * 1024;
-      if (FAR) load_lds16(st * 32 + row_a(q) < n && m0 * 2 + col_a(q) < p.N * 2 ? dy + (int64_t)(st * 32 + row_a(q)) * p.lddy + col_a(q) : (const char *)kZeros, d);
-      else load_stage16(ry, d, sa[q], st * 32 * lddy);
+      if (FAR) load_lds16((PERM ? at_x[q] >= 0 : st * 32 + row_a(q) < n) && m0 * 2 + col_a(q) < p.N * 2 ? dy + (int64_t)(st * 32 + row_a(q)) * p.lddy + col_a(q) : (const char *)kZeros, d);
+      else load_stage16(ry, d, PERM ? named_a[q] : sa[q], st * 32 * lddy);
     }
 #pragma unroll
     for (int q = 0; q < DB; ++q) {

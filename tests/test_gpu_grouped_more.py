@@ -129,3 +129,45 @@ def test_rows_gradient_of_repeated_assignments_is_the_difference():
         up, down = (R.matmul(xv + s * h * u, wv, offsets, rows)[0] for s in (1, -1))
         want = ((up - down) * dyv).sum() / (2 * h)  # linear in x: exact but for 64-bit roundings
         assert abs((host(dx) * u).sum() - want) <= (np.abs(u) * (mx * (2.0**-23 * (N + 5) + 2.0**-11) + R.TINY["f16"])).sum()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("E,N,K,P", [(3, 40, 72, 5), (3, 136, 200, 700), (4, 24, 40, 3000), (512, 264, 264, 20000)])
+def test_weights_gradient_of_positions_that_name_nothing(kind, E, N, K, P):
+    """NaN and infinities of dy where the permutation names no row: padding, which adds nothing."""
+    q = _q()
+    T, rng = P, np.random.default_rng(P)
+    x, _ = half(rng.standard_normal((T, K)), kind)
+    w = torch.zeros(E, N, K, dtype=x.dtype, device="cuda")
+    offsets = np.sort(np.concatenate([[0, P], rng.integers(0, P + 1, E - 1)])).astype(np.int32)
+    perm = rng.permutation(P).astype(np.int32)
+    gone = rng.random(P) < 0.2
+    gone[[0, P - 1]] = True
+    perm[gone] = rng.choice([-1, T, 2**31 - 1, -2**31], gone.sum())
+    dv = 0.1 * rng.standard_normal((P, N))
+    dy, _ = half(np.where(gone[:, None], 0, dv), kind)
+    bad, _ = half(np.where(gone[:, None], rng.choice([np.nan, np.inf, -np.inf], (P, N)), dv), kind)
+    want = q.grouped_matmul_backward(dy, x, w, dev(offsets), dev(perm))
+    got = q.grouped_matmul_backward(bad, x, w, dev(offsets), dev(perm))
+    assert torch.isfinite(want[1]).all() and torch.equal(got[1], want[1]) and torch.equal(got[0], want[0])
+
+
+@pytest.mark.parametrize("step", [8372128 // 2, 8388608 // 2])
+def test_weights_gradient_of_unnamed_positions_far_apart(step):
+    """Rows of dy up to 2^32 bytes from the first, and beyond: NaN in those that name nothing, the last among them."""
+    q = _q()
+    P, N, K = 513, 72, 64
+    rng = np.random.default_rng(0)
+    ds = torch.full((P * step,), float("nan"), dtype=torch.bfloat16, device="cuda").view(P, step)
+    xv, dv = rng.integers(-8, 9, (P, K)) / 4.0, rng.integers(-8, 9, (P, N)) / 4.0
+    perm = rng.permutation(P).astype(np.int32)
+    gone = rng.random(P) < 0.3
+    gone[[0, P - 2, P - 1]] = True
+    perm[gone] = -1
+    at = torch.from_numpy(np.nonzero(~gone)[0]).cuda()
+    ds[at, :N] = torch.from_numpy(dv[~gone]).to(torch.bfloat16).cuda()
+    w = torch.zeros(1, N, K, dtype=torch.bfloat16, device="cuda")
+    offsets = torch.tensor([0, P], dtype=torch.int32, device="cuda")
+    _, dw = q.grouped_matmul_backward(ds[:, :N], torch.from_numpy(xv).to(torch.bfloat16).cuda(), w, offsets, dev(perm), need_dx=False,
+                                      dw_dtype=torch.float32)
+    assert np.array_equal(host(dw)[0], dv[~gone].T @ xv[perm[~gone]])  # sixteenths below 2^24 of them
