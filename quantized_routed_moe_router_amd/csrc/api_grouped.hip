@@ -101,7 +101,8 @@ int ds4moe_grouped_matmul(const ds4moe_grouped_dims *dims, void *y, int64_t ldy,
 
 size_t ds4moe_grouped_workspace_bytes(const ds4moe_grouped_dims *dims) {
   if (validate_grad(dims) != DS4MOE_OK) return 0;
-  return dims->rows == 0 ? 256 : dx_layout(*dims).total;
+  const size_t n = dx_layout(*dims).total;
+  return n > 256 ? n : 256;
 }
 
 int ds4moe_grouped_dx(const ds4moe_grouped_dims *dims, void *dx, int64_t lddx, const void *dy, int64_t lddy, const void *w,

@@ -171,3 +171,17 @@ def test_weights_gradient_of_unnamed_positions_far_apart(step):
     _, dw = q.grouped_matmul_backward(ds[:, :N], torch.from_numpy(xv).to(torch.bfloat16).cuda(), w, offsets, dev(perm), need_dx=False,
                                       dw_dtype=torch.float32)
     assert np.array_equal(host(dw)[0], dv[~gone].T @ xv[perm[~gone]])  # sixteenths below 2^24 of them
+
+
+@pytest.mark.parametrize("T,k", [(1, 1), (1000, 2)])
+def test_tokens_without_positions_of_the_c_abi(T, k):
+    """With exactly the workspace that the library asks for: zeros."""
+    B = _q().binding
+    K, N = 72, 40
+    d = B.make_grouped_dims(N, K, 3, k, 0, T)
+    n = B.ds4moe_grouped_workspace_bytes(d)
+    ws, dx = torch.full((n,), 77, dtype=torch.uint8, device="cuda"), torch.full((T, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    w, some = torch.ones(3, N, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    B.ds4moe_grouped_dx(d, dx, K, None, N, w, some, some, ws, n)
+    torch.cuda.synchronize()
+    assert not dx.any()
