@@ -3,8 +3,9 @@
 Plumbing around the C ABI only, as for the 4-bit operators: shapes, types and devices are checked here, torch allocates
 outputs and workspaces (on the current stream), and every step runs in libds4moe.so, on the device of the call's tensors
 and its current stream.
-Nothing here is recorded by autograd: a tensor that requires a gradient is refused while gradients are on, and
-grouped_matmul_backward is the gradient that there is.
+Nothing here is recorded by autograd: a tensor that requires a gradient, the fp32 scales of 8-bit integers too, is
+refused while gradients are on.  grouped_matmul_backward is the gradient that there is; it takes operands that require
+one, and its results carry none.
 A matrix of 8-bit integers is a pair: int8 codes [rows, K16], K16 the columns rounded up to a multiple of 16, and fp32
 scales [rows].
 """
@@ -61,6 +62,8 @@ def int8_quantize(x: torch.Tensor) -> tuple:
 def int8_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int | None = None,
                     dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """The values of a matrix of 8-bit integers, the first `cols` of each row (all by default)."""
+    if scales.requires_grad:
+        _tracked("scales", "")
     i, kind = codes.get_device(), _real(dtype, "dtype")
     _flat(codes, "codes", torch.int8)
     if codes.dim() != 2 or codes.shape[1] % 16:
@@ -80,8 +83,8 @@ def int8_matmul(a: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, a_scal
                 y_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """a [M,K] times w [N,K16]^T times both scales: w in 8-bit integers, a too (with a_scales), or in fp32, bf16 or fp16,
     which the call quantises row by row."""
-    if a.requires_grad:
-        _tracked("a", "")
+    if a.requires_grad or w_scales.requires_grad or (a_scales is not None and a_scales.requires_grad):
+        _tracked("a or a scale", "")
     kind, i = _real(y_dtype, "y_dtype"), w.get_device()
     _flat(w, "w", torch.int8)
     if w.dim() != 2 or w.shape[1] % 16:
@@ -141,6 +144,8 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, perm
     if x.dtype is torch.int8:
         if x_scales is None or w_scales is None:
             raise ValueError("8-bit integers want x_scales and w_scales")
+        if x_scales.requires_grad or w_scales.requires_grad:
+            _tracked("x_scales or w_scales", "")
         sx = _flat(x_scales, "x_scales", torch.float32, (T,), i).data_ptr()
         sw = _flat(w_scales, "w_scales", torch.float32, (E, N), i).data_ptr()
         y_dtype = torch.bfloat16 if y_dtype is None else y_dtype
