@@ -641,8 +641,8 @@ size_t ds4moe_grouped_workspace_bytes(const ds4moe_grouped_dims *dims);
 /* dx [T, K], lddx elements apart, every row of which is written.  dy: [P, N],
  * lddy elements apart.  Without perm P = T and no workspace is needed.  With
  * it an assignment (a value of perm) may be absent, and adds nothing, and may
- * stand several times: every position of an expert adds its share, the first
- * ones in the order of the ranks, then the others in that of the positions. */
+ * stand several times: every position of an expert adds its share, in the order
+ * of the ranks and of the positions of each. */
 int ds4moe_grouped_dx(const ds4moe_grouped_dims *dims, void *dx, int64_t lddx, const void *dy, int64_t lddy, const void *w,
                       const int32_t *offsets, const int32_t *perm, void *ws, size_t ws_bytes, void *stream);
 

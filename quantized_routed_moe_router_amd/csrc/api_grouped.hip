@@ -55,7 +55,7 @@ DxLayout dx_layout(const ds4moe_grouped_dims &d) {
   L.rows = 0;
   L.next = align256(4 * (size_t)d.rows * (size_t)d.K);
   L.places = L.next + align256(4 * (size_t)d.rows);
-  L.total = L.places + align256(4 * ((size_t)d.tokens * (size_t)d.top_k + 2));
+  L.total = L.places + align256(4 * (size_t)d.tokens * (size_t)d.top_k);
   return L;
 }
 
@@ -125,7 +125,7 @@ int ds4moe_grouped_dx(const ds4moe_grouped_dims *dims, void *dx, int64_t lddx, c
   const hipStream_t s = (hipStream_t)stream;
   float *const rows = reinterpret_cast<float *>((char *)ws + L.rows);
   const GroupedPlaces places{reinterpret_cast<int32_t *>((char *)ws + L.places), reinterpret_cast<int32_t *>((char *)ws + L.next),
-                             (int32_t)(d.tokens * d.top_k)};
+                             perm, offsets, d.n_experts, (int32_t)d.rows, (int32_t)(d.tokens * d.top_k)};
   Grouped p{};
   p.y = perm ? rows : dx;
   p.ldy = perm ? d.K : lddx;
@@ -141,12 +141,12 @@ int ds4moe_grouped_dx(const ds4moe_grouped_dims *dims, void *dx, int64_t lddx, c
   p.P = p.T = (int32_t)d.rows;
   p.N = d.K;
   p.Kb = d.N * elem(d.dtype);
-  p.places = perm ? places.first : nullptr;
-  p.n_places = perm ? places.A + 2 : 0;
+  p.places = perm ? places.place : nullptr;
+  p.n_places = perm ? places.A : 0;
   hipError_t e = hipSuccess;
   if (d.rows) e = launch_grouped(p, s);
   if (e != hipSuccess || !perm) return hip_status(e);
-  e = launch_grouped_places(places, offsets, d.n_experts, perm, (int32_t)d.rows, s);
+  e = launch_grouped_places(places, s);
   if (e != hipSuccess) return hip_status(e);
   return hip_status(launch_grouped_add_up(dx, lddx, d.y_dtype, rows, places, (int32_t)d.tokens, d.top_k, d.K, s));
 }

@@ -47,16 +47,17 @@ struct GroupedDw {
 };
 hipError_t launch_grouped_dw(const GroupedDw &p, hipStream_t s);
 
-// Where the assignments of tokens stand: the first position of each, and what follows it where it stands again
+// Where the assignments of tokens stand: a list of the positions of each, those that have an expert
 struct GroupedPlaces {
-  int32_t *first;  // [A + 2], of which the last two are the kernel's own; -1 before
-  int32_t *next;   // [P]
-  int32_t A;
+  int32_t *place;  // [A]: the first of the list, marked where there are more; -1 before and where there is none
+  int32_t *next;   // [P]: what follows in the list, or -1
+  const int32_t *perm, *offsets;
+  int32_t E, P, A;
 };
-// the places of the positions that have an expert (P = 0: of none, and nothing has to be -1 before)
-hipError_t launch_grouped_places(const GroupedPlaces &p, const int32_t *offsets, int32_t E, const int32_t *perm, int32_t P, hipStream_t s);
-// dx[t] = sum over j of the rows of assignment t k + j: the first of each in the order of j, then of each what follows
-hipError_t launch_grouped_add_up(void *dx, int64_t ldo, int32_t o_type, const float *rows, const GroupedPlaces &p,
+// the lists (P = 0: none, and nothing has to be -1 before)
+hipError_t launch_grouped_places(const GroupedPlaces &q, hipStream_t s);
+// dx[t] = sum over j of the rows of assignment t k + j, in the order of j and of the positions
+hipError_t launch_grouped_add_up(void *dx, int64_t ldo, int32_t o_type, const float *rows, const GroupedPlaces &q,
                                  int32_t T, int32_t k, int64_t K, hipStream_t s);
 
 // ---------------------------------------------------------------- 8-bit integers

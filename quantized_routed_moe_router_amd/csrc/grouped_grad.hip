@@ -236,122 +236,99 @@ __global__ __launch_bounds__(256) void k_grouped_no_places(int32_t *places, int 
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i < A) places[i] = -1;
 }
-// A place is the first position of an assignment (-1: none), with kMore where
-// the assignment stands again: next[position] is the place that follows.
+
+// The positions that have an expert.
+__device__ __forceinline__ int begin_of(const GroupedPlaces &q) { return min(max(q.offsets[0], 0), q.P); }
+__device__ __forceinline__ int end_of(const GroupedPlaces &q) { return max(begin_of(q), min(max(q.offsets[q.E], 0), q.P)); }
+
+// An assignment's place is one of its positions (-1: none); next[position] is
+// another, and so on: a list in no particular order, which nearly always has
+// one.  kMore in the place says that it has more: whoever comes to a place that
+// is taken sets it behind its own entry.  Positions without an expert are in
+// none.
 constexpr int kMore = 1 << 30;  // positions are below 2^23
-constexpr int CHUNK = 1024;     // positions that are sorted at a time
-
-// Assignments that stand more than once, by one workgroup: each one's positions
-// in ascending order, so that the sum's order is that of the positions and the
-// same every time.  From the last CHUNK of positions to the first: sorted by
-// assignment and position, each is followed by its neighbour or by what the
-// chunks behind have left in `places`.  A chunk takes 5 us or so whatever is in
-// it, and calls whose assignments are distinct do not come here.
-__device__ void link_positions(int32_t *places, int32_t *next, const int32_t *perm, int first, int last, int A) {
-  constexpr uint64_t none = ~0ull;
-  __shared__ uint64_t key[CHUNK];
-  const int tid = threadIdx.x;
-  for (int p = first + tid; p < last; p += 256) {
-    const int a = perm[p];
-    if (a >= 0 && a < A) places[a] = -1;
-  }
-  for (int end = last; end > first; end -= CHUNK) {
-    const int begin = max(first, end - CHUNK);
-    for (int i = tid; i < CHUNK; i += 256) {
-      const int a = begin + i < end ? perm[begin + i] : -1;
-      key[i] = a >= 0 && a < A ? (uint64_t)a << 32 | (uint32_t)(begin + i) : none;
-    }
-    for (int size = 2; size <= CHUNK; size *= 2)
-      for (int d = size / 2; d; d /= 2) {
-        __syncthreads();
-        for (int i = tid; i < CHUNK / 2; i += 256) {
-          const int lo = 2 * i - (i & (d - 1)), hi = lo + d;
-          const uint64_t u = key[lo], v = key[hi];
-          if ((u > v) == ((lo & size) == 0)) {
-            key[lo] = v;
-            key[hi] = u;
-          }
-        }
-      }
-    __syncthreads();  // also: the places that the chunk before, or the loop above, has written
-    int behind[CHUNK / 256];
-#pragma unroll
-    for (int j = 0; j < CHUNK / 256; ++j) {
-      const uint64_t u = key[j * 256 + tid];
-      behind[j] = u == none ? -1 : places[u >> 32];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < CHUNK / 256; ++j) {
-      const int i = j * 256 + tid;
-      const uint64_t u = key[i];
-      if (u == none) continue;
-      const uint32_t a = (uint32_t)(u >> 32);
-      auto same = [&](int at) { return at >= 0 && at < CHUNK && (uint32_t)(key[at] >> 32) == a; };
-      int follows = behind[j];
-      if (same(i + 1)) follows = (int)key[i + 1] | (same(i + 2) || behind[j] >= 0 ? kMore : 0);
-      next[(int)u] = follows;
-      if (!same(i - 1)) places[a] = (int)u | (follows >= 0 ? kMore : 0);
-    }
-    __syncthreads();
-  }
+__global__ __launch_bounds__(256) void k_grouped_places(GroupedPlaces q) {
+  const int i = blockIdx.x * 256 + threadIdx.x, a = i < q.P ? q.perm[i] : -1;
+  if (i < begin_of(q) || i >= end_of(q) || a < 0 || a >= q.A) return;
+  const int before = atomicExch(q.place + a, i);
+  q.next[i] = before < 0 ? -1 : before & (kMore - 1);
+  if (before >= 0) atomicOr(q.place + a, kMore);
 }
 
-// The workgroup that is done last sees whether an assignment stood twice; state:
-// workgroups done, and that flag, both from -1 on.  Where none does, nothing
-// but the flag has to be seen by it, and no other fence is paid for.
-__global__ __launch_bounds__(256) void k_grouped_places(int32_t *places, int32_t *next, int32_t *state, const int32_t *offsets, int E,
-                                                        const int32_t *perm, int P, int A) {
-  __shared__ int done, twice;
-  const int i = blockIdx.x * 256 + threadIdx.x, a = i < P ? perm[i] : -1;  // asked for together with the offsets
-  const int first = min(max(offsets[0], 0), P), last = max(first, min(max(offsets[E], 0), P));
-  if (i >= first && i < last && a >= 0 && a < A && atomicMin(reinterpret_cast<uint32_t *>(places) + a, (uint32_t)i) != ~0u) {
-    atomicMax(state + 1, 0);
-    __threadfence();
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    done = atomicAdd(state, 1);
-    twice = done == (int)gridDim.x - 2 ? atomicMax(state + 1, -1) : -1;
-  }
-  __syncthreads();
-  if (twice < 0) return;
-  __threadfence();
-  link_positions(places, next, perm, first, last, A);
-}
-
-// dx[t] = sum over j of the rows of its assignments, in fp32 with one rounding (the rows are fp32 so that there is one): the
-// first of each in the order of j, then of each in turn what follows, if any does.  Bound by the memory: two rows each of 4096 tokens, 4096 wide, 29 us (134 MB in, 34 out, 5.8 TB/s).
+// dx[t] = sum over j of the rows of its assignments, in the order of j and of
+// the positions of each, in fp32 with one rounding.  The rows are fp32 so that
+// there is one.  Bound by the memory: two rows each of 4096 tokens, 4096 wide,
+// 29 us (134 MB in, 34 out, 5.8 TB/s).
+//
+// Where an assignment stands several times, its list is put in order first.  Up
+// to LIST positions are sorted in LDS; an assignment of more is looked for in
+// the permutation from end to end, which has at most P / LIST of these.  Two
+// positions each of 65536 tokens, 512 wide, as tokens' numbers: the gradient of
+// the rows in 201 us, 190 by assignments that are distinct.
 template <int NV>
-__global__ __launch_bounds__(256) void k_grouped_add_up(void *dx, int64_t ldo, int o_type, const float *rows, const int32_t *places, const int32_t *next, int T,
-                                                        int k, int64_t K) {
-  const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * NV;
-  if (c >= K) return;
+__global__ __launch_bounds__(256) void k_grouped_add_up(void *dx, int64_t ldo, int o_type, const float *rows, GroupedPlaces q, int T, int k, int64_t K) {
+  constexpr int LIST = 256;
+  __shared__ int list[LIST], sorted[LIST], length;
+  __shared__ uint64_t found[4];
+  const int tid = threadIdx.x;
+  const int threads = blockDim.x;  // no more waves than columns give work to
+  const int64_t c = ((int64_t)blockIdx.y * threads + tid) * NV;
+  const bool in = c < K;
+  float v[NV];
+  auto add = [&](int at) {
+    if (!in) return;
+#pragma unroll
+    for (int i = 0; i < NV; i += 4) {
+      const f4 u = *reinterpret_cast<const f4 *>(rows + at * K + c + i);
+#pragma unroll
+      for (int l = 0; l < 4; ++l) v[i + l] += u[l];
+    }
+  };
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = 0.0f;
+  };
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    float v[NV] = {};
+    clear();
     int more = 0;
-    auto add = [&](int place) {
-#pragma unroll
-      for (int i = 0; i < NV; i += 4) {
-        const f4 u = *reinterpret_cast<const f4 *>(rows + (place & (kMore - 1)) * K + c + i);
-#pragma unroll
-        for (int l = 0; l < 4; ++l) v[i + l] += u[l];
-      }
-    };
     for (int j = 0; j < k; ++j) {
-      const int place = places[t * k + j];
-      if (place < 0) continue;
-      more |= place & kMore;
-      add(place);
+      const int at = q.place[t * k + j];
+      if (at < 0) continue;
+      more |= at & kMore;
+      add(at & (kMore - 1));
     }
     if (more) {
-      for (int j = 0; j < k; ++j)
-        for (int place = places[t * k + j]; place >= 0 && place & kMore;) {
-          place = next[place & (kMore - 1)];
-          add(place);
+      clear();
+      for (int j = 0; j < k; ++j) {
+        const int a = (int)(t * k + j), head = q.place[a];
+        if (head < 0) continue;
+        __syncthreads();  // what was in LDS has been read
+        if (tid == 0) {
+          int n = 0, at = head & (kMore - 1);
+          for (; at >= 0 && n < LIST; at = q.next[at]) list[n++] = at;
+          length = at >= 0 ? -1 : n;
         }
+        __syncthreads();
+        const int n = length;
+        for (int l = tid; l < n; l += threads) {
+          int rank = 0;
+          for (int i = 0; i < n; ++i) rank += list[i] < list[l];
+          sorted[rank] = list[l];
+        }
+        __syncthreads();
+        for (int i = 0; i < n; ++i) add(sorted[i]);
+        if (n >= 0) continue;
+        for (int from = begin_of(q), end = end_of(q); from < end; from += threads) {
+          const uint64_t here = __ballot(from + tid < end && q.perm[min(from + tid, q.P - 1)] == a);
+          if ((tid & 63) == 0) found[tid >> 6] = here;
+          __syncthreads();
+          for (int w = 0; w < threads / 64; ++w)
+            for (uint64_t m = found[w]; m; m &= m - 1) add(from + 64 * w + __ffsll((unsigned long long)m) - 1);
+          __syncthreads();
+        }
+      }
     }
-    store_values<NV>(dx, o_type, t * ldo + c, K - c, wide_rows(o_type, ldo), v);
+    if (in) store_values<NV>(dx, o_type, t * ldo + c, K - c, wide_rows(o_type, ldo), v);
   }
 }
 
@@ -359,16 +336,17 @@ __global__ __launch_bounds__(256) void k_grouped_add_up(void *dx, int64_t ldo, i
 
 hipError_t launch_grouped_dw(const GroupedDw &p, hipStream_t s) { return p.type == DS4MOE_BF16 ? choose_dw<OpBf16>(p, s) : choose_dw<OpF16>(p, s); }
 
-hipError_t launch_grouped_places(const GroupedPlaces &p, const int32_t *offsets, int32_t E, const int32_t *perm, int32_t P, hipStream_t s) {
-  if (P) hipLaunchKernelGGL(k_grouped_places, dim3((P + 255) / 256), dim3(256), 0, s, p.first, p.next, p.first + p.A, offsets, E, perm, P, p.A);
-  else hipLaunchKernelGGL(k_grouped_no_places, dim3((p.A + 255) / 256), dim3(256), 0, s, p.first, p.A);
+hipError_t launch_grouped_places(const GroupedPlaces &q, hipStream_t s) {
+  if (q.P) hipLaunchKernelGGL(k_grouped_places, dim3((q.P + 255) / 256), dim3(256), 0, s, q);
+  else hipLaunchKernelGGL(k_grouped_no_places, dim3((q.A + 255) / 256), dim3(256), 0, s, q.place, q.A);
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_add_up(void *dx, int64_t ldo, int32_t o_type, const float *rows, const GroupedPlaces &p, int32_t T, int32_t k,
+hipError_t launch_grouped_add_up(void *dx, int64_t ldo, int32_t o_type, const float *rows, const GroupedPlaces &q, int32_t T, int32_t k,
                                  int64_t K, hipStream_t s) {
-  hipLaunchKernelGGL(k_grouped_add_up<8>, dim3((unsigned)(T < (1 << 20) ? T : 1 << 20), (unsigned)((K + 2047) / 2048)), dim3(256), 0, s, dx, ldo,
-                     o_type, rows, p.first, p.next, T, k, K);
+  const unsigned threads = K < 2048 ? (unsigned)((K + 511) / 512 * 64) : 256;
+  hipLaunchKernelGGL(k_grouped_add_up<8>, dim3((unsigned)(T < (1 << 20) ? T : 1 << 20), (unsigned)((K + 2047) / 2048)), dim3(threads), 0, s, dx, ldo,
+                     o_type, rows, q, T, k, K);
   return hipGetLastError();
 }
 

@@ -47,6 +47,9 @@ def routed(T, E, P, k, style, rng):
         perm = rng.permutation(T * k)[:P]
         perm[rng.integers(0, P, 3)] = perm[rng.integers(0, P, 3)]
         perm[rng.integers(0, P, 2)] = [-1, T * k]
+    elif style == "any":
+        offsets = np.sort(np.concatenate([[0, P], rng.integers(0, P + 1, E - 1)]))
+        perm = rng.integers(0, T * k, P)
     else:  # "padded": positions of no expert at both ends, all of which name assignment 0
         a, b = P // 7, P - P // 5
         offsets = np.sort(np.concatenate([[a, b], rng.integers(a, b + 1, E - 1)]))
@@ -58,12 +61,13 @@ def routed(T, E, P, k, style, rng):
 @pytest.mark.parametrize("T,E,P,k,style", [
     (5, 3, 9, 1, "tokens"), (300, 8, 600, 1, "tokens"), (4000, 8, 8000, 1, "tokens"), (1000, 60, 3711, 1, "tokens"), (64, 4, 1023, 1, "tokens"),
     (64, 4, 1024, 1, "tokens"), (64, 4, 1025, 2, "tokens"), (3, 4, 2049, 1, "one"), (7, 2, 5000, 3, "one"), (1, 6, 6, 1, "one"), (700, 5, 1300, 2, "some"),
-    (3000, 5, 9000, 3, "some"), (20, 2, 30, 2, "padded"), (900, 6, 1800, 2, "padded"), (5000, 6, 9001, 2, "padded")])
+    (3000, 5, 9000, 3, "some"), (3, 4, 255, 1, "one"), (3, 4, 256, 1, "one"), (3, 4, 257, 1, "one"), (5, 3, 1280, 1, "tokens"), (2, 3, 1500, 3, "any"),
+    (40, 8, 300, 8, "any"), (20, 2, 30, 2, "padded"), (900, 6, 1800, 2, "padded"), (5000, 6, 9001, 2, "padded")])
 def test_rows_gradient_of_assignments_that_stand_several_times(T, E, P, k, style):
     """Every position of an expert adds to its token's gradient, in an order that is the same every time; those of no expert
     add nothing and take nothing away."""
     q = _q()
-    N, K = 24, 40
+    N, K = 24, 2056 if P < 700 else 1000 if P < 1300 else 40
     x, xv, w, wv, _, _ = case(T, E, 1, N, K, "f16")
     rng = np.random.default_rng(P + T)
     offsets, perm = routed(T, E, P, k, style, rng)
