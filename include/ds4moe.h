@@ -603,7 +603,8 @@ int ds4moe_int8_matmul(void *y, int32_t y_dtype, int64_t ldy, const void *a, con
  *   rows       P, positions: 0..2^23
  *   tokens     T, rows of x: 0..2^23
  *   N, K       1..65536; K values make a multiple of 16 bytes; N is a multiple
- *              of 8 in the gradients; no more than 2^37 values in P by N, P by
+ *              of 8 in the gradients, which load rows of N values in pieces of
+ *              16 bytes (pad W and dy with zeros for others); no more than 2^37 values in P by N, P by
  *              K or E by N by K
  * w: [E, N, K] without gaps.  x and dy: rows a multiple of 16 bytes and at
  * most 2^22 values apart.

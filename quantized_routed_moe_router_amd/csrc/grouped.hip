@@ -10,18 +10,21 @@
 // 4 g + v of a wave's i-th group of 16 is column 8 g + 4 i + v of it, so that a
 // lane's results are 8 adjacent columns of one row of y.
 //
-// What bounds it.  Many rows an expert: the matrix units at the clock that the
-// card's power leaves them, and a last round of tiles that is not full.  16384
-// rows of 8 experts, 2048 x 4096 bf16, take 267 us (1.03 PFLOP/s); one dense
-// 8192^3 runs at 1.39 PFLOP/s (the library's at 1.54) with the units busy for
-// 66 % of 1.6 to 1.9 GHz, and a loop of nothing but matrix instructions for 86 %
-// of 1.9.  Few rows: reading the weights, 256 experts' 4.3 GB for 64 rows each
-// in 797 us (5.5 TB/s), the 1.6 GB of the 8-bit experts that have rows of a
-// skewed choice in 325.  The dense 8-bit product of 2048 rows, 4096 x 4096,
-// takes 39.5 us (1.74 POP/s; the library's, without scales, 40.1).  Left out,
-// of 8192^3 in 784 us: matrix instructions of 32 x 32 862, stages of 64 bytes
-// 850, buffers handed on in parts 787, row tiles in groups of 2, 8 or 16 by all
-// columns 817, 791, 855.
+// What bounds it.  Many rows an expert: no one unit.  16384 rows of 8 experts,
+// 2048 x 4096 bf16, take 264 us (1.04 PFLOP/s).  The matrix units are busy for
+// 49 % of the cycles, at 1.85 GHz; a SIMD holds 1.8 of its two waves on average,
+// the last round of tiles not being full, and the waves stand at waits and
+// barriers for 38 % of their time.  One dense 8192^3 runs at 1.39 PFLOP/s (the
+// library's at 1.54) with the units busy for 66 %, and a loop of nothing but
+// matrix instructions for 86 %.  Few rows: reading the weights, 256 experts'
+// 4.3 GB for 64 rows each in 800 us (5.5 TB/s), the 1.6 GB of the 8-bit experts
+// that have rows of a skewed choice in 324.  The dense 8-bit product of 2048
+// rows, 4096 x 4096, one round of 512 tiles of 32 stages, takes 36.7 to 39.5 us
+// (1.74 to 1.87 POP/s, units busy for 40 % at 1.9 GHz; the library's, without
+// scales, 40.1).  Left out, of 8192^3 in 784 us: matrix instructions of 32 x 32
+// 862, stages of 64 bytes 850, buffers handed on in parts 787, row tiles in
+// groups of 2, 8 or 16 by all columns 817, 791, 855.  Not built: workgroups that
+// load their next tile under the results of this one.
 #include "grouped_dev.h"
 
 namespace ds4 {

@@ -6,10 +6,11 @@
 // A workgroup of 2 WN waves has 32 MT rows and 64 WN columns of one dW_e, 32
 // terms of the sum at a time.  Both operands lie across.
 //
-// With many rows an expert it is the matrix units that bound it (a workgroup's
-// first loads and its results are not under another's products): 8 experts of
-// 1024 rows, 2048 x 4096, 155 us (0.89 PFLOP/s; the library's product of these
-// sizes reaches 1.5).  With few rows it is writing dW: 256 experts of 64 rows,
+// With many rows an expert no one unit bounds it: 8 experts of 1024 rows, 2048
+// x 4096, 151 us (0.91 PFLOP/s; the library's product of these sizes reaches
+// 1.5), the matrix units busy for 39 % of the cycles at 2.1 GHz, the waves at
+// waits and barriers for 35 % of their time; a workgroup's first loads and its
+// results are not under another's products.  With few rows it is writing dW: 256 experts of 64 rows,
 // 1170 us for 4.4 GB (3.7 TB/s).  Left out, of 8192 rows: tiles of 128 x 256
 // 151 us and 1315 with 64 rows an expert; 256 x 256 in two buffers 148 and
 // 1237; one workgroup a CU that goes round 157 and 1298.

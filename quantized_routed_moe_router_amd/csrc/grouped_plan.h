@@ -24,25 +24,51 @@ inline int64_t grouped_workgroups(GroupedForm f, bool ragged, int64_t E, int64_t
   return (grouped_max_tiles(ragged, E, P, f.lowest()) * grouped_col_tiles(f, N) + 7) / 8 * 8;
 }
 
-// few rows: a kernel whose workgroups have 16 rows of the result's columns
+// All rules go by sizes alone: how many rows each expert has is known on the
+// device only.  Times are calls in us on one MI355X, of bf16 matrices of 2048 x
+// 4096 where nothing else is said, with experts drawn evenly; "skewed" is by a
+// power of -1.1 of their rank.
+
+// Few rows: a kernel whose workgroups have 16 rows of weights and 16 of x
+// against tiles of up to 64 rows.  256 experts: 64 rows in all 160 and 164, 256
+// 512 and 533, 512 677 and 709, 1024 823 and 822, 2048 978 and 776.  8 experts:
+// 4 rows 9 and 26, 16 20 and 26, 32 27 and 29, 128 42 and 30.  Of one matrix (8
+// bits, where it takes up to 64 rows at once): 16 rows 7.7 and 15, 64 13 and
+// 16; of 8192 x 4096 32 rows 14.7 and 15.2, 64 23 and 16.
+// Up to 2 E it loses where few experts have the rows, whose weights it reads
+// once per 16: 256 rows of 256 experts skewed 330 and 264, all of one expert
+// 152 and 28; and of 8 bits: 256 rows of 256 experts 329 and 236, 16 of 8 17.6
+// and 16.4 (8 of 8 13 and 16).
 inline bool grouped_is_few(bool ragged, int64_t E, int64_t P) { return ragged ? P <= 2 * E : P <= 64; }
 
-// Rules, with times in us on one MI355X of bf16 matrices of 2048 x 4096.
-// Few rows an expert: tiles as high as those, so that its weights are read
-// once.  64 rows each: of 256 experts eight waves 782 at a height of 128 and
-// 920 at 64 (four waves 822), of 8 experts four waves 28 at 64, 43 at 128, 30
-// with the choice (eight 39); 128 rows each of 8 experts 45 at 64, 48 at 128.
-// Many rows: 2048 each of 8 experts 248 by eight waves with the choice and 256
-// by four, 1024 each 154 and 152, 256 each 60 and 56.
+// More rows: eight waves or four, by the number of results.  Up to 128 rows an
+// expert (64) the tiles are as high as that, so that its weights are read once;
+// beyond, the kernel chooses.  The bound stands between measured sizes, where
+// the sides cross.  Eight and four, both with the choice, by millions of
+// results: 8 experts 16.8 112 and 125, 18.9 148 and 144, 23.1 176 and 172, 25.2
+// 189 and 179, 27.3 208 and 225, 33.5 228 and 269; skewed (-0.6) 141 and 138,
+// 145 and 145, 178 and 168, 191 and 214, 213 and 221, 281 and 276.  4 experts of
+// 8192 x 4096: 21.0 184 and 180, 25.2 195 and 195, 29.4 210 and 267.  8 bits, 8
+// experts: 23.1 106 and 105, 25.2 109 and 108, 27.3 124 and 131.
+// Eight of 128 rows and four of 64: 128 experts 25.2 397 and 536 (skewed 510 and
+// 592); 256 of 1024 x 1024 25.2 139 and 146 (149 and 159); 8 bits 233 and 274, 101
+// and 111.  Below, 64 rows each: 8 experts 38 and 28, 16 55 and 44, 256 of 1024 x
+// 1024 124 and 119 - but 64 experts 188 and 242, and 128 experts 377 and 499 (8
+// bits 133 and 124, 212 and 229): there the tiles of all weights, E N / 256, would
+// tell the sides apart better than the results do.
+constexpr int64_t kEightWaves = 24000000;
 inline GroupedForm grouped_form(bool ragged, int64_t E, int64_t P, int64_t N) {
   const int64_t mean = ragged ? P / E : P;  // rows of an expert
-  if (P * N >= (1 << 25)) return mean <= 128 ? GroupedForm{8, 128} : GroupedForm{8, 0};
+  if (P * N >= kEightWaves) return mean <= 128 ? GroupedForm{8, 128} : GroupedForm{8, 0};
   return mean <= 64 ? GroupedForm{4, 64} : GroupedForm{4, 0};
 }
 // Turned weights, fp32 results: of 256 experts 64 rows each eight waves 857 and
-// four 943, 16 rows each 774 and 830, of 60 experts (488 x 1000) 62 rows each
-// 21.7 and 19.7; of 8 experts 1024 rows each eight waves with the choice 149 to
-// 165 and four 149, 2048 rows each 290 and 271.
+// four 943, 16 rows each 774 and 830; with matrices of 1024 x 1024 145 and 143,
+// 16 rows each 110 and 110; 512 experts of 264 x 264, 64 rows each, 61 and 54.
+// Below: 60 experts (488 x 1000) 62 rows each 21.7 and 19.7, 128 of 512 x 1024
+// 64 rows each 47 and 42, 8 experts 128 rows each 42 and 37.  Many rows, eight
+// waves of 128 rows and four with the choice: 8 experts 512 rows each 94 and 93
+// (skewed 122 and 100), 1024 188 and 188 (210 and 188).
 // Beyond 2^35 results (64 GiB of 16 bits) it is eight waves again, whose tiles
 // are four times as large: four waves' could be 2^24, with more threads than a
 // launch has, and the sizes that the kernel compares would leave 32 bits.
@@ -53,10 +79,20 @@ inline GroupedForm grouped_turned_form(int64_t E, int64_t P, int64_t N) {
 }
 
 // The gradient of the weights: tiles of 256 x 256 (one workgroup on a CU) or
-// 128 x 128 (three).  32768 of the large ones, 64 terms each, 1170 us and 1288;
-// 1024, 1024 terms each, 155 and 158; 480, 62 terms each, 44 and 38; 128, 4096
-// terms each, 115 and 73.
-inline bool grouped_dw_large(int64_t E, int64_t N, int64_t K) { return E * ((N + 255) / 256) * ((K + 255) / 256) >= 1024; }
+// 128 x 128 (three), by the number of the large ones; the bound stands between
+// measured numbers.  32768, 64 terms each, 1170 and 1288; 4096 of 256 experts of
+// 1024 x 1024, 64 terms, 152 and 185 (skewed 235 and 270); 2048 of 16 experts, 64
+// terms, 66 and 71 (93 and 108), 512 terms 161 and 193 (329 and 310); 1536 of 96
+// of 1024 x 1024, 256 terms, 93 and 112 (183 and 166).  1024, 1024 terms each,
+// within a whole backward pass: of 8 experts 345 and 358, of 64 of 1024 x 1024
+// 450 and 483.  960 of 60 experts, 62 terms each, 36 and 30; 480 44 and 38; 128,
+// 4096 terms, 115 and 73.
+// Few terms make the small ones the better at higher numbers too: 1536 of 12
+// experts, 64 terms, 50 and 46 (72 and 66); 1024 of 256 of 512 x 512 38 and 32
+// (101 and 60); and large tiles that are mostly empty at any: 2048 of 512 experts
+// of 264 x 264 59 and 30.
+constexpr int64_t kLargeTiles = 1000;
+inline bool grouped_dw_large(int64_t E, int64_t N, int64_t K) { return E * ((N + 255) / 256) * ((K + 255) / 256) >= kLargeTiles; }
 inline int64_t grouped_dw_workgroups(bool large, int64_t E, int64_t N, int64_t K) {
   const int64_t side = large ? 256 : 128;
   return (E * ((N + side - 1) / side) * ((K + side - 1) / side) + 7) / 8 * 8;

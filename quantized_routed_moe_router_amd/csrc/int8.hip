@@ -120,9 +120,10 @@ __device__ __forceinline__ u2 codes_of(const Eight<TYPE> &v, const RowScale &s) 
 
 // L lanes to a row, 8 values a lane at a time; up to 8 steps stay in registers
 // between the maximum and the codes, more are read again.  Up to 4096 columns a
-// row is one wave's, which needs no barrier.  Bound by the memory: of the bytes
-// that go in and out, 8192 x 4096 bf16 take 29.4 us (3.4 TB/s; a copy reaches
-// 4.9), 65536 x 4096 232 us (3.5).
+// row is one wave's, which needs no barrier.  8192 x 4096 bf16 take 29.4 us (3.4
+// TB/s of the bytes that go in and out; a copy reaches 4.9), 65536 x 4096 232 us
+// (3.5).  Waves stand at waits for 79 % of their time, with 3 of them a SIMD on
+// average; loading the next row under the codes of this one was not tried.
 template <int TYPE, int L>
 __global__ __launch_bounds__(256) void k_int8_quantize(int8_t *codes, float *scales, const void *src, int64_t rows, int64_t cols,
                                                        int64_t ld, bool vec) {
@@ -213,8 +214,11 @@ hipError_t quantize(int8_t *codes, float *scales, const void *src, int64_t rows,
 // own takes longer.  The weights' first lines are asked for before that.  Then
 // as the product of a few rows: the waves share the columns.  Bound by the
 // launch and the latency of what follows another (a row, its maximum, the
-// weights): one token, 2048 x 4096, 9.1 to 9.6 us a call (12.4 in two launches),
-// 1.7 of them for the weights' 8.4 MB.
+// weights): one token, 2048 x 4096, 9.0 to 9.8 us a call, 1.7 of them for the
+// weights' 8.4 MB.  In us, one launch and two: 2048 x 4096 1 row 9.0 and 11.9, 4
+// 9.1 and 13.8, 8 11.8 and 14.2, 12 16.3 and 14.3; 8192 x 4096 1 row 10 and 17,
+// 8 19 and 21, 12 26 and 22; 1001 x 2064 16 rows 10.7 and 11.6.  (16 rows of
+// 4096 do not fit; beyond 8 rows of long matrices two launches are ahead.)
 constexpr int QW = 8;                    // waves
 constexpr int QUANT_LDS = 64 << 10;      // bytes of codes
 
