@@ -189,3 +189,24 @@ def test_tokens_without_positions_of_the_c_abi(T, k):
     B.ds4moe_grouped_dx(d, dx, K, None, N, w, some, some, ws, n)
     torch.cuda.synchronize()
     assert not dx.any()
+
+
+def test_rows_gradient_of_more_tokens_than_workgroups():
+    """2^20 workgroups add the tokens up and go round: tokens of both rounds that stand several times, some very often."""
+    q = _q()
+    T, E, N, K = (1 << 20) + 300, 2, 8, 16
+    rng = np.random.default_rng(0)
+    near = rng.integers(0, 300, 3000)
+    perm = np.concatenate([near, near[:1500] + (1 << 20), rng.integers(0, T, 20000), np.full(300, 7), np.full(400, (1 << 20) + 7)]).astype(np.int32)
+    rng.shuffle(perm)
+    P = perm.size
+    offsets = np.array([0, P // 3, P], dtype=np.int32)
+    x = torch.zeros(T, K, dtype=torch.float16, device="cuda")
+    w, wv = half(rng.integers(-2, 3, (E, N, K)).astype(np.float64), "f16")
+    dy, dyv = half(rng.integers(-2, 3, (P, N)).astype(np.float64), "f16")
+    dx, _ = q.grouped_matmul_backward(dy, x, w, dev(offsets), dev(perm), need_dw=False)
+    want = np.zeros((T, K))
+    for e in range(E):
+        p = slice(offsets[e], offsets[e + 1])
+        np.add.at(want, perm[p], dyv[p] @ wv[e])  # whole numbers: exact in fp32
+    assert torch.equal(dx.cpu(), torch.from_numpy(want).half())
